@@ -363,6 +363,150 @@ int mamba_conv1d_fwd(const void* x, const float* weight, const float* bias, cons
                      void* conv_state_out, void* u, int64_t batch, int64_t dim, int64_t seqlen, int64_t kernel_size,
                      int io_dtype, int silu, void* stream);
 
+/* ---- The state-space-duality layer in serving: packed prompts, single tokens, request slots ----
+ *
+ * Requests keep their past in two pools indexed by slot: the last inputs of the convolution
+ * and the SSM state.  Both are the caller's memory; a call updates the slots it names in place.
+ *
+ *   slots      (n) int64, DEVICE: row or sequence i of the call works on pool entry slots[i].  A
+ *              slot outside [0, nslots) names none: a packed sequence then starts from zeros and
+ *              keeps nothing, a single-token row is padding (nothing read or written, y included).
+ *              No two rows of one call may name the same slot (their results and the slot's
+ *              contents would be unspecified).
+ *   positions  (n) int64, DEVICE: tokens the request has behind it.  0 (or less) starts it afresh:
+ *              whatever its slot holds counts as zeros, so slots need no clearing.
+ *   cu_seqlens (nseq + 1) int64, DEVICE: sequence s is tokens [cu[s], cu[s+1]) of the call's arrays,
+ *              0 <= cu[0] <= ... <= cu[nseq] <= total_len.  A sequence without tokens leaves its
+ *              slot as it is; token rows outside every sequence are not written.
+ * Offsets and slots are not checked on the host: offsets are clamped to [0, total_len], so a bad
+ * array gives wrong results but no out-of-bounds access.
+ *
+ * The *_stride arguments are the elements between two tokens of an array whose tokens are
+ * otherwise contiguous (at least the token's elements), so that the pieces of one projection's
+ * output need not be copied apart.
+ */
+
+/*
+ * The layer's causal depthwise convolution + SiLU over packed sequences, token-major (the layout of
+ * mamba_ssd_fwd; a token's width = nheads * headdim + 2 * ngroups * dstate channels are x | B | C):
+ *
+ *   u[t, c] = SiLU(bias[c] + sum_{k<K} weight[c, k] v[p - (K-1) + k, c]),  p the token's position
+ *
+ * (without SiLU when silu is zero), v[q] the sequence's input at position q and 0 for q < 0.
+ *
+ *   x            (total_len, width)   io    x_stride elements between tokens
+ *   weight       (width, K)           f32   taps, oldest input first
+ *   bias         (width)              f32   NULL means 0
+ *   conv_state   (nslots, K, width)   io    IN/OUT ring of inputs: position q in row q mod K.  Rows of a
+ *                                           sequence's last min(length, K - 1) positions are written, the
+ *                                           others kept.  NULL (with slots and positions NULL): every
+ *                                           sequence starts from zeros and nothing is kept
+ *   u            (total_len, width)   io    OUT
+ * Sizes: nseq >= 1, total_len >= 0, width >= 1, K = kernel_size 2 to 4 (others
+ * MAMBA_SCAN_ERR_UNSUPPORTED).  Arithmetic in fp32.
+ */
+int mamba_ssd_conv_fwd_varlen(const void* x, const float* weight, const float* bias, const int64_t* cu_seqlens,
+                              void* conv_state, const int64_t* slots, const int64_t* positions, void* u, int64_t nseq,
+                              int64_t total_len, int64_t width, int64_t kernel_size, int64_t x_stride, int64_t nslots,
+                              int io_dtype, int silu, void* stream);
+
+/*
+ * mamba_ssd_fwd over packed sequences with a state per slot and groups of B and C (heads
+ * g * nheads / ngroups .. share group g):
+ *
+ *   x, z, y    (total_len, nheads, headdim)  bf16   z NULL means no gate; y without a stride of its own
+ *   dt         (total_len, nheads)           bf16
+ *   B, C       (total_len, ngroups, dstate)  bf16
+ *   A_log, D, dt_bias (nheads)               f32    D, dt_bias may be NULL
+ *   state      (nslots, nheads, headdim, dstate) f32   IN/OUT; NULL with slots and positions NULL
+ *   workspace  at least mamba_ssd_fwd_varlen_workspace_size(...) bytes, 256-byte aligned; contents on
+ *              entry ignored, on exit undefined (may be NULL where that size is 0)
+ * Supported: io_dtype MAMBA_SCAN_BF16, headdim a multiple of 32 up to 256, dstate 64 or 128, ngroups a
+ * divisor of nheads, strides up to 2^24 (others MAMBA_SCAN_ERR_UNSUPPORTED); x, B, C, z, y and state
+ * 16-byte aligned, the strides of x, B, C and z multiples of 8.  Products of bf16 operands with fp32
+ * accumulation; the state's own update carries fp32's accuracy (the scaled x in three bf16 parts).
+ */
+int mamba_ssd_fwd_varlen(const void* x, const void* dt, const float* A_log, const void* B, const void* C,
+                         const float* D, const void* z, const float* dt_bias, const int64_t* cu_seqlens, float* state,
+                         const int64_t* slots, const int64_t* positions, void* y, int64_t nseq, int64_t total_len,
+                         int64_t nheads, int64_t headdim, int64_t dstate, int64_t ngroups, int64_t nslots,
+                         int64_t x_stride, int64_t dt_stride, int64_t B_stride, int64_t C_stride, int64_t z_stride,
+                         int io_dtype, int flags, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace mamba_ssd_fwd_varlen needs (may be 0); (size_t)-1 for rejected sizes. */
+size_t mamba_ssd_fwd_varlen_workspace_size(int64_t nseq, int64_t total_len, int64_t nheads, int64_t headdim,
+                                           int64_t dstate);
+
+/*
+ * One token per request through the layer's core: the convolution of mamba_ssd_conv_fwd_varlen (with
+ * SiLU) and the recurrence of mamba_ssd_fwd_varlen in one launch, u kept in fp32 in between.
+ *
+ *   xbc         (batch, width)            io   x | B | C before the convolution
+ *   dt          (batch, nheads)           io
+ *   conv_weight (width, K), conv_bias (width)   f32   conv_bias may be NULL
+ *   conv_state  (nslots, K, width)        io   IN/OUT: row positions[i] mod K of slot i is written
+ *   state       (nslots, nheads, headdim, dstate) f32   IN/OUT, 16-byte aligned
+ *   slots       (batch), NULL: row i has slot i
+ *   positions   (batch)
+ *   z, y        (batch, nheads, headdim)  io   z NULL means no gate; y without a stride of its own
+ * Sizes: batch >= 1, headdim a multiple of 32 up to 256, dstate 64 or 128, ngroups a divisor of
+ * nheads, K 2 to 4; batch * nheads * headdim / 8 * 256 < 2^32 (the launch's work-items).
+ */
+int mamba_ssd_step(const void* xbc, const void* dt, const float* A_log, const float* conv_weight,
+                   const float* conv_bias, void* conv_state, float* state, const int64_t* slots,
+                   const int64_t* positions, const float* D, const void* z, const float* dt_bias, void* y,
+                   int64_t batch, int64_t nheads, int64_t headdim, int64_t dstate, int64_t ngroups,
+                   int64_t kernel_size, int64_t nslots, int64_t xbc_stride, int64_t dt_stride, int64_t z_stride,
+                   int io_dtype, int flags, void* stream);
+
+/* Output formats of mamba_rms_norm_fwd */
+#define MAMBA_NORM_OUT_IO 0   /* y in the io dtype */
+#define MAMBA_NORM_OUT_ROW8 1 /* y in e4m3 (OCP: largest value 448), one fp32 scale per row */
+#define MAMBA_NORM_OUT_MX8 2  /* y in e4m3, one e8m0 scale (2^(byte - 127)) per 32 columns of a row */
+
+/*
+ * Root-mean-square norm with the residual's addition, in front of a layer's projections:
+ *
+ *   r = x + residual,   rstd = 1 / sqrt(mean(r^2) + eps),   y = r rstd weight
+ *
+ *   x            (rows, dim)  io
+ *   residual     (rows, dim)  residual_dtype: the io dtype or MAMBA_SCAN_F32; NULL means none (r = x)
+ *   weight       (dim)        f32
+ *   residual_out (rows, dim)  residual_dtype  OUT: r, required iff residual is given; may equal residual.
+ *                                             The norm is taken of r in fp32, before this rounding
+ *   y            (rows, dim)  io or e4m3      OUT
+ *   scales       (rows) f32, or (rows, ceil(dim / 32)) bytes   OUT for the 8-bit formats: y's value is e4m3 *
+ *                             scale.  Row scale: largest magnitude / 448; block scale: the smallest power of two
+ *                             that keeps the block's magnitudes within 448; 1 where all values are 0
+ *   rstd         (rows)       f32             OUT, NULL: not written
+ * Sizes: rows >= 0, dim >= 1; the launch's work-items (at most rows * 256) below 2^32.  A row with a NaN or an
+ * Inf has NaNs in y.
+ */
+int mamba_rms_norm_fwd(const void* x, const void* residual, const float* weight, float eps, void* residual_out,
+                       void* y, void* scales, float* rstd, int64_t rows, int64_t dim, int io_dtype,
+                       int residual_dtype, int out_format, void* stream);
+
+/*
+ * Gradient of mamba_rms_norm_fwd, given r (residual_out, or x where there was no residual) and rstd:
+ *
+ *   xh = r rstd, g = dy weight:  dr = rstd (g - xh mean(g xh)) + d_residual,  dweight = sum over rows of dy xh
+ *
+ *   dy          (rows, dim) io
+ *   r           (rows, dim) residual_dtype
+ *   d_residual  (rows, dim) residual_dtype   gradient that reaches r from the residual stream, NULL means 0
+ *   dx          (rows, dim) io        OUT: dr, the gradient of x (and of residual, where that has the io dtype)
+ *   dresidual   (rows, dim) f32       OUT: dr unrounded, for an fp32 residual of a bf16 layer; NULL: not written;
+ *                                     must be NULL where residual_dtype is the io dtype
+ *   dweight     (dim)       f32       OUT, summed in a fixed order
+ *   workspace   at least mamba_rms_norm_bwd_workspace_size(rows, dim) bytes, 256-byte aligned
+ */
+int mamba_rms_norm_bwd(const void* dy, const void* r, const float* weight, const float* rstd, const void* d_residual,
+                       void* dx, float* dresidual, float* dweight, int64_t rows, int64_t dim, int io_dtype,
+                       int residual_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace mamba_rms_norm_bwd needs (0 only for rows == 0); (size_t)-1 for rejected sizes. */
+size_t mamba_rms_norm_bwd_workspace_size(int64_t rows, int64_t dim);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char* mamba_scan_status_str(int status);
 

@@ -39,8 +39,10 @@ EXPORTED = (
     "mamba_scan_fwd_conv",
     "mamba_scan_fwd_varlen", "mamba_scan_fwd_varlen_workspace_size", "mamba_scan_step", "mamba_scan_bwd",
     "mamba_scan_bwd_workspace_size", "mamba_conv1d_fwd", "mamba_ssd_fwd", "mamba_scan_status_str",
-    "mamba_scan_abi_version",
+    "mamba_scan_abi_version", "mamba_ssd_conv_fwd_varlen", "mamba_ssd_fwd_varlen",
+    "mamba_ssd_fwd_varlen_workspace_size", "mamba_ssd_step",
 )
+EXPORTED_NORM = ("mamba_rms_norm_fwd", "mamba_rms_norm_bwd", "mamba_rms_norm_bwd_workspace_size")
 
 _lib = None
 
@@ -86,6 +88,20 @@ def load_library():
     lib.mamba_ssd_fwd.argtypes = [P] * 11 + [I64] * 5 + [I, I, P]
     lib.mamba_conv1d_fwd.restype = I
     lib.mamba_conv1d_fwd.argtypes = [P] * 6 + [I64] * 4 + [I, I, P]
+    lib.mamba_ssd_conv_fwd_varlen.restype = I
+    lib.mamba_ssd_conv_fwd_varlen.argtypes = [P] * 8 + [I64] * 6 + [I, I, P]
+    lib.mamba_ssd_fwd_varlen.restype = I
+    lib.mamba_ssd_fwd_varlen.argtypes = [P] * 13 + [I64] * 12 + [I, I, P, SZ, P]
+    lib.mamba_ssd_fwd_varlen_workspace_size.restype = SZ
+    lib.mamba_ssd_fwd_varlen_workspace_size.argtypes = [I64] * 5
+    lib.mamba_ssd_step.restype = I
+    lib.mamba_ssd_step.argtypes = [P] * 13 + [I64] * 10 + [I, I, P]
+    lib.mamba_rms_norm_fwd.restype = I
+    lib.mamba_rms_norm_fwd.argtypes = [P] * 3 + [ctypes.c_float] + [P] * 4 + [I64] * 2 + [I, I, I, P]
+    lib.mamba_rms_norm_bwd.restype = I
+    lib.mamba_rms_norm_bwd.argtypes = [P] * 8 + [I64] * 2 + [I, I, P, SZ, P]
+    lib.mamba_rms_norm_bwd_workspace_size.restype = SZ
+    lib.mamba_rms_norm_bwd_workspace_size.argtypes = [I64] * 2
     lib.mamba_scan_status_str.restype = ctypes.c_char_p
     lib.mamba_scan_status_str.argtypes = [I]
     lib.mamba_scan_abi_version.restype = I
@@ -583,3 +599,327 @@ def ssd_fwd(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, B: torch.Ten
                            _flags(dt_softplus, discretization), _stream(dev, stream))
     _check("mamba_ssd_fwd", rc)
     return (y, fs) if return_final_state else y
+
+
+def _on_device(fn):
+    """Runs fn with the first argument's device current (the library launches on the current device)."""
+
+    @functools.wraps(fn)
+    def run(*args, **kwargs):
+        t0 = args[0] if args else next(iter(kwargs.values()), None)
+        if not isinstance(t0, torch.Tensor) or t0.device.type != "cuda" or t0.get_device() == torch.cuda.current_device():
+            return fn(*args, **kwargs)
+        with torch.cuda.device(t0.device):
+            return fn(*args, **kwargs)
+
+    return run
+
+
+def _token_stride(name: str, t: torch.Tensor, shape, dtype, device) -> int:
+    """Checks a tensor of tokens whose rows are contiguous but may lie apart; returns the elements between them."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device or t.dtype != dtype or t.shape != shape:
+        _req(name, t, shape, dtype, device)
+    st = t.stride()
+    if st[-1] == 1 and (len(st) == 2 or st[1] == shape[2]) and shape[0] > 1:
+        return st[0]
+    if shape[0] and not t[0].is_contiguous():
+        raise ValueError(f"{name}: the elements of a token must be contiguous")
+    width = shape[1] if len(shape) == 2 else shape[1] * shape[2]
+    return st[0] if shape[0] > 1 else -(-width // 8) * 8
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _pool_index(n: int, slots, positions, device):
+    _req("slots", slots, (n,), torch.int64, device)
+    _req("positions", positions, (n,), torch.int64, device)
+
+
+@_on_device
+@_on_stream
+def ssd_conv_fwd_varlen(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: torch.Tensor,
+                        bias: Optional[torch.Tensor] = None, conv_state: Optional[torch.Tensor] = None,
+                        slots: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                        silu: bool = True, *, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The SSD layer's causal depthwise conv (+ SiLU) over packed sequences, token-major.  x (total, width)
+    in the io dtype (its rows may lie apart, as a slice of a projection's output), weight (width, K) float32
+    with K 2 to 4, bias (width,) float32, cu_seqlens (nseq + 1,) int64 on the device.  conv_state
+    (nslots, K, width) in the io dtype is updated IN PLACE: sequence s reads and writes ring slots[s]
+    (outside [0, nslots): starts from zeros, keeps nothing), positions[s] tokens (0: a new request) behind
+    it, both (nseq,) int64.  No slot may be named twice.  Returns u (total, width); rows outside every
+    sequence are not written."""
+    lib = load_library()
+    if x.dim() != 2:
+        raise ValueError("x must be (total, width)")
+    total, width = x.shape
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("ssd_conv_fwd_varlen needs device tensors (HIP)")
+    io, iot = _io_dtype(x), x.dtype
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be (nseq + 1,)")
+    nseq = cu_seqlens.numel() - 1
+    K = weight.shape[-1] if weight.dim() == 2 else -1
+    xs = _token_stride("x", x, (total, width), iot, dev)
+    _req("weight", weight, (width, K), torch.float32, dev)
+    _req("bias", bias, (width,), torch.float32, dev)
+    _req("cu_seqlens", cu_seqlens, (nseq + 1,), torch.int64, dev)
+    nslots = 0
+    if conv_state is not None:
+        nslots = conv_state.shape[0] if conv_state.dim() == 3 else -1
+        _req("conv_state", conv_state, (nslots, K, width), iot, dev)
+        if slots is None or positions is None:
+            raise ValueError("conv_state needs slots and positions")
+    _pool_index(nseq, slots, positions, dev)
+    u = out if out is not None else torch.empty((total, width), dtype=iot, device=dev)
+    _req("out", u, (total, width), iot, dev)
+    rc = lib.mamba_ssd_conv_fwd_varlen(_addr(x), _addr(weight), _addr(bias), _addr(cu_seqlens), _addr(conv_state),
+                                       _addr(slots), _addr(positions), _addr(u), nseq, total, width, K, xs, nslots, io,
+                                       int(bool(silu)), _stream(dev, stream))
+    _check("mamba_ssd_conv_fwd_varlen", rc)
+    return u
+
+
+def ssd_fwd_varlen_workspace_size(nseq: int, total_len: int, nheads: int, headdim: int, dstate: int) -> int:
+    n = load_library().mamba_ssd_fwd_varlen_workspace_size(nseq, total_len, nheads, headdim, dstate)
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("mamba_ssd_fwd_varlen_workspace_size: sizes rejected")
+    return int(n)
+
+
+@_on_device
+@_on_stream
+def ssd_fwd_varlen(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                   cu_seqlens: torch.Tensor, D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                   dt_bias: Optional[torch.Tensor] = None, state: Optional[torch.Tensor] = None,
+                   slots: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                   dt_softplus: bool = True, *, out: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, discretization: str = "zoh", stream=None) -> torch.Tensor:
+    """ssd_fwd over packed sequences.  x, z (total, H, P), dt (total, H), B, C (total, G, N) in bfloat16, heads in
+    G groups that share B and C; tokens may lie apart (slices of a wider row), each contiguous; x, B, C and
+    z 16-byte aligned.  cu_seqlens (nseq + 1,) int64 on the device.  state (nslots, H, P, N) float32 is
+    updated IN PLACE by slot, as conv_state in ssd_conv_fwd_varlen.  Returns y (total, H, P); rows outside every
+    sequence are not written."""
+    lib = load_library()
+    if x.dim() != 3:
+        raise ValueError("x must be (total, H, P)")
+    total, H, P = x.shape
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("ssd_fwd_varlen needs device tensors (HIP)")
+    io, iot = _io_dtype(x), x.dtype
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be (nseq + 1,)")
+    nseq = cu_seqlens.numel() - 1
+    if B.dim() != 3:
+        raise ValueError("B must be (total, G, N)")
+    G, N = B.shape[1:]
+    f32 = torch.float32
+    xs = _token_stride("x", x, (total, H, P), iot, dev)
+    ds = _token_stride("dt", dt, (total, H), iot, dev)
+    bs = _token_stride("B", B, (total, G, N), iot, dev)
+    cs = _token_stride("C", C, (total, G, N), iot, dev)
+    zs = 0 if z is None else _token_stride("z", z, (total, H, P), iot, dev)
+    _req("A_log", A_log, (H,), f32, dev)
+    _req("D", D, (H,), f32, dev)
+    _req("dt_bias", dt_bias, (H,), f32, dev)
+    _req("cu_seqlens", cu_seqlens, (nseq + 1,), torch.int64, dev)
+    nslots = 0
+    if state is not None:
+        nslots = state.shape[0] if state.dim() == 4 else -1
+        _req("state", state, (nslots, H, P, N), f32, dev)
+        if slots is None or positions is None:
+            raise ValueError("state needs slots and positions")
+    _pool_index(nseq, slots, positions, dev)
+    y = out if out is not None else torch.empty((total, H, P), dtype=iot, device=dev)
+    _req("out", y, (total, H, P), iot, dev)
+    need = ssd_fwd_varlen_workspace_size(nseq, total, H, P, N)
+    ws = workspace
+    if ws is None and need > 0:
+        ws = torch.empty(need + 256, dtype=torch.uint8, device=dev)
+    ws_ptr, ws_bytes = None, 0
+    if ws is not None:
+        base = ws.data_ptr()
+        off = (-base) % 256
+        ws_ptr, ws_bytes = base + off, max(0, ws.numel() * ws.element_size() - off)
+    rc = lib.mamba_ssd_fwd_varlen(_addr(x), _addr(dt), _addr(A_log), _addr(B), _addr(C), _addr(D), _addr(z),
+                                  _addr(dt_bias), _addr(cu_seqlens), _addr(state), _addr(slots), _addr(positions),
+                                  _addr(y), nseq, total, H, P, N, G, nslots, xs, ds, bs, cs, zs, io,
+                                  _flags(dt_softplus, discretization), ws_ptr, ws_bytes, _stream(dev, stream))
+    _check("mamba_ssd_fwd_varlen", rc)
+    return y
+
+
+@_on_device
+@_on_stream
+def ssd_step(xbc: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, conv_weight: torch.Tensor,
+             conv_state: torch.Tensor, state: torch.Tensor, positions: torch.Tensor,
+             slots: Optional[torch.Tensor] = None, D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+             dt_bias: Optional[torch.Tensor] = None, conv_bias: Optional[torch.Tensor] = None,
+             dt_softplus: bool = True, *, out: Optional[torch.Tensor] = None, discretization: str = "zoh",
+             stream=None) -> torch.Tensor:
+    """One token per request: the conv + SiLU of its x | B | C channels (xbc (batch, H P + 2 G N)), the SSM
+    update and readout, the D skip and the gate, in one launch.  dt (batch, H) and z (batch, H, P) as xbc in
+    the io dtype (float32 or bfloat16; rows may lie apart).  conv_state (nslots, K, width) in the io dtype and
+    state (nslots, H, P, N) float32 are updated IN PLACE at slots[i] (default: i); a row whose slot is
+    outside [0, nslots) is padding and its y is not written.  positions (batch,): tokens each request has
+    behind it (0: a new one).  No slot may be named twice.  Returns y (batch, H, P)."""
+    lib = load_library()
+    if xbc.dim() != 2 or state.dim() != 4:
+        raise ValueError("xbc must be (batch, width) and state (nslots, H, P, N)")
+    batch, width = xbc.shape
+    nslots, H, P, N = state.shape
+    dev = xbc.device
+    if dev.type != "cuda":
+        raise ValueError("ssd_step needs device tensors (HIP)")
+    io, iot = _io_dtype(xbc), xbc.dtype
+    K = conv_weight.shape[-1] if conv_weight.dim() == 2 else -1
+    G, rest = divmod(width - H * P, 2 * N)
+    if rest or G < 1:
+        raise ValueError(f"xbc has {width} channels, expected {H * P} + 2 G {N}")
+    f32 = torch.float32
+    xs = _token_stride("xbc", xbc, (batch, width), iot, dev)
+    ds = _token_stride("dt", dt, (batch, H), iot, dev)
+    zs = 0 if z is None else _token_stride("z", z, (batch, H, P), iot, dev)
+    _req("A_log", A_log, (H,), f32, dev)
+    _req("conv_weight", conv_weight, (width, K), f32, dev)
+    _req("conv_bias", conv_bias, (width,), f32, dev)
+    _req("conv_state", conv_state, (nslots, K, width), iot, dev)
+    _req("state", state, (nslots, H, P, N), f32, dev)
+    _req("D", D, (H,), f32, dev)
+    _req("dt_bias", dt_bias, (H,), f32, dev)
+    if slots is None and batch > nslots:
+        raise ValueError(f"{batch} rows without slots, but {nslots} pool entries")
+    if positions is None:
+        raise ValueError("ssd_step needs positions")
+    _pool_index(batch, slots, positions, dev)
+    y = out if out is not None else torch.empty((batch, H, P), dtype=iot, device=dev)
+    _req("out", y, (batch, H, P), iot, dev)
+    rc = lib.mamba_ssd_step(_addr(xbc), _addr(dt), _addr(A_log), _addr(conv_weight), _addr(conv_bias), _addr(conv_state),
+                            _addr(state), _addr(slots), _addr(positions), _addr(D), _addr(z), _addr(dt_bias), _addr(y),
+                            batch, H, P, N, G, K, nslots, xs, ds, zs, io, _flags(dt_softplus, discretization),
+                            _stream(dev, stream))
+    _check("mamba_ssd_step", rc)
+    return y
+
+
+_NORM_OUT = {None: 0, "row": 1, "mx": 2}   # MAMBA_NORM_OUT_*
+
+
+@_on_device
+@_on_stream
+def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, *, eps: float = 1e-5,
+                 quant: Optional[str] = None, return_rstd: bool = False, out: Optional[torch.Tensor] = None,
+                 scales: Optional[torch.Tensor] = None, residual_out: Optional[torch.Tensor] = None, stream=None):
+    """Root-mean-square norm of r = x + residual over the last axis: y = r rstd weight.  x (..., dim) in the io
+    dtype, weight (dim,) float32, residual (..., dim) in the io dtype or float32.  quant None: y in the io
+    dtype; "row": y in float8_e4m3fn with one float32 scale per row (shape x.shape[:-1]); "mx": y in
+    float8_e4m3fn with one float8_e8m0fnu scale per 32 columns.  Returns y, followed by the scales (quant), r in
+    the residual's dtype (residual given; residual_out may be residual itself) and rstd float32 (return_rstd)."""
+    lib = load_library()
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be (..., dim)")
+    shape, dim, dev = x.shape, x.shape[-1], x.device
+    rows = x.numel() // dim
+    if dev.type != "cuda":
+        raise ValueError("rms_norm_fwd needs device tensors (HIP)")
+    if quant not in _NORM_OUT:
+        raise ValueError(f"quant must be None, 'row' or 'mx', got {quant!r}")
+    io, iot = _io_dtype(x), x.dtype
+    _req("x", x, shape, iot, dev)
+    _req("weight", weight, (dim,), torch.float32, dev)
+    rio = io
+    ro = residual_out
+    if residual is not None:
+        rio = _io_dtype(residual)
+        if rio != io and rio != F32:
+            raise ValueError("residual must have x's dtype or float32")
+        _req("residual", residual, shape, residual.dtype, dev)
+        if ro is None:
+            ro = torch.empty(shape, dtype=residual.dtype, device=dev)
+        _req("residual_out", ro, shape, residual.dtype, dev)
+    elif ro is not None:
+        raise ValueError("residual_out needs residual")
+    if quant is None:
+        if scales is not None:
+            raise ValueError("scales needs quant")
+        yt = iot
+    else:
+        yt = torch.float8_e4m3fn
+        st = torch.float32 if quant == "row" else torch.float8_e8m0fnu
+        ss = shape[:-1] if quant == "row" else shape[:-1] + ((dim + 31) // 32,)
+        if scales is None:
+            scales = torch.empty(ss, dtype=st, device=dev)
+        _req("scales", scales, ss, st, dev)
+    y = out if out is not None else torch.empty(shape, dtype=yt, device=dev)
+    _req("out", y, shape, yt, dev)
+    rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev) if return_rstd else None
+    rc = lib.mamba_rms_norm_fwd(_addr(x), _addr(residual), _addr(weight), eps, _addr(ro), _addr(y), _addr(scales),
+                                _addr(rstd), rows, dim, io, rio, _NORM_OUT[quant], _stream(dev, stream))
+    _check("mamba_rms_norm_fwd", rc)
+    res = [y]
+    if quant is not None:
+        res.append(scales)
+    if residual is not None:
+        res.append(ro)
+    if return_rstd:
+        res.append(rstd)
+    return res[0] if len(res) == 1 else tuple(res)
+
+
+def rms_norm_bwd_workspace_size(rows: int, dim: int) -> int:
+    n = load_library().mamba_rms_norm_bwd_workspace_size(rows, dim)
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("mamba_rms_norm_bwd_workspace_size: sizes rejected")
+    return int(n)
+
+
+@_on_device
+@_on_stream
+def rms_norm_bwd(dy: torch.Tensor, r: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                 d_residual: Optional[torch.Tensor] = None, *, workspace: Optional[torch.Tensor] = None,
+                 stream=None) -> dict:
+    """Gradient of rms_norm_fwd.  dy (..., dim) in the io dtype; r, what was normed (residual_out, or x where there
+    was no residual), in the io dtype or float32; rstd float32 from the forward; d_residual, the gradient that
+    reaches r from the residual stream, in r's dtype.  Returns a dict: dx in the io dtype, dweight float32, and
+    with d_residual also dresidual in r's dtype (dx itself where that is the io dtype)."""
+    lib = load_library()
+    if dy.dim() < 1 or dy.shape[-1] < 1:
+        raise ValueError("dy must be (..., dim)")
+    shape, dim, dev = dy.shape, dy.shape[-1], dy.device
+    rows = dy.numel() // dim
+    if dev.type != "cuda":
+        raise ValueError("rms_norm_bwd needs device tensors (HIP)")
+    io, iot = _io_dtype(dy), dy.dtype
+    rio = _io_dtype(r)
+    if rio != io and rio != F32:
+        raise ValueError("r must have dy's dtype or float32")
+    _req("dy", dy, shape, iot, dev)
+    _req("r", r, shape, r.dtype, dev)
+    _req("weight", weight, (dim,), torch.float32, dev)
+    _req("rstd", rstd, shape[:-1], torch.float32, dev)
+    _req("d_residual", d_residual, shape, r.dtype, dev)
+    dx = torch.empty(shape, dtype=iot, device=dev)
+    apart = d_residual is not None and rio != io
+    dres = torch.empty(shape, dtype=torch.float32, device=dev) if apart else None
+    dw = torch.empty((dim,), dtype=torch.float32, device=dev)
+    need = rms_norm_bwd_workspace_size(rows, dim)
+    ws = workspace
+    if ws is None and need > 0:
+        ws = torch.empty(need + 256, dtype=torch.uint8, device=dev)
+    ws_ptr, ws_bytes = None, 0
+    if ws is not None:
+        base = ws.data_ptr()
+        off = (-base) % 256
+        ws_ptr, ws_bytes = base + off, max(0, ws.numel() * ws.element_size() - off)
+    rc = lib.mamba_rms_norm_bwd(_addr(dy), _addr(r), _addr(weight), _addr(rstd), _addr(d_residual), _addr(dx),
+                                _addr(dres), _addr(dw), rows, dim, io, rio, ws_ptr, ws_bytes, _stream(dev, stream))
+    _check("mamba_rms_norm_bwd", rc)
+    g = {"dx": dx, "dweight": dw}
+    if d_residual is not None:
+        g["dresidual"] = dres if apart else dx
+    return g

@@ -13,7 +13,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libmamba_scan.so")
-SOURCES = ["api.hip", "scan_fwd.hip", "scan_fwd_varlen.hip", "scan_step.hip", "scan_bwd.hip", "conv1d.hip", "ssd_fwd.hip"]
+SOURCES = ["api.hip", "scan_fwd.hip", "scan_fwd_varlen.hip", "scan_step.hip", "scan_bwd.hip", "conv1d.hip", "ssd_fwd.hip",
+           "ssd_conv.hip", "ssd_varlen.hip", "ssd_step.hip", "rms_norm.hip"]
 ARCH = "gfx950"
 
 

@@ -443,4 +443,238 @@ int mamba_conv1d_fwd(const void* x, const float* weight, const float* bias, cons
   return e == hipSuccess ? MAMBA_SCAN_OK : MAMBA_SCAN_ERR_HIP;
 }
 
+// ---- the SSD layer in serving, and the norm ----
+
+namespace {
+
+int check_ssd_heads(int64_t nheads, int64_t headdim, int64_t dstate, int64_t ngroups) {
+  if (nheads < 1 || headdim < 1 || dstate < 1 || ngroups < 1) return MAMBA_SCAN_ERR_SHAPE;
+  if (headdim % 32 != 0 || headdim > 256 || (dstate != 64 && dstate != 128)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  if (nheads > (1 << 24) / headdim || nheads % ngroups != 0) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  return MAMBA_SCAN_OK;
+}
+
+// `rows` tokens of `width` elements, `stride` apart
+int check_rows(int64_t rows, int64_t width, int64_t stride) {
+  int64_t t;
+  if (stride < width || !mul_ok(rows, stride, &t) || !mul_ok(t, 4, &t)) return MAMBA_SCAN_ERR_SHAPE;
+  return MAMBA_SCAN_OK;
+}
+
+// a pool goes with its slots and positions
+bool pool_args_ok(const void* pool, const int64_t* slots, const int64_t* positions) {
+  return (pool != nullptr) == (slots != nullptr) && (pool != nullptr) == (positions != nullptr);
+}
+
+}  // namespace
+
+int mamba_ssd_conv_fwd_varlen(const void* x, const float* weight, const float* bias, const int64_t* cu_seqlens,
+                              void* conv_state, const int64_t* slots, const int64_t* positions, void* u, int64_t nseq,
+                              int64_t total_len, int64_t width, int64_t kernel_size, int64_t x_stride, int64_t nslots,
+                              int io_dtype, int silu, void* stream) {
+  if (io_dtype != MAMBA_SCAN_F32 && io_dtype != MAMBA_SCAN_BF16) return MAMBA_SCAN_ERR_DTYPE;
+  if (nseq < 1 || total_len < 0 || width < 1 || nslots < 0) return MAMBA_SCAN_ERR_SHAPE;
+  if (kernel_size < 2 || kernel_size > 4) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  int st = check_rows(total_len, width, x_stride);
+  if (st != MAMBA_SCAN_OK) return st;
+  int64_t t;
+  if (!mul_ok(nslots, width, &t) || !mul_ok(t, 16, &t) || !mul_ok(nseq, 32, &t)) return MAMBA_SCAN_ERR_SHAPE;
+  // grid: runs of tokens x groups of (at least) 64 channels
+  if (!launch_ok((mscan::ssd_conv_runs(nseq, total_len) + 3) / 4, 256) || (width + 63) / 64 > 65535)
+    return MAMBA_SCAN_ERR_UNSUPPORTED;
+  if (!weight || !cu_seqlens || !pool_args_ok(conv_state, slots, positions)) return MAMBA_SCAN_ERR_NULL;
+  if (total_len > 0 && (!x || !u)) return MAMBA_SCAN_ERR_NULL;
+  const size_t esz = io_dtype == MAMBA_SCAN_BF16 ? 2 : 4;
+  const void* io_ptrs[] = {x, u, conv_state};
+  for (const void* p : io_ptrs)
+    if (p && !aligned(p, esz)) return MAMBA_SCAN_ERR_ALIGN;
+  const void* f_ptrs[] = {weight, bias};
+  for (const void* p : f_ptrs)
+    if (p && !aligned(p, 4)) return MAMBA_SCAN_ERR_ALIGN;
+  const void* i_ptrs[] = {cu_seqlens, slots, positions};
+  for (const void* p : i_ptrs)
+    if (p && !aligned(p, 8)) return MAMBA_SCAN_ERR_ALIGN;
+  if (total_len == 0) return MAMBA_SCAN_OK;
+  mscan::SsdConvArgs a{};
+  a.x = x; a.weight = weight; a.bias = bias; a.cu = cu_seqlens; a.conv_state = conv_state; a.slots = slots;
+  a.positions = positions; a.u = u; a.nseq = nseq; a.total = total_len; a.width = width; a.x_stride = x_stride;
+  a.nslots = nslots; a.K = (int)kernel_size; a.io_bf16 = io_dtype == MAMBA_SCAN_BF16; a.silu = silu != 0;
+  hipError_t e = mscan::launch_ssd_conv(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MAMBA_SCAN_OK : MAMBA_SCAN_ERR_HIP;
+}
+
+static int check_ssd_varlen_sizes(int64_t nseq, int64_t total_len, int64_t nheads, int64_t headdim, int64_t dstate,
+                                  int64_t ngroups, mscan::SsdVarlenPlan* plan) {
+  if (nseq < 1 || total_len < 0) return MAMBA_SCAN_ERR_SHAPE;
+  int st = check_ssd_heads(nheads, headdim, dstate, ngroups);
+  if (st != MAMBA_SCAN_OK) return st;
+  int64_t t;
+  if (nseq > INT32_MAX || !mul_ok(total_len, nheads * headdim, &t) || !mul_ok(t, 4, &t)) return MAMBA_SCAN_ERR_SHAPE;
+  *plan = mscan::make_ssd_varlen_plan(nseq, total_len, nheads, headdim, dstate);
+  // grid: (piece, head, slice of 64 or 32 channels), 256 work-items each
+  if (!mul_ok(plan->pieces, nheads * (headdim / 32), &t) || !launch_ok(t, 256)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  return MAMBA_SCAN_OK;
+}
+
+size_t mamba_ssd_fwd_varlen_workspace_size(int64_t nseq, int64_t total_len, int64_t nheads, int64_t headdim,
+                                           int64_t dstate) {
+  mscan::SsdVarlenPlan plan;
+  if (check_ssd_varlen_sizes(nseq, total_len, nheads, headdim, dstate, 1, &plan) != MAMBA_SCAN_OK) return (size_t)-1;
+  return plan.ws_total;
+}
+
+int mamba_ssd_fwd_varlen(const void* x, const void* dt, const float* A_log, const void* B, const void* C,
+                         const float* D, const void* z, const float* dt_bias, const int64_t* cu_seqlens, float* state,
+                         const int64_t* slots, const int64_t* positions, void* y, int64_t nseq, int64_t total_len,
+                         int64_t nheads, int64_t headdim, int64_t dstate, int64_t ngroups, int64_t nslots,
+                         int64_t x_stride, int64_t dt_stride, int64_t B_stride, int64_t C_stride, int64_t z_stride,
+                         int io_dtype, int flags, void* workspace, size_t workspace_bytes, void* stream) {
+  if (io_dtype != MAMBA_SCAN_F32 && io_dtype != MAMBA_SCAN_BF16) return MAMBA_SCAN_ERR_DTYPE;
+  if (io_dtype != MAMBA_SCAN_BF16) return MAMBA_SCAN_ERR_UNSUPPORTED;   // bf16 operands only
+  mscan::SsdVarlenPlan plan;
+  int st = check_ssd_varlen_sizes(nseq, total_len, nheads, headdim, dstate, ngroups, &plan);
+  if (st != MAMBA_SCAN_OK) return st;
+  if (flags & ~(MAMBA_SCAN_FLAG_SOFTPLUS | MAMBA_SCAN_FLAG_EULER)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  int64_t t;
+  if (nslots < 0 || !mul_ok(nslots, nheads * headdim, &t) || !mul_ok(t, dstate * 4, &t)) return MAMBA_SCAN_ERR_SHAPE;
+  const int64_t inner = nheads * headdim;
+  const int64_t widths[] = {inner, nheads, ngroups * dstate, ngroups * dstate, z ? inner : 0};
+  const int64_t strides[] = {x_stride, dt_stride, B_stride, C_stride, z ? z_stride : 0};
+  for (int i = 0; i < 5; ++i) {
+    st = check_rows(total_len, widths[i], strides[i]);
+    if (st != MAMBA_SCAN_OK) return st;
+    if (strides[i] > (1 << 24)) return MAMBA_SCAN_ERR_UNSUPPORTED;   // a chunk's rows take 32-bit offsets
+    if (i != 1 && strides[i] % 8 != 0) return MAMBA_SCAN_ERR_ALIGN;  // 16-byte accesses
+  }
+  if (!A_log || !cu_seqlens || !pool_args_ok(state, slots, positions)) return MAMBA_SCAN_ERR_NULL;
+  if (total_len > 0 && (!x || !dt || !B || !C || !y)) return MAMBA_SCAN_ERR_NULL;
+  const void* v16[] = {x, B, C, z, y, state};
+  for (const void* p : v16)
+    if (p && !aligned(p, 16)) return MAMBA_SCAN_ERR_ALIGN;
+  if (dt && !aligned(dt, 2)) return MAMBA_SCAN_ERR_ALIGN;
+  const void* f_ptrs[] = {A_log, D, dt_bias};
+  for (const void* p : f_ptrs)
+    if (p && !aligned(p, 4)) return MAMBA_SCAN_ERR_ALIGN;
+  const void* i_ptrs[] = {cu_seqlens, slots, positions};
+  for (const void* p : i_ptrs)
+    if (p && !aligned(p, 8)) return MAMBA_SCAN_ERR_ALIGN;
+  if (plan.ws_total > 0) {
+    if (!workspace || workspace_bytes < plan.ws_total || !aligned(workspace, 256)) return MAMBA_SCAN_ERR_WORKSPACE;
+  }
+  if (total_len == 0) return MAMBA_SCAN_OK;
+  mscan::SsdVarlenArgs a{};
+  a.x = x; a.dt = dt; a.A_log = A_log; a.B = B; a.C = C; a.D = D; a.z = z; a.dt_bias = dt_bias; a.cu = cu_seqlens;
+  a.state = state; a.slots = slots; a.positions = positions; a.y = y; a.nseq = nseq; a.total = total_len;
+  a.nslots = nslots; a.nheads = nheads; a.headdim = headdim; a.dstate = dstate; a.ngroups = ngroups;
+  a.x_stride = x_stride; a.dt_stride = dt_stride; a.b_stride = B_stride; a.c_stride = C_stride; a.z_stride = z_stride;
+  a.softplus = (flags & MAMBA_SCAN_FLAG_SOFTPLUS) != 0;
+  a.euler = (flags & MAMBA_SCAN_FLAG_EULER) != 0;
+  a.workspace = workspace;
+  hipError_t e = mscan::launch_ssd_varlen(a, plan, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MAMBA_SCAN_OK : MAMBA_SCAN_ERR_HIP;
+}
+
+int mamba_ssd_step(const void* xbc, const void* dt, const float* A_log, const float* conv_weight,
+                   const float* conv_bias, void* conv_state, float* state, const int64_t* slots,
+                   const int64_t* positions, const float* D, const void* z, const float* dt_bias, void* y,
+                   int64_t batch, int64_t nheads, int64_t headdim, int64_t dstate, int64_t ngroups,
+                   int64_t kernel_size, int64_t nslots, int64_t xbc_stride, int64_t dt_stride, int64_t z_stride,
+                   int io_dtype, int flags, void* stream) {
+  if (io_dtype != MAMBA_SCAN_F32 && io_dtype != MAMBA_SCAN_BF16) return MAMBA_SCAN_ERR_DTYPE;
+  if (batch < 1 || nslots < 0) return MAMBA_SCAN_ERR_SHAPE;
+  int st = check_ssd_heads(nheads, headdim, dstate, ngroups);
+  if (st != MAMBA_SCAN_OK) return st;
+  if (kernel_size < 2 || kernel_size > 4) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  if (flags & ~(MAMBA_SCAN_FLAG_SOFTPLUS | MAMBA_SCAN_FLAG_EULER)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  const int64_t inner = nheads * headdim, width = inner + 2 * ngroups * dstate;
+  int64_t t;
+  // grid: slices of at least 8 channels, 256 work-items each
+  if (!mul_ok(batch, inner / 8, &t) || !launch_ok(t, 256)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  if (!mul_ok(nslots, inner, &t) || !mul_ok(t, dstate * 4, &t) || !mul_ok(nslots, width * 16, &t)) return MAMBA_SCAN_ERR_SHAPE;
+  st = check_rows(batch, width, xbc_stride);
+  if (st == MAMBA_SCAN_OK) st = check_rows(batch, nheads, dt_stride);
+  if (st == MAMBA_SCAN_OK && z) st = check_rows(batch, inner, z_stride);
+  if (st != MAMBA_SCAN_OK) return st;
+  if (!xbc || !dt || !A_log || !conv_weight || !conv_state || !state || !positions || !y) return MAMBA_SCAN_ERR_NULL;
+  const size_t esz = io_dtype == MAMBA_SCAN_BF16 ? 2 : 4;
+  const void* io_ptrs[] = {xbc, dt, z, y, conv_state};
+  for (const void* p : io_ptrs)
+    if (p && !aligned(p, esz)) return MAMBA_SCAN_ERR_ALIGN;
+  const void* f_ptrs[] = {A_log, conv_weight, conv_bias, D, dt_bias};
+  for (const void* p : f_ptrs)
+    if (p && !aligned(p, 4)) return MAMBA_SCAN_ERR_ALIGN;
+  if (!aligned(state, 16) || !aligned(positions, 8) || (slots && !aligned(slots, 8))) return MAMBA_SCAN_ERR_ALIGN;
+  mscan::SsdStepArgs a{};
+  a.xbc = xbc; a.dt = dt; a.A_log = A_log; a.conv_weight = conv_weight; a.conv_bias = conv_bias;
+  a.conv_state = conv_state; a.state = state; a.slots = slots; a.positions = positions; a.D = D; a.z = z;
+  a.dt_bias = dt_bias; a.y = y; a.batch = batch; a.nslots = nslots; a.xbc_stride = xbc_stride;
+  a.dt_stride = dt_stride; a.z_stride = z_stride; a.nheads = (int)nheads; a.headdim = (int)headdim;
+  a.dstate = (int)dstate; a.ngroups = (int)ngroups; a.K = (int)kernel_size;
+  a.io_bf16 = io_dtype == MAMBA_SCAN_BF16;
+  a.softplus = (flags & MAMBA_SCAN_FLAG_SOFTPLUS) != 0;
+  a.euler = (flags & MAMBA_SCAN_FLAG_EULER) != 0;
+  hipError_t e = mscan::launch_ssd_step(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MAMBA_SCAN_OK : MAMBA_SCAN_ERR_HIP;
+}
+
+// sizes and element types shared by the norm and its gradient
+static int check_norm(int64_t rows, int64_t dim, int io_dtype, int residual_dtype) {
+  if (io_dtype != MAMBA_SCAN_F32 && io_dtype != MAMBA_SCAN_BF16) return MAMBA_SCAN_ERR_DTYPE;
+  if (residual_dtype != io_dtype && residual_dtype != MAMBA_SCAN_F32) return MAMBA_SCAN_ERR_DTYPE;
+  if (rows < 0 || dim < 1) return MAMBA_SCAN_ERR_SHAPE;
+  int64_t t;
+  if (!mul_ok(rows + 512, dim + 1, &t) || !mul_ok(t, 4, &t)) return MAMBA_SCAN_ERR_SHAPE;
+  // grids: at most a workgroup per row, a column per work-item
+  if (!launch_ok(rows, 256) || !launch_ok((dim + 63) / 64, 256)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  return MAMBA_SCAN_OK;
+}
+
+int mamba_rms_norm_fwd(const void* x, const void* residual, const float* weight, float eps, void* residual_out,
+                       void* y, void* scales, float* rstd, int64_t rows, int64_t dim, int io_dtype,
+                       int residual_dtype, int out_format, void* stream) {
+  int st = check_norm(rows, dim, io_dtype, residual_dtype);
+  if (st != MAMBA_SCAN_OK) return st;
+  if (out_format < MAMBA_NORM_OUT_IO || out_format > MAMBA_NORM_OUT_MX8) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  if (!weight || (rows > 0 && (!x || !y || (out_format != MAMBA_NORM_OUT_IO && !scales)))) return MAMBA_SCAN_ERR_NULL;
+  if (rows > 0 && (residual == nullptr) != (residual_out == nullptr)) return MAMBA_SCAN_ERR_NULL;
+  const size_t esz = io_dtype == MAMBA_SCAN_BF16 ? 2 : 4, rsz = residual_dtype == MAMBA_SCAN_BF16 ? 2 : 4;
+  if (!aligned(x, esz) || (out_format == MAMBA_NORM_OUT_IO && !aligned(y, esz)) || !aligned(residual, rsz) ||
+      !aligned(residual_out, rsz) || !aligned(weight, 4) || !aligned(rstd, 4) ||
+      (out_format == MAMBA_NORM_OUT_ROW8 && !aligned(scales, 4)))
+    return MAMBA_SCAN_ERR_ALIGN;
+  if (rows == 0) return MAMBA_SCAN_OK;
+  mscan::NormArgs a{};
+  a.x = x; a.residual = residual; a.weight = weight; a.residual_out = residual_out; a.y = y; a.scales = scales;
+  a.rstd = rstd; a.rows = rows; a.dim = dim; a.eps = eps; a.io_bf16 = io_dtype == MAMBA_SCAN_BF16;
+  a.res_f32 = residual_dtype == MAMBA_SCAN_F32; a.out = out_format;
+  hipError_t e = mscan::launch_norm_fwd(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MAMBA_SCAN_OK : MAMBA_SCAN_ERR_HIP;
+}
+
+size_t mamba_rms_norm_bwd_workspace_size(int64_t rows, int64_t dim) {
+  if (check_norm(rows, dim, MAMBA_SCAN_F32, MAMBA_SCAN_F32) != MAMBA_SCAN_OK) return (size_t)-1;
+  return (size_t)(mscan::norm_bwd_parts(rows) * dim) * 4;
+}
+
+int mamba_rms_norm_bwd(const void* dy, const void* r, const float* weight, const float* rstd, const void* d_residual,
+                       void* dx, float* dresidual, float* dweight, int64_t rows, int64_t dim, int io_dtype,
+                       int residual_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_norm(rows, dim, io_dtype, residual_dtype);
+  if (st != MAMBA_SCAN_OK) return st;
+  if (dresidual && residual_dtype == io_dtype) return MAMBA_SCAN_ERR_UNSUPPORTED;   // dx is that gradient
+  if (!weight || !dweight || (rows > 0 && (!dy || !r || !rstd || !dx))) return MAMBA_SCAN_ERR_NULL;
+  const size_t esz = io_dtype == MAMBA_SCAN_BF16 ? 2 : 4, rsz = residual_dtype == MAMBA_SCAN_BF16 ? 2 : 4;
+  if (!aligned(dy, esz) || !aligned(dx, esz) || !aligned(r, rsz) || !aligned(d_residual, rsz) ||
+      !aligned(dresidual, 4) || !aligned(weight, 4) || !aligned(rstd, 4) || !aligned(dweight, 4))
+    return MAMBA_SCAN_ERR_ALIGN;
+  const size_t need = mamba_rms_norm_bwd_workspace_size(rows, dim);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return MAMBA_SCAN_ERR_WORKSPACE;
+  mscan::NormArgs a{};
+  a.x = dy; a.residual = r; a.weight = weight; a.rstd = const_cast<float*>(rstd); a.dres = d_residual; a.y = dx;
+  a.residual_out = dresidual; a.dweight = dweight; a.rows = rows; a.dim = dim;
+  a.io_bf16 = io_dtype == MAMBA_SCAN_BF16; a.res_f32 = residual_dtype == MAMBA_SCAN_F32; a.workspace = workspace;
+  hipError_t e = mscan::launch_norm_bwd(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MAMBA_SCAN_OK : MAMBA_SCAN_ERR_HIP;
+}
+
 }  // extern "C"

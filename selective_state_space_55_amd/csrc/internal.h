@@ -182,4 +182,97 @@ struct SsdArgs {
 
 hipError_t launch_ssd(const SsdArgs& a, hipStream_t stream);
 
+// Root-mean-square norm with the residual's addition, and its gradient (rms_norm.hip).
+enum { kNormIo = 0, kNormRow8 = 1, kNormMx8 = 2 };
+struct NormArgs {
+  const void* x;          // (rows, dim) io; backward: dy
+  const void* residual;   // (rows, dim) io or fp32, or NULL; backward: r
+  const float* weight;    // (dim)
+  const void* dres;       // backward: gradient of the residual stream (r's type) or NULL
+  void* residual_out;     // forward: r; backward: fp32 gradient of r where r's type is not io, else NULL
+  void* y;                // forward: (rows, dim) io or e4m3; backward: dx, io
+  void* scales;           // (rows) fp32 or (rows, ceil(dim / 32)) e8m0
+  float* rstd;            // (rows): forward OUT or NULL; backward input
+  float* dweight;
+  int64_t rows, dim;
+  float eps;
+  int io_bf16, res_f32, out;
+  void* workspace;
+};
+
+int64_t norm_bwd_parts(int64_t rows);   // workgroups whose partial dweight (dim fp32) the workspace holds
+hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t stream);
+hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t stream);
+
+// Causal conv + SiLU of packed token-major sequences, with a ring of inputs per slot (ssd_conv.hip).
+struct SsdConvArgs {
+  const void* x;          // (total, width) io, x_stride elements between tokens
+  const float* weight;    // (width, K)
+  const float* bias;      // (width) or NULL
+  const int64_t* cu;      // (nseq + 1)
+  void* conv_state;       // (nslots, K, width) io or NULL
+  const int64_t* slots;   // (nseq) or NULL
+  const int64_t* positions;
+  void* u;                // (total, width) io
+  int64_t nseq, total, width, x_stride, nslots;
+  int K, io_bf16, silu;
+};
+
+int64_t ssd_conv_runs(int64_t nseq, int64_t total);   // waves per 64 lanes of channels
+hipError_t launch_ssd_conv(const SsdConvArgs& a, hipStream_t stream);
+
+// One token per row: conv + SSD state update + readout + gate (ssd_step.hip).
+struct SsdStepArgs {
+  const void* xbc;        // (batch, H P + 2 G N) io
+  const void* dt;         // (batch, H) io
+  const float* A_log;     // (H)
+  const float* conv_weight;   // (width, K)
+  const float* conv_bias;
+  void* conv_state;       // (nslots, K, width) io
+  float* state;           // (nslots, H, P, N)
+  const int64_t* slots;   // (batch) or NULL: row i has slot i
+  const int64_t* positions;   // (batch)
+  const float* D;
+  const void* z;          // (batch, H, P) io or NULL
+  const float* dt_bias;
+  void* y;                // (batch, H, P) io
+  int64_t batch, nslots, xbc_stride, dt_stride, z_stride;
+  int nheads, headdim, dstate, ngroups, K;
+  int io_bf16, softplus, euler;
+};
+
+int ssd_step_slice(const SsdStepArgs& a);   // head channels per workgroup
+hipError_t launch_ssd_step(const SsdStepArgs& a, hipStream_t stream);
+
+// Multi-head SSM over packed sequences with a state per slot (ssd_varlen.hip), bf16 io.
+struct SsdVarlenPlan {
+  int64_t piece;       // tokens per piece, a multiple of 64; 0: every sequence is one piece
+  int64_t pieces;      // piece numbers (some of them empty), at least nseq
+  size_t off_state;    // (pieces, H, P, N) fp32
+  size_t off_decay;    // (pieces, H) fp32
+  size_t ws_total;
+};
+SsdVarlenPlan make_ssd_varlen_plan(int64_t nseq, int64_t total, int64_t nheads, int64_t headdim, int64_t dstate);
+
+struct SsdVarlenArgs {
+  const void* x;          // (total, H, P)
+  const void* dt;         // (total, H)
+  const float* A_log;
+  const void* B;          // (total, G, N)
+  const void* C;
+  const float* D;
+  const void* z;          // (total, H, P) or NULL
+  const float* dt_bias;
+  const int64_t* cu;
+  float* state;           // (nslots, H, P, N) or NULL
+  const int64_t* slots;
+  const int64_t* positions;
+  void* y;                // (total, H, P), contiguous
+  int64_t nseq, total, nslots, nheads, headdim, dstate, ngroups;
+  int64_t x_stride, dt_stride, b_stride, c_stride, z_stride;   // elements between tokens
+  int softplus, euler;
+  void* workspace;
+};
+hipError_t launch_ssd_varlen(const SsdVarlenArgs& a, const SsdVarlenPlan& p, hipStream_t stream);
+
 }  // namespace mscan

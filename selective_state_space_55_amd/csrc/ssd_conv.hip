@@ -1,0 +1,147 @@
+// ssd_conv.hip -- the short causal convolution + SiLU in front of the SSD, over
+// packed prompts, token-major (a token's x | B | C channels contiguous, as the
+// in-projection leaves them).
+//
+//   u[t, c] = SiLU(bias[c] + sum_{k<K} w[c, k] v[p - (K - 1) + k]),  p = the token's position
+//
+// v[q] is the sequence's input at position q: a row of x for tokens of this
+// call, ring row q mod K of the sequence's slot for the tokens before it, 0 for
+// q < 0.  A ring of K rows (one more than the K - 1 a token looks back) lets the
+// single-token kernel write a new row that no workgroup of that launch reads, and
+// nothing is ever shifted.
+//
+// A stream (x read once, u written once), bound by HBM.  A wave takes a run of
+// up to kRun tokens of one sequence, a lane W channels of it (8: one 16-byte
+// access, or 1 where rows are not 16-byte aligned), so its K - 1 previous inputs
+// stay in registers.  Runs are counted from each sequence's start (run k of
+// sequence s has number cu[s] / kRun + s + k, of which some are empty), so only a
+// sequence's first run looks at the ring: it reads the rows behind it and then
+// writes the new ones, and no other wave has to be waited for.
+#include "internal.h"
+#include "io.h"
+#include "packed.h"
+
+#include <algorithm>
+
+namespace mscan {
+namespace {
+
+constexpr int kRun = 8;   // tokens a thread walks
+
+struct CArgs {
+  Packed seq;
+  const void* x;
+  const float* w;
+  const float* bias;
+  void* ring;      // (nslots, K, width) or null
+  void* u;
+  int64_t width, xstride;
+  int silu;
+};
+
+template <typename IoT, int W>
+__device__ __forceinline__ void to_f32(const IoT* p, float (&f)[W]) {
+  if constexpr (W == 8)
+    Io<IoT>::to_f32(Io<IoT>::load8(p), f);
+  else
+    f[0] = Io<IoT>::load1(p);
+}
+
+template <typename IoT, int W, int K>
+__global__ __launch_bounds__(256) void ssd_conv_kernel(CArgs a) {
+  const int lane = threadIdx.x & 63;
+  const Packed& q = a.seq;
+  const int64_t run = uniform64((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6));
+  const int64_t s = uniform64(last_not_above(q.nseq, run, [&](int64_t i) { return seq_offset(q, i) / kRun + i; }));
+  if (s < 0) return;   // whole waves
+  const int64_t start = seq_offset(q, s), end = seq_offset(q, s + 1);
+  const int64_t k0 = run - (start / kRun + s), t0 = start + k0 * kRun;
+  if (t0 >= end) return;
+  const int64_t c = ((int64_t)blockIdx.y * 64 + lane) * W;
+  if (c >= a.width) return;
+  const IoT* x = static_cast<const IoT*>(a.x) + c;
+  IoT* u = static_cast<IoT*>(a.u) + c;
+  IoT* ring = static_cast<IoT*>(a.ring) + c;
+
+  // v[0 .. K-2]: the inputs behind the run, v[K-1 ..]: the run's own
+  float v[K - 1 + kRun][W], w[K][W], b[W];
+#pragma unroll
+  for (int i = 0; i < kRun; ++i) to_f32<IoT, W>(x + min(t0 + i, end - 1) * a.xstride, v[K - 1 + i]);
+  const int64_t slot = k0 ? -1 : seq_slot(q, s);
+  const int64_t pos = slot < 0 ? 0 : seq_position(q, s);
+#pragma unroll
+  for (int i = 0; i < K - 1; ++i) {
+    const int64_t p = pos - (K - 1) + i;
+#pragma unroll
+    for (int j = 0; j < W; ++j) v[i][j] = 0.0f;
+    if (k0)
+      to_f32<IoT, W>(x + (t0 - (K - 1) + i) * a.xstride, v[i]);
+    else if (slot >= 0 && p >= 0)
+      to_f32<IoT, W>(ring + (slot * K + p % K) * a.width, v[i]);
+  }
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) w[k][j] = a.w[(c + j) * K + k];
+    b[j] = a.bias ? a.bias[c + j] : 0.0f;
+  }
+  if (slot >= 0) {   // the sequence's first run: the rows of its last tokens
+    const int64_t n = min(end - start, (int64_t)(K - 1));
+    for (int64_t i = 1; i <= n; ++i) {
+      IoT* to = ring + (slot * K + (pos + end - start - i) % K) * a.width;
+      const IoT* from = x + (end - i) * a.xstride;
+#pragma unroll
+      for (int j = 0; j < W; ++j) to[j] = from[j];
+    }
+  }
+  const int n = (int)min((int64_t)kRun, end - t0);
+#pragma unroll
+  for (int i = 0; i < kRun; ++i) {
+    if (i >= n) break;
+    float out[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      float acc = b[j];
+#pragma unroll
+      for (int k = 0; k < K; ++k) acc = fmaf(w[k][j], v[i + k][j], acc);
+      out[j] = a.silu ? silu(acc) : acc;
+    }
+    if constexpr (W == 8)
+      Io<IoT>::store8(u + (t0 + i) * a.width, Io<IoT>::from_f32(out));
+    else
+      Io<IoT>::store1(u + (t0 + i) * a.width, out[0]);
+  }
+}
+
+template <typename IoT, int W>
+hipError_t run(const CArgs& a, int K, hipStream_t s) {
+  const dim3 grid((unsigned)((ssd_conv_runs(a.seq.nseq, a.seq.total) + 3) / 4), (unsigned)((a.width + 64 * W - 1) / (64 * W)));
+  switch (K) {
+    case 2: hipLaunchKernelGGL((ssd_conv_kernel<IoT, W, 2>), grid, dim3(256), 0, s, a); break;
+    case 3: hipLaunchKernelGGL((ssd_conv_kernel<IoT, W, 3>), grid, dim3(256), 0, s, a); break;
+    case 4: hipLaunchKernelGGL((ssd_conv_kernel<IoT, W, 4>), grid, dim3(256), 0, s, a); break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// the run numbers end below total / kRun + nseq
+int64_t ssd_conv_runs(int64_t nseq, int64_t total) { return total / kRun + nseq; }
+
+hipError_t launch_ssd_conv(const SsdConvArgs& p, hipStream_t stream) {
+  CArgs a{};
+  a.seq.cu = p.cu; a.seq.slots = p.slots; a.seq.positions = p.positions;
+  a.seq.nseq = p.nseq; a.seq.total = p.total; a.seq.nslots = p.nslots;
+  a.x = p.x; a.w = p.weight; a.bias = p.bias; a.ring = p.conv_state; a.u = p.u;
+  a.width = p.width; a.xstride = p.x_stride; a.silu = p.silu;
+  const uintptr_t mis = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.u) |
+                        reinterpret_cast<uintptr_t>(p.conv_state);
+  const int64_t e = p.io_bf16 ? 2 : 4;
+  const bool vec = p.width % 8 == 0 && (mis & 15) == 0 && (p.x_stride * e) % 16 == 0;
+  if (p.io_bf16) return vec ? run<uint16_t, 8>(a, p.K, stream) : run<uint16_t, 1>(a, p.K, stream);
+  return vec ? run<float, 8>(a, p.K, stream) : run<float, 1>(a, p.K, stream);
+}
+
+}  // namespace mscan

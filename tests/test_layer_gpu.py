@@ -1,0 +1,546 @@
+"""GPU: the SSD layer's serving operators and the norm against their fp64 definitions (oracle/layer.py).
+
+Tolerances are counted in roundings.  A bf16 result is off by half a step, 2^-8 of its value; an e4m3 one by
+2^-4 of its value or half the smallest step, 2^-10.  fp32 arithmetic adds a few 2^-24 of the sums over
+absolute values; F32 = 2^-18 of them covers some sixty roundings in a row (a 128-term dot product in a tree
+has 8, exp and its argument 4, the convolution 8).  In the packed SSM the masked decay matrix is rounded to
+bf16 (2^-8 of each term, so of the sum over absolute values) and S^T to two bf16 parts (2^-16); its state sums
+64-token chunks of three bf16 parts in fp32, 192 terms at 2^-24 each at the very most (2^-16), and each
+chunk scales it by an exponential (2^-21)."""
+import sys
+
+import pytest
+import torch
+
+import selective_state_space_55_amd as mscan
+from oracle import layer
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+F32 = 2.0 ** -18
+
+
+def say(msg):
+    print(f"[layer] {msg}", flush=True)
+    sys.stdout.flush()
+
+
+class Rng:
+    def __init__(self, seed):
+        self.g = torch.Generator().manual_seed(seed)
+
+    def __call__(self, *shape, dtype=torch.float32, scale=1.0):
+        return (torch.randn(*shape, generator=self.g) * scale).to(dtype)
+
+    def uniform(self, lo, hi, *shape):
+        return lo + (hi - lo) * torch.rand(*shape, generator=self.g)
+
+    def slots(self, n, pool):
+        return torch.randperm(pool, generator=self.g)[:n]
+
+
+def dev(*ts):
+    got = [None if t is None else t.to(DEV) for t in ts]
+    return got[0] if len(got) == 1 else got
+
+
+def i64(v):
+    return torch.tensor(v, dtype=torch.int64)
+
+
+def close(name, got, want, tol):
+    """|got - want| <= tol element by element; NaN where `want` is NaN is not looked at."""
+    got, want = got.detach().cpu().double(), want.double()
+    seen = ~torch.isnan(want)
+    assert torch.isfinite(got[seen]).all(), name
+    over = ((got - want).abs() / (tol + 1e-300))[seen]
+    worst = float(over.max()) if over.numel() else 0.0
+    say(f"  {name}: {worst:.3f} of the tolerance")
+    assert worst <= 1.0, (name, worst)
+
+
+def apart(t, gap):
+    """The same rows with `gap` elements between them (a slice of a wider row)."""
+    rows, width = t.shape[0], t[0].numel()
+    wide = torch.full((rows, width + gap), float("nan"), dtype=t.dtype)
+    wide[:, :width] = t.reshape(rows, -1)
+    return wide.to(DEV)[:, :width].view(t.shape) if t.dim() == 2 else wide.to(DEV)[:, :width].unflatten(1, t.shape[1:])
+
+
+# ---------------------------------------------------------------- norm
+
+NORM = [  # rows, dim: every shape of a row, odd sizes, rows off 16-byte alignment, long rows
+    (1, 1), (3, 8), (5, 500), (2, 512), (7, 768), (3, 1024), (9, 2048), (4, 2560), (2, 4096), (3, 8192), (2, 16384),
+    (2, 16392), (6, 33), (5, 511), (3, 2047), (4, 5001), (2, 8191), (2, 8201), (300, 72), (1030, 64)]
+
+
+@pytest.mark.parametrize("io,res", [("bf16", "f32"), ("bf16", "bf16"), ("bf16", None), ("f32", "f32"), ("f32", None)])
+@pytest.mark.parametrize("rows,dim", NORM)
+def test_norm(rows, dim, io, res):
+    t = {"bf16": torch.bfloat16, "f32": torch.float32, None: None}
+    r = Rng(rows * 7 + dim)
+    x, w = r(rows, dim, dtype=t[io]), 1 + r(dim, scale=0.1)
+    residual = r(rows, dim, dtype=t[res], scale=3.0) if res else None
+    x[0] = 0   # a row of zeros, where there is no residual
+    if rows > 1:
+        x[1] *= 1e-3
+    y64, r64, rstd64 = layer.rms_norm(x, w, residual, 1e-5)
+    say(f"norm {rows} x {dim} {io} residual {res}")
+    xd, wd, rd = dev(x, w, residual)
+    for quant in (None, "row", "mx"):
+        got = mscan.rms_norm_fwd(xd, wd, rd, eps=1e-5, quant=quant, return_rstd=True)
+        torch.cuda.synchronize()
+        got = list(got)
+        y = got.pop(0)
+        if quant is None:
+            close("y", y, y64, HALF[t[io]] * y64.abs() + F32 * y64.abs())
+        else:
+            scale = got.pop(0).float().cpu().double()
+            want = layer.row_scale(y64) if quant == "row" else layer.block_scale(y64)
+            if quant == "row":
+                close("scale", scale, want, F32 * want)
+                each = scale[:, None]
+            else:
+                # the border between two powers of two is met in fp32
+                top = torch.stack([p.abs().amax(1) for p in y64.split(32, 1)], 1) / want
+                edge = (top - 448).abs() < 1e-4 * 448
+                assert torch.equal(scale[~edge], want[~edge])
+                each = scale.repeat_interleave(32, 1)[:, :dim]
+            q = y.cpu().float().double()
+            close("q", q * each, y64, 2.0 ** -4 * y64.abs() + 2.0 ** -10 * each + F32 * y64.abs())
+        if residual is not None:
+            close("r", got.pop(0), r64, (HALF[t[res]] + 2.0 ** -24) * r64.abs())
+        close("rstd", got.pop(0), rstd64, F32 * rstd64)
+
+
+@pytest.mark.parametrize("io,res", [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("rows,dim", NORM)
+def test_norm_gradient(rows, dim, io, res):
+    t = {"bf16": torch.bfloat16, "f32": torch.float32}
+    g = Rng(rows * 5 + dim)
+    r, w = g(rows, dim, dtype=t[res], scale=2.0), 1 + g(dim, scale=0.1)
+    dy, dres = g(rows, dim, dtype=t[io]), g(rows, dim, dtype=t[res])
+    rstd = (1 / torch.sqrt(r.double().square().mean(1) + 1e-5)).float()
+    say(f"norm gradient {rows} x {dim} {io} r {res}")
+    # sums over rows: at most 2048 terms in a row of one workgroup here, 2^-13 of the sum over absolute values
+    many = 2.0 ** -24 * (rows + 16)
+    for d in (dres, None):
+        dr64, dw64, dra, dwa = layer.rms_norm_bwd(dy, r, w, rstd, d)
+        out = mscan.rms_norm_bwd(*dev(dy, r, w, rstd, d))
+        again = mscan.rms_norm_bwd(*dev(dy, r, w, rstd, d))
+        torch.cuda.synchronize()
+        close("dx", out["dx"], dr64, HALF[t[io]] * dr64.abs() + F32 * dra)
+        close("dweight", out["dweight"], dw64, (F32 + many) * dwa)
+        assert ("dresidual" in out) == (d is not None)
+        if d is not None:
+            close("dresidual", out["dresidual"], dr64, HALF[t[res]] * dr64.abs() + F32 * dra)
+        for k in out:
+            assert torch.equal(out[k], again[k]), k
+
+
+def test_norm_non_finite_rows_stay_in_their_row():
+    x = Rng(3)(5, 264)
+    x[1, 7], x[3, 200] = float("nan"), float("inf")
+    w = torch.ones(264)
+    good = [0, 2, 4]
+    for quant in (None, "row", "mx"):
+        y = mscan.rms_norm_fwd(dev(x), dev(w), quant=quant)
+        y = y if quant is None else y[0]
+        y = y.float().cpu()
+        assert torch.isfinite(y[good]).all()
+        assert torch.isnan(y[1]).any() and torch.isnan(y[3]).any()
+
+
+def test_norm_scales_of_extreme_rows():
+    """Zero rows have scale 1; the smallest fp32 numbers and the largest bf16 ones stay finite."""
+    x = torch.zeros(4, 96)
+    x[1, 5] = 1e-38
+    x[2] = 3e18
+    x[3, :32] = 1.0
+    y, s = mscan.rms_norm_fwd(dev(x), dev(torch.ones(96)), quant="mx", eps=1e-5)
+    assert s.float().cpu()[0].tolist() == [1.0, 1.0, 1.0] and s.float().cpu()[3, 1:].tolist() == [1.0, 1.0]
+    assert torch.isfinite(y.float()).all() and torch.isfinite(s.float()).all()
+    y, s = mscan.rms_norm_fwd(dev(x), dev(torch.ones(96)), quant="row", eps=1e-5)
+    assert float(s[0]) == 1.0 and torch.isfinite(y.float()).all() and torch.isfinite(s).all()
+
+
+def test_norm_residual_in_place_and_shapes():
+    g = Rng(4)
+    for dim in (256, 255, 16400):   # vector rows, odd rows, long rows
+        x, res, w = dev(g(2, 3, dim, dtype=torch.bfloat16), g(2, 3, dim, dtype=torch.bfloat16), g(dim))
+        y, r = mscan.rms_norm_fwd(x, w, res)
+        keep = res.clone()
+        y2, r2 = mscan.rms_norm_fwd(x, w, res, residual_out=res)
+        assert r2 is res and torch.equal(res, r) and torch.equal(y, y2) and not torch.equal(res, keep)
+        assert y.shape == (2, 3, dim)
+    empty = mscan.rms_norm_fwd(torch.empty(0, 8, device=DEV), torch.ones(8, device=DEV))
+    assert empty.shape == (0, 8)
+    out = mscan.rms_norm_bwd(torch.empty(0, 8, device=DEV), torch.empty(0, 8, device=DEV), torch.ones(8, device=DEV),
+                             torch.empty(0, device=DEV))
+    assert torch.equal(out["dweight"], torch.zeros(8, device=DEV))
+
+
+# ---------------------------------------------------------------- packed convolution
+
+LENS = [[1], [5], [1, 1, 1], [3, 0, 2, 64], [0, 7, 8, 9, 0], [16, 17, 1, 2, 3, 130], [2] * 70, [300]]
+
+
+def packed(lens):
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    return cu
+
+
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("width,K,gap", [(264, 4, 0), (256, 3, 8), (96, 2, 8), (77, 4, 0), (80, 4, 3), (1032, 4, 0)])
+@pytest.mark.parametrize("lens", LENS, ids=[str(len(v)) + "x" + str(max(v)) for v in LENS])
+def test_conv(lens, width, K, gap, io):
+    r = Rng(sum(lens) + width + K)
+    n, cu = len(lens), packed(lens)
+    x, w, b = r(cu[-1], width, dtype=io), r(width, K, scale=0.5), r(width, scale=0.1)
+    ring = r(n + 2, K, width, dtype=io)
+    slots = r.slots(n, n + 2)
+    pos = i64([[0, 1, 2, 3, 4, 1000, -5][i % 7] for i in range(n)])
+    if n > 2:
+        slots[2] = -1 if n % 2 else n + 2   # no slot
+    u64, ring64 = layer.conv_varlen(x, w, cu, b, ring, slots, pos)
+    size = layer.conv_varlen(x.double().abs(), w.abs(), cu, b.abs(), ring.double().abs(), slots, pos, silu=False)[0]
+    say(f"conv {lens[:8]} width {width} K {K} {io}")
+    rd = dev(ring.clone())
+    u = mscan.ssd_conv_fwd_varlen(apart(x, gap), dev(w), dev(i64(cu)), bias=dev(b), conv_state=rd, slots=dev(slots),
+                                  positions=dev(pos))
+    close("u", u, u64, HALF[io] * u64.abs() + F32 * size)
+    assert torch.equal(rd.cpu().double(), ring64)
+
+
+def test_conv_without_pool_and_rows_outside():
+    r = Rng(9)
+    x, w = r(20, 40), r(40, 4)
+    u64, _ = layer.conv_varlen(x, w, [3, 9, 15], silu=False)
+    out = torch.full((20, 40), 5.0, device=DEV)
+    mscan.ssd_conv_fwd_varlen(dev(x), dev(w), dev(i64([3, 9, 15])), silu=False, out=out)
+    close("u", out, u64, 2.0 ** -18 * 8 * x.abs().max() * w.abs().max() * torch.ones_like(u64))
+    assert torch.equal(out[:3].cpu(), torch.full((3, 40), 5.0)) and torch.equal(out[15:].cpu(), torch.full((5, 40), 5.0))
+
+
+def test_conv_bad_offsets_stay_in_bounds():
+    """Offsets that are no offsets give some numbers, within the arrays, and rings of other slots stay."""
+    r = Rng(10)
+    x, w = dev(r(30, 64, dtype=torch.bfloat16), r(64, 4))
+    for cu in ([-7, 12, 99], [20, 10, 30], [1 << 40, -(1 << 40), 5]):
+        ring = torch.full((3, 4, 64), 2.0, dtype=torch.bfloat16, device=DEV)
+        mscan.ssd_conv_fwd_varlen(x, w, dev(i64(cu)), conv_state=ring, slots=dev(i64([0, 7])), positions=dev(i64([0, 0])))
+        torch.cuda.synchronize()
+        assert torch.equal(ring[1:].cpu(), torch.full((2, 4, 64), 2.0, dtype=torch.bfloat16))
+
+
+# ---------------------------------------------------------------- packed SSM
+
+
+def ssd_case(r, lens, H, P, N, G, delta=(0.001, 0.1), dt_std=1.0):
+    total = sum(lens)
+    bf = torch.bfloat16
+    bias = torch.log(torch.expm1(r.uniform(*delta, H)))
+    return dict(x=r(total, H, P, dtype=bf), dt=r(total, H, dtype=bf, scale=dt_std), A_log=torch.log(r.uniform(1, 16, H)),
+                B=r(total, G, N, dtype=bf), C=r(total, G, N, dtype=bf), D=r(H), z=r(total, H, P, dtype=bf), dt_bias=bias)
+
+
+def run_ssd(c, lens, state, slots, pos, gated, softplus, euler, gap=0, **more):
+    cu = packed(lens)
+    z = c["z"] if gated else None
+    ref = layer.ssd_varlen(c["x"], c["dt"], c["A_log"], c["B"], c["C"], cu, c["D"], z, c["dt_bias"], state, slots, pos, softplus, euler)
+    sd, sl, po = dev(None if state is None else state.clone(), slots, pos)
+    y = mscan.ssd_fwd_varlen(apart(c["x"], gap), apart(c["dt"], gap), dev(c["A_log"]), apart(c["B"], gap), apart(c["C"], gap),
+                             dev(i64(cu)), D=dev(c["D"]), z=None if z is None else apart(z, gap), dt_bias=dev(c["dt_bias"]),
+                             state=sd, slots=sl, positions=po, dt_softplus=softplus,
+                             discretization="euler" if euler else "zoh", **more)
+    torch.cuda.synchronize()
+    return y, sd, ref
+
+
+def check_ssd(lens, y, state, ref):
+    y64, s64, ya, sa = ref
+    close("y", y, y64, 2.0 ** -8 * y64.abs() + (2.0 ** -8 + 2.0 ** -14) * ya)
+    if state is not None:
+        chunks = max(lens) // 64 + 1
+        close("state", state, s64, (2.0 ** -16 + chunks * 2.0 ** -21) * sa)
+
+
+SSD = [  # lens, H, P, N, G, gated, softplus, euler, gap
+    ([1], 1, 64, 128, 1, True, True, False, 0),
+    ([64], 2, 64, 128, 1, False, True, False, 8),
+    ([65], 2, 64, 64, 2, True, True, True, 0),
+    ([1, 0, 130, 63, 64, 2], 3, 64, 128, 1, True, True, False, 16),
+    ([33, 200], 2, 32, 128, 1, True, True, False, 0),
+    ([31, 97], 3, 96, 64, 3, False, True, True, 8),
+    ([150], 2, 128, 128, 2, True, False, False, 0),
+    ([140, 5], 2, 192, 64, 1, True, True, False, 0),
+    ([70], 1, 256, 128, 1, False, False, True, 0),
+    ([3] * 130, 2, 64, 64, 1, True, True, False, 0),
+    ([1300], 4, 64, 128, 2, True, True, False, 0),
+]
+
+
+@pytest.mark.parametrize("case", SSD, ids=[f"{len(c[0])}x{max(c[0])}H{c[1]}P{c[2]}N{c[3]}G{c[4]}" for c in SSD])
+def test_ssd(case):
+    lens, H, P, N, G, gated, softplus, euler, gap = case
+    r = Rng(sum(lens) + H + P)
+    c = ssd_case(r, lens, H, P, N, G)
+    if not softplus:
+        c["dt"], c["dt_bias"] = (c["dt"].float().abs() * 0.05).bfloat16(), c["dt_bias"].abs() * 0.01
+    n = len(lens)
+    state, slots = r(n + 2, H, P, N), r.slots(n, n + 2)
+    pos = i64([[5, 0, 1, 700][i % 4] for i in range(n)])
+    if n > 3:
+        slots[3] = -1
+    say(f"ssd {case}")
+    y, sd, ref = run_ssd(c, lens, state, slots, pos, gated, softplus, euler, gap)
+    check_ssd(lens, y, sd, ref)
+    y2, sd2, _ = run_ssd(c, lens, state, slots, pos, gated, softplus, euler, gap)
+    assert torch.equal(y, y2) and torch.equal(sd, sd2)
+    y3, _, ref3 = run_ssd(c, lens, None, None, None, gated, softplus, euler)
+    check_ssd(lens, y3, None, ref3)
+
+
+@pytest.mark.parametrize("delta,dt_std,x_std", [((1e-4, 2e-4), 0.1, 1.0), ((1e-4, 2e-4), 0.1, 0.01), ((2.0, 6.0), 1.0, 1.0)])
+def test_ssd_small_and_large_steps(delta, dt_std, x_std):
+    """Delta ~ 1e-4, where a state keeps its inputs over the whole prompt, and Delta |A| ~ 100, where it keeps none."""
+    lens = [700, 90]
+    r = Rng(5)
+    c = ssd_case(r, lens, 3, 64, 128, 1, delta, dt_std)
+    c["x"] = (c["x"].float() * x_std).bfloat16()
+    say(f"ssd steps {delta}")
+    y, sd, ref = run_ssd(c, lens, r(2, 3, 64, 128), i64([1, 0]), i64([9, 0]), True, True, False)
+    check_ssd(lens, y, sd, ref)
+
+
+def test_ssd_new_requests_ignore_what_their_slot_holds():
+    r = Rng(6)
+    lens = [70, 3]
+    c = ssd_case(r, lens, 2, 64, 128, 1)
+    bad = torch.full((2, 2, 64, 128), float("nan"))
+    y, sd, _ = run_ssd(c, lens, bad, i64([0, 1]), i64([0, 0]), True, True, False)
+    y2, sd2, ref = run_ssd(c, lens, torch.zeros(2, 2, 64, 128), i64([0, 1]), i64([0, 0]), True, True, False)
+    check_ssd(lens, y2, sd2, ref)
+    assert torch.equal(y, y2) and torch.equal(sd, sd2)
+
+
+def test_ssd_rows_outside_are_left():
+    r = Rng(7)
+    c = ssd_case(r, [100], 2, 64, 64, 1)
+    out = torch.full((100, 2, 64), 3.0, dtype=torch.bfloat16, device=DEV)
+    mscan.ssd_fwd_varlen(dev(c["x"]), dev(c["dt"]), dev(c["A_log"]), dev(c["B"]), dev(c["C"]), dev(i64([10, 40, 90])), out=out)
+    assert torch.equal(out[:10].cpu(), torch.full((10, 2, 64), 3.0).bfloat16())
+    assert torch.equal(out[90:].cpu(), torch.full((10, 2, 64), 3.0).bfloat16())
+    ref = layer.ssd_varlen(c["x"], c["dt"], c["A_log"], c["B"], c["C"], [10, 40, 90])
+    check_ssd([50], out, None, ref)
+
+
+def test_ssd_equals_the_fixed_length_forward():
+    """A packed batch of equal sequences against mamba_ssd_fwd, each within a bf16 step and its own bf16 products."""
+    r = Rng(8)
+    b, L, H, P, N = 2, 150, 3, 64, 128
+    c = ssd_case(r, [L] * b, H, P, N, 1)
+    h0 = r(b, H, P, N)
+    ref = layer.ssd_varlen(c["x"], c["dt"], c["A_log"], c["B"], c["C"], packed([L] * b), c["D"], c["z"], c["dt_bias"], h0, i64([0, 1]), i64([1, 1]))
+    y, fs = mscan.ssd_fwd(dev(c["x"].view(b, L, H, P)), dev(c["dt"].view(b, L, H)), dev(c["A_log"]), dev(c["B"].view(b, L, N)),
+                          dev(c["C"].view(b, L, N)), D=dev(c["D"]), z=dev(c["z"].view(b, L, H, P)), dt_bias=dev(c["dt_bias"]),
+                          initial_state=dev(h0), return_final_state=True)
+    st = dev(h0.clone())
+    yv = mscan.ssd_fwd_varlen(dev(c["x"]), dev(c["dt"]), dev(c["A_log"]), dev(c["B"]), dev(c["C"]), dev(i64(packed([L] * b))),
+                              D=dev(c["D"]), z=dev(c["z"]), dt_bias=dev(c["dt_bias"]), state=st, slots=dev(i64([0, 1])),
+                              positions=dev(i64([1, 1])))
+    tol = 2 * (2.0 ** -8 * ref[0].abs() + (2.0 ** -8 + 2.0 ** -14) * ref[2])
+    close("y", yv, y.cpu().double().view(b * L, H, P), tol)
+    close("state", st, fs.cpu().double(), 2.0 ** -14 * ref[3])
+
+
+# ---------------------------------------------------------------- single tokens
+
+STEP = [  # batch, pad, H, P, N, G, K, io, gated, softplus, euler, gap
+    (1, 0, 1, 32, 64, 1, 4, torch.bfloat16, True, True, False, 0),
+    (1, 0, 5, 64, 128, 1, 4, torch.bfloat16, True, True, False, 8),
+    (3, 1, 4, 64, 128, 2, 4, torch.float32, True, True, False, 3),
+    (5, 0, 3, 96, 128, 3, 2, torch.bfloat16, False, True, True, 1),
+    (4, 2, 2, 256, 64, 1, 3, torch.float32, False, False, False, 0),
+    (2, 0, 6, 160, 64, 2, 4, torch.bfloat16, True, False, True, 5),
+    (40, 7, 16, 64, 128, 1, 4, torch.bfloat16, True, True, False, 0),   # whole slices of 64 channels
+    (40, 3, 16, 32, 128, 4, 4, torch.float32, True, True, True, 0),
+    (40, 1, 16, 32, 64, 1, 4, torch.bfloat16, True, True, False, 0),
+    (40, 0, 14, 64, 64, 7, 4, torch.float32, True, True, False, 0),
+]
+
+
+def step_case(r, batch, H, P, N, G, K, io):
+    width = H * P + 2 * G * N
+    return dict(xbc=r(batch, width, dtype=io), dt=r(batch, H, dtype=io), A_log=torch.log(r.uniform(1, 16, H)),
+                conv_weight=r(width, K, scale=0.5), conv_bias=r(width, scale=0.1), D=r(H), z=r(batch, H, P, dtype=io),
+                dt_bias=torch.log(torch.expm1(r.uniform(0.001, 0.1, H))))
+
+
+@pytest.mark.parametrize("case", STEP, ids=[f"b{c[0]}H{c[2]}P{c[3]}N{c[4]}G{c[5]}K{c[6]}" for c in STEP])
+def test_step(case):
+    batch, pad, H, P, N, G, K, io, gated, softplus, euler, gap = case
+    r = Rng(batch + H + P)
+    c = step_case(r, batch, H, P, N, G, K, io)
+    ring, state = r(batch + 3, K, c["xbc"].shape[1], dtype=io), r(batch + 3, H, P, N)
+    slots = r.slots(batch, batch + 3)
+    for i in range(pad):
+        slots[batch - 1 - i] = [-1, batch + 3, 1 << 40][i % 3]
+    pos = i64([[0, 1, 2, 3, 4, 77, 1 << 40, -2][i % 8] for i in range(batch)])
+    say(f"step {case}")
+    for sl in (slots, None):
+        z = c["z"] if gated else None
+        y64, ring64, st64, ya, sa = layer.ssd_step(c["xbc"], c["dt"], c["A_log"], c["conv_weight"], ring, state, pos, sl, c["D"], z,
+                                                   c["dt_bias"], c["conv_bias"], softplus, euler)
+        rd, sd = dev(ring.clone(), state.clone())
+        out = torch.full((batch, H, P), 9.0, dtype=io, device=DEV)
+        y = mscan.ssd_step(apart(c["xbc"], gap), apart(c["dt"], gap), dev(c["A_log"]), dev(c["conv_weight"]), rd, sd, dev(pos),
+                           slots=dev(sl), D=dev(c["D"]), z=None if z is None else apart(z, gap), dt_bias=dev(c["dt_bias"]),
+                           conv_bias=dev(c["conv_bias"]), dt_softplus=softplus, out=out,
+                           discretization="euler" if euler else "zoh")
+        # SiLU of the convolution: 1.1 times its error, which is F32 of sums that the products here hide; the
+        # widest is ~20 times the result, so 2^-18 of the sums over absolute values becomes 2^-15
+        close("y", y, y64, HALF[io] * y64.abs() + 2.0 ** -15 * (ya + 1))
+        close("state", sd, st64, 2.0 ** -17 * (sa + 1))
+        assert torch.equal(rd.cpu().double(), ring64)
+        if sl is not None and pad:
+            assert torch.equal(y[batch - pad:].cpu(), torch.full((pad, H, P), 9.0, dtype=io))
+
+
+def test_step_new_requests_ignore_what_their_slot_holds():
+    r = Rng(2)
+    c = step_case(r, 2, 2, 64, 128, 1, 4, torch.bfloat16)
+    args = dev(c["xbc"], c["dt"], c["A_log"], c["conv_weight"])
+    got = []
+    for fill in (float("nan"), 0.0):
+        ring = torch.full((2, 4, c["xbc"].shape[1]), fill, dtype=torch.bfloat16, device=DEV)
+        state = torch.full((2, 2, 64, 128), fill, device=DEV)
+        got.append((mscan.ssd_step(*args, ring, state, dev(i64([0, 0]))), state))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+# ---------------------------------------------------------------- together
+
+
+def layer_weights(r, d, H, P, N, G):
+    inner, width = H * P, H * P + 2 * G * N
+    return dict(norm=1 + r(d, scale=0.1), w_in=r(inner + width + H, d, scale=d ** -0.5), conv_weight=r(width, 4, scale=0.5),
+                conv_bias=r(width, scale=0.1), A_log=torch.log(r.uniform(1, 16, H)), D=r(H),
+                dt_bias=torch.log(torch.expm1(r.uniform(0.001, 0.1, H))), norm2=1 + r(inner, scale=0.1), w_out=r(d, inner, scale=inner ** -0.5))
+
+
+def run_layer(w, h, residual, H, P, N, G, ring, state, positions, slots, cu=None):
+    """norm -> in-projection -> conv + SSM -> norm -> out-projection, for packed prompts (cu) or one token a row."""
+    inner, width = H * P, H * P + 2 * G * N
+    n, residual = mscan.rms_norm_fwd(h, w["norm"], residual)
+    # in fp64, so that a token's projection does not depend on how many tokens it came with
+    proj = (n.double() @ w["w_in"].double().t()).bfloat16()
+    z, xbc, dt = proj[:, :inner].unflatten(1, (H, P)), proj[:, inner:inner + width], proj[:, inner + width:]
+    if cu is None:
+        y = mscan.ssd_step(xbc, dt, w["A_log"], w["conv_weight"], ring, state, positions, slots=slots, D=w["D"], z=z,
+                           dt_bias=w["dt_bias"], conv_bias=w["conv_bias"])
+    else:
+        u = mscan.ssd_conv_fwd_varlen(xbc, w["conv_weight"], cu, bias=w["conv_bias"], conv_state=ring, slots=slots, positions=positions)
+        y = mscan.ssd_fwd_varlen(u[:, :inner].unflatten(1, (H, P)), dt, w["A_log"], u[:, inner:inner + G * N].unflatten(1, (G, N)),
+                                 u[:, inner + G * N:].unflatten(1, (G, N)), cu, D=w["D"], z=z, dt_bias=w["dt_bias"], state=state,
+                                 slots=slots, positions=positions)
+    q, scale = mscan.rms_norm_fwd(y.flatten(1), w["norm2"], quant="row")
+    return ((q.float() * scale[:, None]).bfloat16() @ w["w_out"].bfloat16().t()), residual
+
+
+def test_prompts_then_tokens_equal_one_long_prompt():
+    """Two requests: a prompt each (in two parts), then tokens one at a time, against the whole sequences as one packed
+    prompt.  The states agree to the rounding of the convolution's outputs to bf16, which only the packed form
+    has: 2^-8 of each of x and B in the tokens' terms, so 2^-7 of the sum over absolute values."""
+    r = Rng(11)
+    d, H, P, N, G = 256, 8, 64, 128, 2
+    w = {k: v.to(DEV) for k, v in layer_weights(r, d, H, P, N, G).items()}
+    lens, tail = [90, 37], 6
+    h = [r(n + tail, d, dtype=torch.bfloat16).to(DEV) for n in lens]
+    width = H * P + 2 * G * N
+
+    def pools():
+        return torch.zeros(4, 4, width, dtype=torch.bfloat16, device=DEV), torch.zeros(4, H, P, N, device=DEV)
+
+    slots = dev(i64([2, 0]))
+    ring_a, state_a = pools()
+    whole = torch.cat(h)
+    out_a, _ = run_layer(w, whole, whole * 0, H, P, N, G, ring_a, state_a, dev(i64([0, 0])), slots, dev(i64(packed([n + tail for n in lens]))))
+    ring_b, state_b = pools()
+    outs = [[], []]
+    for a, e in (((0, 0), (50, 2)), ((50, 2), lens)):
+        part = torch.cat([t[x:y] for t, x, y in zip(h, a, e)])
+        cu = packed([y - x for x, y in zip(a, e)])
+        o, _ = run_layer(w, part, part * 0, H, P, N, G, ring_b, state_b, dev(i64(list(a))), slots, dev(i64(cu)))
+        for i in range(2):
+            outs[i].append(o[cu[i]:cu[i + 1]])
+    for k in range(tail):
+        one = torch.stack([t[n + k] for t, n in zip(h, lens)])
+        o, _ = run_layer(w, one, one * 0, H, P, N, G, ring_b, state_b, dev(i64([n + k for n in lens])), slots)
+        for i in range(2):
+            outs[i].append(o[i:i + 1])
+    for i in range(2):   # the rows of the last K - 1 positions (the fourth holds a token that no one will read)
+        rows = [(lens[i] + tail - back) % 4 for back in (1, 2, 3)]
+        assert torch.equal(ring_a[slots[i]][rows], ring_b[slots[i]][rows])
+    size = state_a.abs().mean(dim=(2, 3), keepdim=True).cpu().double()
+    close("state", state_b, state_a.cpu().double(), 2.0 ** -7 * (state_a.abs().cpu().double() + 8 * size) + 1e-12)
+    got, want = torch.cat([torch.cat(v) for v in outs]).float(), out_a.float()
+    off = float((got - want).norm() / want.norm())
+    say(f"outputs of the two ways differ by {off:.2e} of their norm")
+    assert off < 2.0 ** -4   # 8-bit activations: one step where a value falls on the other side
+
+
+def test_layer_graph_replays_equal_eager():
+    """The whole layer for one token a row captured and replayed, rows padded, with eager work on the same library in
+    between; and packed prompts captured the same way."""
+    r = Rng(12)
+    d, H, P, N, G, batch = 128, 8, 64, 128, 1, 6
+    w = {k: v.to(DEV) for k, v in layer_weights(r, d, H, P, N, G).items()}
+    width = H * P + 2 * G * N
+    for cu in (None, dev(i64([0, 70, 75, 200, 200, 330, 400]))):
+        n = batch if cu is None else 400
+        h, res = dev(r(n, d, dtype=torch.bfloat16), r(n, d, dtype=torch.bfloat16))
+        slots, pos = dev(i64([4, 1, 0, -1, 5, 2])), dev(i64([3, 0, 9, 4, 1, 2]))
+        pools = [(dev(r(batch, 4, width, dtype=torch.bfloat16)), dev(r(batch, H, P, N))) for _ in range(1)][0]
+        eager, graphed = [p.clone() for p in pools], [p.clone() for p in pools]
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            run_layer(w, h, res, H, P, N, G, *[p.clone() for p in pools], pos, slots, cu)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out, _ = run_layer(w, h, res, H, P, N, G, *graphed, pos, slots, cu)
+        keep = [0, 1, 2, 4, 5] if cu is None else list(range(400))
+        for rep in range(4):
+            want, _ = run_layer(w, h, res, H, P, N, G, *eager, pos, slots, cu)
+            graph.replay()
+            torch.cuda.synchronize()
+            say(f"replay {rep}")
+            assert torch.equal(out[keep], want[keep])
+            for a, b in zip(eager, graphed):
+                assert torch.equal(a, b)
+
+
+def test_side_streams_at_once():
+    """Two prompts batches on two streams at the same time, each with its own workspace, equal what they give alone."""
+    r = Rng(13)
+    lens = [600, 40]
+    cases = [ssd_case(r, lens, 4, 64, 128, 1) for _ in range(2)]
+    cu = dev(i64(packed(lens)))
+    cases = [{k: v.to(DEV) for k, v in c.items()} for c in cases]   # alive until the streams are done with them
+
+    def call(c, stream=None):
+        return mscan.ssd_fwd_varlen(c["x"], c["dt"], c["A_log"], c["B"], c["C"], cu, D=c["D"], stream=stream)
+
+    alone = [call(c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(3):
+        both = [call(c, s) for c, s in zip(cases, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(alone, both))

@@ -1,0 +1,235 @@
+"""The SSD layer's serving operators and the norm on the CPU: the refusals of the C ABI (each call fails
+validation, so the fake pointers are never touched), those of the binding, and the fp64 definitions
+against closed forms, the conv and SSD oracles, and differences."""
+import ctypes
+import os
+import re
+import subprocess
+
+import pytest
+import torch
+
+import oracle
+import selective_state_space_55_amd as mscan
+from oracle import layer
+from selective_state_space_55_amd import build as hipbuild
+
+OK, ENULL, ESHAPE, EDTYPE, EALIGN, EUNSUP, EWS, EHIP = range(8)
+P = 0x10000   # a fake, 256-byte aligned device address
+BAD = ctypes.c_size_t(-1).value
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return mscan.load_library()
+
+
+def test_norm_symbols_are_exported(lib):
+    for n in mscan.EXPORTED_NORM:
+        assert hasattr(lib, n), n
+
+
+def conv(lib, x=P, w=P, b=None, cu=P, ring=P, slots=P, pos=P, u=P, nseq=2, total=10, width=64, K=4, xs=64, nslots=4,
+         io=1, silu=1):
+    return lib.mamba_ssd_conv_fwd_varlen(x, w, b, cu, ring, slots, pos, u, nseq, total, width, K, xs, nslots, io, silu, None)
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(w=None), ENULL), (dict(cu=None), ENULL), (dict(x=None), ENULL), (dict(u=None), ENULL),
+    (dict(slots=None), ENULL), (dict(pos=None), ENULL), (dict(ring=None), ENULL),   # a pool, its slots and positions
+    (dict(nseq=0), ESHAPE), (dict(total=-1), ESHAPE), (dict(width=0), ESHAPE), (dict(nslots=-1), ESHAPE),
+    (dict(xs=63), ESHAPE), (dict(total=1 << 60), ESHAPE), (dict(K=1), EUNSUP), (dict(K=5), EUNSUP), (dict(io=2), EDTYPE),
+    (dict(x=P + 1), EALIGN), (dict(io=0, u=P + 2), EALIGN), (dict(w=P + 2), EALIGN), (dict(cu=P + 4), EALIGN),
+    (dict(slots=P + 4), EALIGN), (dict(pos=P + 4), EALIGN), (dict(total=1 << 33), EUNSUP),
+    (dict(width=1 << 23, xs=1 << 23), EUNSUP),
+])
+def test_conv_refusals(lib, bad, code):
+    assert conv(lib, **bad) == code
+
+
+def ssd(lib, x=P, dt=P, A=P, B=P, C=P, D=None, z=None, bias=None, cu=P, state=P, slots=P, pos=P, y=P, nseq=2, total=100,
+        H=4, hd=64, N=128, G=1, nslots=4, xs=256, ds=4, bs=128, cs=128, zs=256, io=1, flags=1, ws=P, wsb=1 << 40):
+    return lib.mamba_ssd_fwd_varlen(x, dt, A, B, C, D, z, bias, cu, state, slots, pos, y, nseq, total, H, hd, N, G, nslots,
+                                    xs, ds, bs, cs, zs, io, flags, ws, wsb, None)
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(x=None), ENULL), (dict(dt=None), ENULL), (dict(A=None), ENULL), (dict(B=None), ENULL), (dict(y=None), ENULL),
+    (dict(cu=None), ENULL), (dict(slots=None), ENULL), (dict(pos=None), ENULL), (dict(state=None), ENULL),
+    (dict(nseq=0), ESHAPE), (dict(total=-1), ESHAPE), (dict(H=0), ESHAPE), (dict(G=0), ESHAPE), (dict(nslots=-1), ESHAPE),
+    (dict(xs=248), ESHAPE), (dict(ds=3), ESHAPE), (dict(bs=120), ESHAPE), (dict(z=P, zs=0), ESHAPE),
+    (dict(G=3), EUNSUP), (dict(hd=48, xs=192), EUNSUP), (dict(hd=288, xs=1152), EUNSUP), (dict(N=96), EUNSUP),
+    (dict(io=0), EUNSUP), (dict(flags=4), EUNSUP), (dict(xs=(1 << 24) + 8), EUNSUP), (dict(nseq=1 << 30), EUNSUP),
+    (dict(io=9), EDTYPE),
+    (dict(xs=257), EALIGN), (dict(bs=132), EALIGN), (dict(cs=132), EALIGN), (dict(z=P, zs=260), EALIGN), (dict(x=P + 8), EALIGN),
+    (dict(z=P + 8), EALIGN), (dict(state=P + 8), EALIGN), (dict(y=P + 8), EALIGN), (dict(dt=P + 1), EALIGN),
+    (dict(A=P + 2), EALIGN), (dict(cu=P + 4), EALIGN), (dict(slots=P + 4), EALIGN),
+])
+def test_ssd_refusals(lib, bad, code):
+    assert ssd(lib, **bad) == code
+
+
+def test_ssd_workspace(lib):
+    f = lib.mamba_ssd_fwd_varlen_workspace_size
+    assert f(0, 10, 4, 64, 128) == BAD and f(1, 10, 4, 48, 128) == BAD and f(1, 10, 4, 64, 32) == BAD
+    # where a workspace is needed, one that is missing, short or badly aligned is refused
+    need = f(1, 1 << 20, 4, 64, 128)
+    assert need != BAD
+    if need:
+        big = dict(nseq=1, total=1 << 20)
+        assert ssd(lib, ws=None, **big) == EWS
+        assert ssd(lib, wsb=need - 1, **big) == EWS
+        assert ssd(lib, ws=P + 128, **big) == EWS
+
+
+def step(lib, xbc=P, dt=P, A=P, cw=P, cb=None, ring=P, state=P, slots=P, pos=P, D=None, z=None, bias=None, y=P, batch=3,
+         H=4, hd=64, N=128, G=1, K=4, nslots=4, xs=512, ds=4, zs=256, io=1, flags=1):
+    return lib.mamba_ssd_step(xbc, dt, A, cw, cb, ring, state, slots, pos, D, z, bias, y, batch, H, hd, N, G, K, nslots, xs, ds,
+                              zs, io, flags, None)
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(xbc=None), ENULL), (dict(dt=None), ENULL), (dict(cw=None), ENULL), (dict(ring=None), ENULL),
+    (dict(state=None), ENULL), (dict(pos=None), ENULL), (dict(y=None), ENULL),
+    (dict(batch=0), ESHAPE), (dict(xs=511), ESHAPE), (dict(ds=3), ESHAPE), (dict(z=P, zs=255), ESHAPE), (dict(nslots=-1), ESHAPE),
+    (dict(K=1), EUNSUP), (dict(K=5), EUNSUP), (dict(hd=40), EUNSUP), (dict(N=16), EUNSUP), (dict(G=3), EUNSUP),
+    (dict(flags=8), EUNSUP), (dict(batch=1 << 30), EUNSUP), (dict(io=2), EDTYPE),
+    (dict(xbc=P + 1), EALIGN), (dict(state=P + 8), EALIGN), (dict(pos=P + 4), EALIGN), (dict(slots=P + 4), EALIGN),
+    (dict(cw=P + 2), EALIGN), (dict(io=0, ring=P + 2), EALIGN),
+])
+def test_step_refusals(lib, bad, code):
+    assert step(lib, **bad) == code
+
+
+def norm(lib, x=P, res=None, w=P, ro=None, y=P, sc=None, rstd=None, rows=3, dim=64, io=1, rio=1, out=0):
+    return lib.mamba_rms_norm_fwd(x, res, w, 1e-5, ro, y, sc, rstd, rows, dim, io, rio, out, None)
+
+
+def norm_bwd(lib, dy=P, r=P, w=P, rstd=P, dres=None, dx=P, dr=None, dw=P, rows=3, dim=64, io=1, rio=1, ws=P, wsb=1 << 40):
+    return lib.mamba_rms_norm_bwd(dy, r, w, rstd, dres, dx, dr, dw, rows, dim, io, rio, ws, wsb, None)
+
+
+@pytest.mark.parametrize("call,bad,code", [
+    (norm, dict(x=None), ENULL), (norm, dict(w=None), ENULL), (norm, dict(y=None), ENULL), (norm, dict(out=1), ENULL),
+    (norm, dict(res=P), ENULL), (norm, dict(ro=P), ENULL), (norm, dict(rows=-1), ESHAPE), (norm, dict(dim=0), ESHAPE),
+    (norm, dict(io=3), EDTYPE), (norm, dict(io=0, rio=1), EDTYPE), (norm, dict(out=3, sc=P), EUNSUP),
+    (norm, dict(rows=1 << 40), EUNSUP), (norm, dict(x=P + 1), EALIGN), (norm, dict(rio=0, res=P + 2, ro=P), EALIGN),
+    (norm, dict(out=1, sc=P + 2), EALIGN), (norm, dict(rstd=P + 2), EALIGN),
+    (norm_bwd, dict(dy=None), ENULL), (norm_bwd, dict(rstd=None), ENULL), (norm_bwd, dict(dw=None), ENULL),
+    (norm_bwd, dict(dx=None), ENULL), (norm_bwd, dict(dr=P), EUNSUP), (norm_bwd, dict(io=0, rio=1), EDTYPE),
+    (norm_bwd, dict(rows=-1), ESHAPE), (norm_bwd, dict(dim=0), ESHAPE), (norm_bwd, dict(ws=None), EWS),
+    (norm_bwd, dict(wsb=100), EWS), (norm_bwd, dict(ws=P + 64), EWS), (norm_bwd, dict(dx=P + 1), EALIGN),
+])
+def test_norm_refusals(lib, call, bad, code):
+    assert call(lib, **bad) == code
+
+
+def test_empty_calls_return_ok_without_a_launch(lib):
+    assert conv(lib, total=0, x=None, u=None) == OK
+    assert ssd(lib, total=0, x=None, dt=None, B=None, C=None, y=None) == OK
+    assert norm(lib, rows=0, x=None, y=None) == OK
+
+
+def test_binding_refusals():
+    x = torch.zeros(4, 64)
+    for call in (lambda: mscan.ssd_conv_fwd_varlen(x, torch.zeros(64, 4), torch.zeros(2, dtype=torch.int64)),
+                 lambda: mscan.ssd_fwd_varlen(torch.zeros(4, 1, 64), x, x, x, x, x),
+                 lambda: mscan.ssd_step(x, x, x, x, x, torch.zeros(1, 1, 32, 64), x),
+                 lambda: mscan.rms_norm_fwd(x, torch.zeros(64)),
+                 lambda: mscan.rms_norm_bwd(x, x, torch.zeros(64), torch.zeros(4))):
+        with pytest.raises(ValueError):   # host tensors, wrong ranks
+            call()
+
+
+@pytest.mark.parametrize("src", ["rms_norm.hip", "ssd_conv.hip", "ssd_step.hip", "ssd_varlen.hip"])
+def test_assembly(src, tmp_path):
+    """No packed fp32 instructions, no scratch memory."""
+    out = str(tmp_path / "k.s")
+    flags = [f for f in hipbuild.flags() if f not in ("-shared", "-fPIC")]
+    subprocess.run([hipbuild.hipcc()] + flags + ["--cuda-device-only", "-S", "-o", out, os.path.join(hipbuild.CSRC, src)],
+                   check=True, capture_output=True)
+    text = open(out).read()
+    assert not re.findall(r"\bv_pk_(?:add|mul|fma)_f32\b", text)
+    sizes = [int(v) for v in re.findall(r"\.private_segment_fixed_size:\s+(\d+)", text)]
+    assert sizes and max(sizes) == 0
+
+
+# ---------------------------------------------------------------- the definitions
+
+
+def rnd(*shape, seed=0, scale=1.0):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed), dtype=torch.float64) * scale
+
+
+def test_conv_definition_against_the_conv_oracle():
+    """Whole sequences through the padded conv's oracle, and any split through the ring."""
+    L, W, K = 11, 5, 4
+    x, w, b = rnd(L, W, seed=1).float(), rnd(W, K, seed=2).float(), rnd(W, seed=3).float()
+    ref = oracle.conv1d_fwd(x.t()[None].contiguous(), w, bias=b)
+    ref = torch.as_tensor(ref[0] if isinstance(ref, tuple) else ref)[0].t()
+    u, _ = layer.conv_varlen(x, w, [0, L], b)
+    assert torch.allclose(u, ref.double(), rtol=0, atol=1e-12)
+    for cuts in ([1], [2, 3], [4, 5, 6, 9], list(range(1, L))):
+        ring = torch.full((3, K, W), 7.0)   # what a slot holds before a request does not matter
+        edges, out = [0] + cuts + [L], []
+        for a, e in zip(edges, edges[1:]):
+            part, ring = layer.conv_varlen(x[a:e], w, [0, e - a], b, ring, [1], [a])
+            out.append(part)
+        assert torch.equal(torch.cat(out), u)
+        assert torch.equal(ring[0], torch.full((K, W), 7.0).double())   # another slot
+
+
+def test_ssd_definition_against_the_ssd_oracle():
+    L, H, Pd, N = 9, 2, 32, 64
+    x, dt, B, C, z = (rnd(*s, seed=i).bfloat16() for i, s in enumerate([(1, L, H, Pd), (1, L, H), (1, L, N), (1, L, N), (1, L, H, Pd)]))
+    A, D, bias = rnd(H, seed=7).float(), rnd(H, seed=8).float(), rnd(H, seed=9).float()
+    h0 = rnd(1, H, Pd, N, seed=10).float()
+    for disc in ("zoh", "euler"):
+        yr, fr = oracle.ssd_fwd(x, dt, A, B, C, D=D, z=z, dt_bias=bias, initial_state=h0, discretization=disc)
+        state = h0.double().clone()
+        parts = []
+        for a, e in ((0, 4), (4, L)):
+            yp, state, _, _ = layer.ssd_varlen(x[0, a:e], dt[0, a:e], A, B[0, a:e, None], C[0, a:e, None], [0, e - a], D, z[0, a:e],
+                                               bias, state, [0], [a + 1], euler=disc == "euler")
+            parts.append(yp)
+        assert torch.allclose(torch.cat(parts), torch.as_tensor(yr)[0].double(), rtol=1e-10, atol=1e-12)
+        assert torch.allclose(state, torch.as_tensor(fr).double(), rtol=1e-10, atol=1e-12)
+
+
+def test_norm_definitions():
+    x, w = rnd(4, 40, seed=1), 1 + rnd(40, seed=2, scale=0.1)
+    y, r, rstd = layer.rms_norm(x, w, rnd(4, 40, seed=3), eps=0.0)
+    assert torch.allclose((y / w).square().mean(1), torch.ones(4, dtype=torch.float64))
+    # e4m3 against torch's own values, on every representable value and the points between
+    grid = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+    grid = grid[torch.isfinite(grid)].unique()
+    mid = (grid[1:] + grid[:-1]) / 2
+    for v in (grid, mid * (1 + 1e-9), mid * (1 - 1e-9)):
+        q = layer.e4m3(v)
+        near = (grid[None] - v[:, None]).abs().argmin(1)
+        assert torch.equal(q, grid[near])
+    s = layer.block_scale(torch.tensor([[448.0] * 32 + [448.5] * 32 + [0.0] * 3]).double())
+    assert s.tolist() == [[1.0, 2.0, 1.0]]
+
+
+@pytest.mark.parametrize("with_res", [False, True])
+def test_norm_gradient_definition_against_differences(with_res):
+    x, w, dy = rnd(3, 10, seed=1), 1 + rnd(10, seed=2, scale=0.2), rnd(3, 10, seed=3)
+    dres = rnd(3, 10, seed=4) if with_res else None
+
+    def loss(x, w):
+        y, r, _ = layer.rms_norm(x, w)
+        return (y * dy).sum() + ((r * dres).sum() if with_res else 0)
+
+    _, r, rstd = layer.rms_norm(x, w)
+    dr, dw, _, _ = layer.rms_norm_bwd(dy, r, w, rstd, dres)
+    e = 1e-6
+    for i in range(3):
+        for c in range(10):
+            d = torch.zeros_like(x)
+            d[i, c] = e
+            assert abs((loss(x + d, w) - loss(x - d, w)) / (2 * e) - dr[i, c]) < 1e-7
+    for c in range(10):
+        d = torch.zeros_like(w)
+        d[c] = e
+        assert abs((loss(x, w + d) - loss(x, w - d)) / (2 * e) - dw[c]) < 1e-7
