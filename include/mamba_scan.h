@@ -435,7 +435,7 @@ int mamba_ssd_fwd_varlen(const void* x, const void* dt, const float* A_log, cons
 
 /* Bytes of workspace mamba_ssd_fwd_varlen needs (may be 0); (size_t)-1 for rejected sizes. */
 size_t mamba_ssd_fwd_varlen_workspace_size(int64_t nseq, int64_t total_len, int64_t nheads, int64_t headdim,
-                                           int64_t dstate);
+                                           int64_t dstate, int64_t ngroups);
 
 /*
  * One token per request through the layer's core: the convolution of mamba_ssd_conv_fwd_varlen (with

@@ -93,7 +93,7 @@ def load_library():
     lib.mamba_ssd_fwd_varlen.restype = I
     lib.mamba_ssd_fwd_varlen.argtypes = [P] * 13 + [I64] * 12 + [I, I, P, SZ, P]
     lib.mamba_ssd_fwd_varlen_workspace_size.restype = SZ
-    lib.mamba_ssd_fwd_varlen_workspace_size.argtypes = [I64] * 5
+    lib.mamba_ssd_fwd_varlen_workspace_size.argtypes = [I64] * 6
     lib.mamba_ssd_step.restype = I
     lib.mamba_ssd_step.argtypes = [P] * 13 + [I64] * 10 + [I, I, P]
     lib.mamba_rms_norm_fwd.restype = I
@@ -601,25 +601,37 @@ def ssd_fwd(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, B: torch.Ten
     return (y, fs) if return_final_state else y
 
 
-def _on_device(fn):
-    """Runs fn with the first argument's device current (the library launches on the current device)."""
+def _entry(fn):
+    """Runs fn with the device of its first argument current (the library launches on the current device) and
+    with its `stream` argument, if any, made the current stream, as _on_stream does."""
+    on_stream = _on_stream(fn)
 
     @functools.wraps(fn)
     def run(*args, **kwargs):
         t0 = args[0] if args else next(iter(kwargs.values()), None)
-        if not isinstance(t0, torch.Tensor) or t0.device.type != "cuda" or t0.get_device() == torch.cuda.current_device():
-            return fn(*args, **kwargs)
-        with torch.cuda.device(t0.device):
-            return fn(*args, **kwargs)
+        dev = t0.get_device() if isinstance(t0, torch.Tensor) and t0.is_cuda else -1
+        if dev < 0 or dev == torch.cuda.current_device():
+            return fn(*args, **kwargs) if kwargs.get("stream") is None else on_stream(*args, **kwargs)
+        with torch.cuda.device(dev):
+            return fn(*args, **kwargs) if kwargs.get("stream") is None else on_stream(*args, **kwargs)
 
     return run
+
+
+def _need(name: str, t, shape, dtype, device) -> Optional[int]:
+    """_req of a contiguous tensor (or None), fast where it passes; returns its address (None)."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype and t.device == device and t.is_contiguous()):
+        _req(name, t, shape, dtype, device)
+    return t.data_ptr()
 
 
 def _token_stride(name: str, t: torch.Tensor, shape, dtype, device) -> int:
     """Checks a tensor of tokens whose rows are contiguous but may lie apart; returns the elements between them."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device or t.dtype != dtype or t.shape != shape:
+    if t.shape != shape or t.dtype != dtype or t.device != device:
         _req(name, t, shape, dtype, device)
     st = t.stride()
     if st[-1] == 1 and (len(st) == 2 or st[1] == shape[2]) and shape[0] > 1:
@@ -630,17 +642,26 @@ def _token_stride(name: str, t: torch.Tensor, shape, dtype, device) -> int:
     return st[0] if shape[0] > 1 else -(-width // 8) * 8
 
 
-def _addr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+def _handle(device: torch.device, stream) -> int:
+    """The HIP stream of a call: its stream argument (already current) or the current stream."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _pool_index(n: int, slots, positions, device):
-    _req("slots", slots, (n,), torch.int64, device)
-    _req("positions", positions, (n,), torch.int64, device)
+def _scratch(need: int, workspace: Optional[torch.Tensor], device):
+    """(tensor to keep alive, 256-byte aligned address, bytes) of a call's workspace."""
+    ws = workspace
+    if ws is None:
+        if need == 0:
+            return None, None, 0
+        ws = torch.empty(need + 256, dtype=torch.uint8, device=device)
+    base = ws.data_ptr()
+    off = (-base) % 256
+    return ws, base + off, max(0, ws.numel() * ws.element_size() - off)
 
 
-@_on_device
-@_on_stream
+@_entry
 def ssd_conv_fwd_varlen(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: torch.Tensor,
                         bias: Optional[torch.Tensor] = None, conv_state: Optional[torch.Tensor] = None,
                         slots: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
@@ -665,34 +686,32 @@ def ssd_conv_fwd_varlen(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: torch
     nseq = cu_seqlens.numel() - 1
     K = weight.shape[-1] if weight.dim() == 2 else -1
     xs = _token_stride("x", x, (total, width), iot, dev)
-    _req("weight", weight, (width, K), torch.float32, dev)
-    _req("bias", bias, (width,), torch.float32, dev)
-    _req("cu_seqlens", cu_seqlens, (nseq + 1,), torch.int64, dev)
+    f32, i64 = torch.float32, torch.int64
     nslots = 0
     if conv_state is not None:
         nslots = conv_state.shape[0] if conv_state.dim() == 3 else -1
-        _req("conv_state", conv_state, (nslots, K, width), iot, dev)
         if slots is None or positions is None:
             raise ValueError("conv_state needs slots and positions")
-    _pool_index(nseq, slots, positions, dev)
     u = out if out is not None else torch.empty((total, width), dtype=iot, device=dev)
-    _req("out", u, (total, width), iot, dev)
-    rc = lib.mamba_ssd_conv_fwd_varlen(_addr(x), _addr(weight), _addr(bias), _addr(cu_seqlens), _addr(conv_state),
-                                       _addr(slots), _addr(positions), _addr(u), nseq, total, width, K, xs, nslots, io,
-                                       int(bool(silu)), _stream(dev, stream))
+    rc = lib.mamba_ssd_conv_fwd_varlen(
+        x.data_ptr(), _need("weight", weight, (width, K), f32, dev), _need("bias", bias, (width,), f32, dev),
+        _need("cu_seqlens", cu_seqlens, (nseq + 1,), i64, dev),
+        _need("conv_state", conv_state, (nslots, K, width), iot, dev), _need("slots", slots, (nseq,), i64, dev),
+        _need("positions", positions, (nseq,), i64, dev), _need("out", u, (total, width), iot, dev), nseq, total, width,
+        K, xs, nslots, io, 1 if silu else 0, _handle(dev, stream))
     _check("mamba_ssd_conv_fwd_varlen", rc)
     return u
 
 
-def ssd_fwd_varlen_workspace_size(nseq: int, total_len: int, nheads: int, headdim: int, dstate: int) -> int:
-    n = load_library().mamba_ssd_fwd_varlen_workspace_size(nseq, total_len, nheads, headdim, dstate)
+def ssd_fwd_varlen_workspace_size(nseq: int, total_len: int, nheads: int, headdim: int, dstate: int,
+                                  ngroups: int = 1) -> int:
+    n = load_library().mamba_ssd_fwd_varlen_workspace_size(nseq, total_len, nheads, headdim, dstate, ngroups)
     if n == ctypes.c_size_t(-1).value:
         raise ValueError("mamba_ssd_fwd_varlen_workspace_size: sizes rejected")
     return int(n)
 
 
-@_on_device
-@_on_stream
+@_entry
 def ssd_fwd_varlen(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
                    cu_seqlens: torch.Tensor, D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
                    dt_bias: Optional[torch.Tensor] = None, state: Optional[torch.Tensor] = None,
@@ -724,38 +743,26 @@ def ssd_fwd_varlen(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, B: to
     bs = _token_stride("B", B, (total, G, N), iot, dev)
     cs = _token_stride("C", C, (total, G, N), iot, dev)
     zs = 0 if z is None else _token_stride("z", z, (total, H, P), iot, dev)
-    _req("A_log", A_log, (H,), f32, dev)
-    _req("D", D, (H,), f32, dev)
-    _req("dt_bias", dt_bias, (H,), f32, dev)
-    _req("cu_seqlens", cu_seqlens, (nseq + 1,), torch.int64, dev)
+    i64 = torch.int64
     nslots = 0
     if state is not None:
         nslots = state.shape[0] if state.dim() == 4 else -1
-        _req("state", state, (nslots, H, P, N), f32, dev)
         if slots is None or positions is None:
             raise ValueError("state needs slots and positions")
-    _pool_index(nseq, slots, positions, dev)
     y = out if out is not None else torch.empty((total, H, P), dtype=iot, device=dev)
-    _req("out", y, (total, H, P), iot, dev)
-    need = ssd_fwd_varlen_workspace_size(nseq, total, H, P, N)
-    ws = workspace
-    if ws is None and need > 0:
-        ws = torch.empty(need + 256, dtype=torch.uint8, device=dev)
-    ws_ptr, ws_bytes = None, 0
-    if ws is not None:
-        base = ws.data_ptr()
-        off = (-base) % 256
-        ws_ptr, ws_bytes = base + off, max(0, ws.numel() * ws.element_size() - off)
-    rc = lib.mamba_ssd_fwd_varlen(_addr(x), _addr(dt), _addr(A_log), _addr(B), _addr(C), _addr(D), _addr(z),
-                                  _addr(dt_bias), _addr(cu_seqlens), _addr(state), _addr(slots), _addr(positions),
-                                  _addr(y), nseq, total, H, P, N, G, nslots, xs, ds, bs, cs, zs, io,
-                                  _flags(dt_softplus, discretization), ws_ptr, ws_bytes, _stream(dev, stream))
+    ws, ws_ptr, ws_bytes = _scratch(ssd_fwd_varlen_workspace_size(nseq, total, H, P, N, G), workspace, dev)
+    rc = lib.mamba_ssd_fwd_varlen(
+        x.data_ptr(), dt.data_ptr(), _need("A_log", A_log, (H,), f32, dev), B.data_ptr(), C.data_ptr(),
+        _need("D", D, (H,), f32, dev), None if z is None else z.data_ptr(), _need("dt_bias", dt_bias, (H,), f32, dev),
+        _need("cu_seqlens", cu_seqlens, (nseq + 1,), i64, dev), _need("state", state, (nslots, H, P, N), f32, dev),
+        _need("slots", slots, (nseq,), i64, dev), _need("positions", positions, (nseq,), i64, dev),
+        _need("out", y, (total, H, P), iot, dev), nseq, total, H, P, N, G, nslots, xs, ds, bs, cs, zs, io,
+        _flags(dt_softplus, discretization), ws_ptr, ws_bytes, _handle(dev, stream))
     _check("mamba_ssd_fwd_varlen", rc)
     return y
 
 
-@_on_device
-@_on_stream
+@_entry
 def ssd_step(xbc: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, conv_weight: torch.Tensor,
              conv_state: torch.Tensor, state: torch.Tensor, positions: torch.Tensor,
              slots: Optional[torch.Tensor] = None, D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
@@ -785,24 +792,20 @@ def ssd_step(xbc: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, conv_weig
     xs = _token_stride("xbc", xbc, (batch, width), iot, dev)
     ds = _token_stride("dt", dt, (batch, H), iot, dev)
     zs = 0 if z is None else _token_stride("z", z, (batch, H, P), iot, dev)
-    _req("A_log", A_log, (H,), f32, dev)
-    _req("conv_weight", conv_weight, (width, K), f32, dev)
-    _req("conv_bias", conv_bias, (width,), f32, dev)
-    _req("conv_state", conv_state, (nslots, K, width), iot, dev)
-    _req("state", state, (nslots, H, P, N), f32, dev)
-    _req("D", D, (H,), f32, dev)
-    _req("dt_bias", dt_bias, (H,), f32, dev)
     if slots is None and batch > nslots:
         raise ValueError(f"{batch} rows without slots, but {nslots} pool entries")
     if positions is None:
         raise ValueError("ssd_step needs positions")
-    _pool_index(batch, slots, positions, dev)
     y = out if out is not None else torch.empty((batch, H, P), dtype=iot, device=dev)
-    _req("out", y, (batch, H, P), iot, dev)
-    rc = lib.mamba_ssd_step(_addr(xbc), _addr(dt), _addr(A_log), _addr(conv_weight), _addr(conv_bias), _addr(conv_state),
-                            _addr(state), _addr(slots), _addr(positions), _addr(D), _addr(z), _addr(dt_bias), _addr(y),
-                            batch, H, P, N, G, K, nslots, xs, ds, zs, io, _flags(dt_softplus, discretization),
-                            _stream(dev, stream))
+    i64 = torch.int64
+    rc = lib.mamba_ssd_step(
+        xbc.data_ptr(), dt.data_ptr(), _need("A_log", A_log, (H,), f32, dev),
+        _need("conv_weight", conv_weight, (width, K), f32, dev), _need("conv_bias", conv_bias, (width,), f32, dev),
+        _need("conv_state", conv_state, (nslots, K, width), iot, dev), _need("state", state, (nslots, H, P, N), f32, dev),
+        _need("slots", slots, (batch,), i64, dev), _need("positions", positions, (batch,), i64, dev),
+        _need("D", D, (H,), f32, dev), None if z is None else z.data_ptr(), _need("dt_bias", dt_bias, (H,), f32, dev),
+        _need("out", y, (batch, H, P), iot, dev), batch, H, P, N, G, K, nslots, xs, ds, zs, io,
+        _flags(dt_softplus, discretization), _handle(dev, stream))
     _check("mamba_ssd_step", rc)
     return y
 
@@ -810,8 +813,7 @@ def ssd_step(xbc: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, conv_weig
 _NORM_OUT = {None: 0, "row": 1, "mx": 2}   # MAMBA_NORM_OUT_*
 
 
-@_on_device
-@_on_stream
+@_entry
 def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, *, eps: float = 1e-5,
                  quant: Optional[str] = None, return_rstd: bool = False, out: Optional[torch.Tensor] = None,
                  scales: Optional[torch.Tensor] = None, residual_out: Optional[torch.Tensor] = None, stream=None):
@@ -830,36 +832,37 @@ def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
     if quant not in _NORM_OUT:
         raise ValueError(f"quant must be None, 'row' or 'mx', got {quant!r}")
     io, iot = _io_dtype(x), x.dtype
-    _req("x", x, shape, iot, dev)
-    _req("weight", weight, (dim,), torch.float32, dev)
     rio = io
     ro = residual_out
     if residual is not None:
         rio = _io_dtype(residual)
         if rio != io and rio != F32:
             raise ValueError("residual must have x's dtype or float32")
-        _req("residual", residual, shape, residual.dtype, dev)
+        rt = residual.dtype
         if ro is None:
-            ro = torch.empty(shape, dtype=residual.dtype, device=dev)
-        _req("residual_out", ro, shape, residual.dtype, dev)
+            ro = torch.empty(shape, dtype=rt, device=dev)
     elif ro is not None:
         raise ValueError("residual_out needs residual")
+    if residual is None:
+        rt = iot
     if quant is None:
         if scales is not None:
             raise ValueError("scales needs quant")
-        yt = iot
+        yt = st = iot
+        ss = shape
     else:
         yt = torch.float8_e4m3fn
         st = torch.float32 if quant == "row" else torch.float8_e8m0fnu
         ss = shape[:-1] if quant == "row" else shape[:-1] + ((dim + 31) // 32,)
         if scales is None:
             scales = torch.empty(ss, dtype=st, device=dev)
-        _req("scales", scales, ss, st, dev)
     y = out if out is not None else torch.empty(shape, dtype=yt, device=dev)
-    _req("out", y, shape, yt, dev)
     rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev) if return_rstd else None
-    rc = lib.mamba_rms_norm_fwd(_addr(x), _addr(residual), _addr(weight), eps, _addr(ro), _addr(y), _addr(scales),
-                                _addr(rstd), rows, dim, io, rio, _NORM_OUT[quant], _stream(dev, stream))
+    rc = lib.mamba_rms_norm_fwd(
+        _need("x", x, shape, iot, dev), _need("residual", residual, shape, rt, dev),
+        _need("weight", weight, (dim,), torch.float32, dev), eps, _need("residual_out", ro, shape, rt, dev),
+        _need("out", y, shape, yt, dev), _need("scales", scales, ss, st, dev), None if rstd is None else rstd.data_ptr(),
+        rows, dim, io, rio, _NORM_OUT[quant], _handle(dev, stream))
     _check("mamba_rms_norm_fwd", rc)
     res = [y]
     if quant is not None:
@@ -878,8 +881,7 @@ def rms_norm_bwd_workspace_size(rows: int, dim: int) -> int:
     return int(n)
 
 
-@_on_device
-@_on_stream
+@_entry
 def rms_norm_bwd(dy: torch.Tensor, r: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
                  d_residual: Optional[torch.Tensor] = None, *, workspace: Optional[torch.Tensor] = None,
                  stream=None) -> dict:
@@ -898,26 +900,16 @@ def rms_norm_bwd(dy: torch.Tensor, r: torch.Tensor, weight: torch.Tensor, rstd: 
     rio = _io_dtype(r)
     if rio != io and rio != F32:
         raise ValueError("r must have dy's dtype or float32")
-    _req("dy", dy, shape, iot, dev)
-    _req("r", r, shape, r.dtype, dev)
-    _req("weight", weight, (dim,), torch.float32, dev)
-    _req("rstd", rstd, shape[:-1], torch.float32, dev)
-    _req("d_residual", d_residual, shape, r.dtype, dev)
+    f32, rt = torch.float32, r.dtype
     dx = torch.empty(shape, dtype=iot, device=dev)
     apart = d_residual is not None and rio != io
-    dres = torch.empty(shape, dtype=torch.float32, device=dev) if apart else None
-    dw = torch.empty((dim,), dtype=torch.float32, device=dev)
-    need = rms_norm_bwd_workspace_size(rows, dim)
-    ws = workspace
-    if ws is None and need > 0:
-        ws = torch.empty(need + 256, dtype=torch.uint8, device=dev)
-    ws_ptr, ws_bytes = None, 0
-    if ws is not None:
-        base = ws.data_ptr()
-        off = (-base) % 256
-        ws_ptr, ws_bytes = base + off, max(0, ws.numel() * ws.element_size() - off)
-    rc = lib.mamba_rms_norm_bwd(_addr(dy), _addr(r), _addr(weight), _addr(rstd), _addr(d_residual), _addr(dx),
-                                _addr(dres), _addr(dw), rows, dim, io, rio, ws_ptr, ws_bytes, _stream(dev, stream))
+    dres = torch.empty(shape, dtype=f32, device=dev) if apart else None
+    dw = torch.empty((dim,), dtype=f32, device=dev)
+    ws, ws_ptr, ws_bytes = _scratch(rms_norm_bwd_workspace_size(rows, dim), workspace, dev)
+    rc = lib.mamba_rms_norm_bwd(
+        _need("dy", dy, shape, iot, dev), _need("r", r, shape, rt, dev), _need("weight", weight, (dim,), f32, dev),
+        _need("rstd", rstd, shape[:-1], f32, dev), _need("d_residual", d_residual, shape, rt, dev), dx.data_ptr(),
+        None if dres is None else dres.data_ptr(), dw.data_ptr(), rows, dim, io, rio, ws_ptr, ws_bytes, _handle(dev, stream))
     _check("mamba_rms_norm_bwd", rc)
     g = {"dx": dx, "dweight": dw}
     if d_residual is not None:

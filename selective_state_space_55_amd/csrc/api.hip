@@ -510,16 +510,16 @@ static int check_ssd_varlen_sizes(int64_t nseq, int64_t total_len, int64_t nhead
   if (st != MAMBA_SCAN_OK) return st;
   int64_t t;
   if (nseq > INT32_MAX || !mul_ok(total_len, nheads * headdim, &t) || !mul_ok(t, 4, &t)) return MAMBA_SCAN_ERR_SHAPE;
-  *plan = mscan::make_ssd_varlen_plan(nseq, total_len, nheads, headdim, dstate);
-  // grid: (piece, head, slice of 64 or 32 channels), 256 work-items each
-  if (!mul_ok(plan->pieces, nheads * (headdim / 32), &t) || !launch_ok(t, 256)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  *plan = mscan::make_ssd_varlen_plan(nseq, total_len, nheads, headdim, dstate, ngroups);
+  // grid: (piece, group of heads, four units of 32 channels), 256 work-items each
+  if (!mul_ok(plan->pieces, plan->quads, &t) || !launch_ok(t, 256)) return MAMBA_SCAN_ERR_UNSUPPORTED;
   return MAMBA_SCAN_OK;
 }
 
 size_t mamba_ssd_fwd_varlen_workspace_size(int64_t nseq, int64_t total_len, int64_t nheads, int64_t headdim,
-                                           int64_t dstate) {
+                                           int64_t dstate, int64_t ngroups) {
   mscan::SsdVarlenPlan plan;
-  if (check_ssd_varlen_sizes(nseq, total_len, nheads, headdim, dstate, 1, &plan) != MAMBA_SCAN_OK) return (size_t)-1;
+  if (check_ssd_varlen_sizes(nseq, total_len, nheads, headdim, dstate, ngroups, &plan) != MAMBA_SCAN_OK) return (size_t)-1;
   return plan.ws_total;
 }
 
@@ -624,8 +624,8 @@ static int check_norm(int64_t rows, int64_t dim, int io_dtype, int residual_dtyp
   if (rows < 0 || dim < 1) return MAMBA_SCAN_ERR_SHAPE;
   int64_t t;
   if (!mul_ok(rows + 512, dim + 1, &t) || !mul_ok(t, 4, &t)) return MAMBA_SCAN_ERR_SHAPE;
-  // grids: at most a workgroup per row, a column per work-item
-  if (!launch_ok(rows, 256) || !launch_ok((dim + 63) / 64, 256)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  // grids: at most a workgroup per row; 64 work-items a column
+  if (!launch_ok(rows, 256) || !launch_ok((dim + 15) / 16, 1024)) return MAMBA_SCAN_ERR_UNSUPPORTED;
   return MAMBA_SCAN_OK;
 }
 

@@ -248,11 +248,12 @@ hipError_t launch_ssd_step(const SsdStepArgs& a, hipStream_t stream);
 struct SsdVarlenPlan {
   int64_t piece;       // tokens per piece, a multiple of 64; 0: every sequence is one piece
   int64_t pieces;      // piece numbers (some of them empty), at least nseq
-  size_t off_state;    // (pieces, H, P, N) fp32
-  size_t off_decay;    // (pieces, H) fp32
+  int64_t quads;       // workgroups per piece
+  size_t off_decay;    // workspace: (pieces, H, P, N) fp32 states, then (pieces, H) fp32
   size_t ws_total;
 };
-SsdVarlenPlan make_ssd_varlen_plan(int64_t nseq, int64_t total, int64_t nheads, int64_t headdim, int64_t dstate);
+SsdVarlenPlan make_ssd_varlen_plan(int64_t nseq, int64_t total, int64_t nheads, int64_t headdim, int64_t dstate,
+                                   int64_t ngroups);
 
 struct SsdVarlenArgs {
   const void* x;          // (total, H, P)

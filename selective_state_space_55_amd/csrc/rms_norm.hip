@@ -413,17 +413,24 @@ __global__ __launch_bounds__(kThreads) void dweight_long_kernel(NArgs a) {
   a.part[(int64_t)blockIdx.y * a.dim + c] = s;
 }
 
-// dweight[c] = sum of part[0 .. n)[c]: 64 columns a workgroup, four groups of partial rows
-__global__ __launch_bounds__(kThreads) void dweight_kernel(const float* part, float* dw, int n, int64_t dim) {
-  __shared__ float red[4][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+// dweight[c] = sum of part[0 .. n)[c]: 16 columns a workgroup, 64 threads a column, so that a thread has few
+// loads and all of them are in flight (512 parts x 2048 columns: 4.7 us; with four threads a column 39.7 us)
+__global__ __launch_bounds__(1024) void dweight_kernel(const float* part, float* dw, int n, int64_t dim) {
+  __shared__ float red[64][17];
+  const int col = threadIdx.x & 15, g = threadIdx.x >> 4;
+  const int64_t c = (int64_t)blockIdx.x * 16 + col;
   float s = 0.0f;
-  if (c < dim)
-    for (int k = w; k < n; k += 4) s += part[(int64_t)k * dim + c];
-  red[w][lane] = s;
+  if (c < dim) {
+#pragma unroll 8
+    for (int k = g; k < n; k += 64) s += part[(int64_t)k * dim + c];
+  }
+  red[g][col] = s;
   __syncthreads();
-  if (w == 0 && c < dim) dw[c] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+  for (int h = 32; h; h >>= 1) {
+    if (g < h) red[g][col] += red[g + h][col];
+    __syncthreads();
+  }
+  if (g == 0 && c < dim) dw[c] = red[0][col];
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -500,7 +507,7 @@ hipError_t run_bwd(const NormArgs& p, hipStream_t s) {
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(dweight_kernel, dim3((unsigned)((p.dim + 63) / 64)), dim3(kThreads), 0, s, a.part, p.dweight,
+  hipLaunchKernelGGL(dweight_kernel, dim3((unsigned)((p.dim + 15) / 16)), dim3(1024), 0, s, a.part, p.dweight,
                      (int)parts, p.dim);
   return hipGetLastError();
 }

@@ -13,25 +13,28 @@
 //   Y^T = S_in^T C^T diag(e^cum) + X^T M^T,  M_ij = (C B^T)_ij e^(cum_i - cum_j) w_j (j <= i)
 //   S_out = e^cum_Q S_in + B^T (diag(e^(cum_Q - cum_j) w_j) X)
 //
-// Mapping.  A workgroup of 4 waves owns one (piece of a sequence, head, slice of P
-// = 64 or 32 channels) and walks its chunks.  Every product is a 32x32x16 MFMA on
-// bf16 operands with fp32 accumulation; wave w has output rows p-tile pb = w mod PB
-// and tokens i-tile ib = w / PB, and a part of S (p-tile pb, some of the n-tiles) in
-// its accumulators.  What stays in registers:
-//   C      as the B operand of both C B^T and S^T C^T: a lane's 16-byte pieces of one
-//          token's row, loaded straight from memory
-//   M      C B^T comes out as (B C^T)[j][i], lane = column i, rows j in runs of four; the
-//          order of an MFMA's k index is free as long as both operands agree, so the
-//          masked, decayed tile is the B operand of X^T M^T as it is, and X^T (and B^T and
-//          X in the state update) are read from LDS in that order of tokens
-//   Y      leaves as Y^T: a lane holds four consecutive channels of its token, two lanes
-//          trade halves (v_permlane32_swap), and 16 bytes go out per lane
-// In LDS: the chunk's B and x as loaded, S^T as bf16 hi + lo for the readout (~2^-17), and
-// the decay terms, 65 KB at (N, P) = (128, 64), so that two workgroups share a CU and one's
-// waits overlap the other's work.  The scaled x of the state update is split into three
-// bf16 parts by truncation (8 bits each: exact), so the state keeps fp32's accuracy over a
-// long prompt; e^(cum_Q - cum_j) is taken from the sum of the logs behind j, not from a
-// difference of two long sums.
+// Mapping.  A wave owns a unit of 32 channels of a head: its S (N x 32) stays in the wave's
+// accumulators, and every product is a 32x32x16 MFMA on bf16 operands with fp32 accumulation.
+// A workgroup is four units of one group of heads, which share B, C and B C^T, and a piece of
+// one sequence, whose chunks it walks.  The order of an MFMA's k index is free as long as both
+// operands agree, so what an accumulator holds (lane = column, rows in runs of four) is an operand
+// as it stands, and neither S nor M passes through LDS:
+//   S^T C^T  S (lane = channel, k = state, in accumulator order), split into bf16 hi + lo (~2^-17),
+//            times C, whose LDS rows are stored in that order
+//   M        (B C^T)[j][i], lane = token i, comes from LDS once per workgroup; masked and decayed, it
+//            is the right operand of X^T M^T
+//   X, B     as the operands of X^T M^T and of the state update, by transposing LDS reads in
+//            accumulator order of the tokens; the scaled x is split into three bf16 parts by
+//            truncation (8 bits each: exact), so that the state keeps fp32's accuracy over a long prompt
+//   Y        leaves as Y^T: a lane holds four consecutive channels of its token, two lanes
+//            trade halves (v_permlane32_swap), and 16 bytes go out per lane
+// e^(cum_Q - cum_j) is taken from the sum of the logs behind j, not from a difference of two long
+// sums.  73 KB of LDS at N = 128: two workgroups share a CU.
+//
+// Sequences are cut into pieces that run at once where there are too few sequences and heads to fill
+// the GPU: a first pass forms each piece's own state (from zero) and its decay, a fold turns those
+// into the state that enters each piece (the associative (a, b) operator), and the main pass
+// starts from it.
 #include "internal.h"
 #include "io.h"
 #include "mfma.h"
@@ -56,22 +59,27 @@ struct VArgs {
   const float* dt_bias;
   float* state;
   uint16_t* y;
-  int64_t x_stride, dt_stride, b_stride, c_stride, z_stride;
+  int x_stride, dt_stride, b_stride, c_stride, z_stride;
   int64_t piece;      // tokens per piece, 0: whole sequences
   float* ws_state;    // (pieces, H, P, N): a piece's own state, then the state that enters it
   float* ws_decay;    // (pieces, H): sum of log a over a piece
-  int H, HP, G, S;    // heads, head dim, groups, P-channel slices per head
+  int H, HP, G;       // heads, head dim, groups
+  int nquad;          // workgroups per group of heads
   int softplus, euler;
 };
 
-template <int N, int P>
+constexpr int kWaves = 4;   // units of 32 channels per workgroup
+
+template <int N>
 struct Lds {
-  static constexpr int kRowB = N + 16;                 // pitches that put the transposing reads' rows
-  static constexpr int kRowX = P == 64 ? 96 : 40;      // in different banks
-  static constexpr int kRowS = N + 8;
-  static constexpr int kHalves = kQ * kRowB + kQ * kRowX + 2 * P * kRowS;
-  static constexpr int kTerms = 4 * kQ;                // cum | e^cum | e^(cum_Q - cum) w | w
-  static constexpr size_t bytes() { return 2 * (size_t)kHalves + 4 * (size_t)(2 * kTerms + 4); }
+  static constexpr int kRowB = N + 16;   // pitches that spread the rows of one read over the banks
+  static constexpr int kRowC = N + 8;
+  static constexpr int kRowX = 40;
+  static constexpr int kX = kQ * kRowX;                      // a wave's x tile
+  static constexpr int kTerms = 4 * kQ;                      // a wave's cum | cum - log2 |w| | 2^(cum_Q - cum) w | sign of w
+  static constexpr int kHalves = kQ * kRowB + kQ * kRowC + kWaves * kX;
+  static constexpr int kFloats = 3 * 1024 + kWaves * kTerms;   // the causal tiles of B C^T, the terms
+  static constexpr size_t bytes() { return 2 * (size_t)kHalves + 4 * (size_t)kFloats; }
 };
 
 // k slice s of 16 tokens in the order an accumulator holds its rows: lane half h gets tokens
@@ -96,270 +104,241 @@ __device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
   b = r[1];
 }
 
-template <int N, int P>
-__global__ __launch_bounds__(256, 2) void ssd_varlen_kernel(VArgs a) {
-  using L = Lds<N, P>;
-  constexpr int PB = P / 32;                            // p-tiles
-  constexpr int TPW = (N / 32) * PB >= 4 ? (N / 32) * PB / 4 : 1;   // S tiles per wave
-  constexpr int NS = N / 16;                            // k slices over the states
-  extern __shared__ __align__(16) uint16_t sm[];
-  uint16_t* Bs = sm;
-  uint16_t* Xs = Bs + kQ * L::kRowB;
-  uint16_t* Sh = Xs + kQ * L::kRowX;
-  uint16_t* Sl = Sh + P * L::kRowS;
-  float* terms = reinterpret_cast<float*>(Sl + P * L::kRowS);   // two sets
-  float* atots = terms + 2 * L::kTerms;                         // e^cum_Q of the two sets
-  lds_poison(sm, (int)L::bytes());
+// exp(x) - 1 without cancellation: the series up to x^7 below 1/2, where its rest is under 2^-22 of the
+// result, and the difference above
+__device__ __forceinline__ float expm1_small(float x) {
+  float p = fmaf(x, 1.0f / 5040.0f, 1.0f / 720.0f);
+  p = fmaf(x, p, 1.0f / 120.0f);
+  p = fmaf(x, p, 1.0f / 24.0f);
+  p = fmaf(x, p, 1.0f / 6.0f);
+  p = fmaf(x, p, 0.5f);
+  p = fmaf(x * x, p, x);
+  return fabsf(x) < 0.5f ? p : __expf(x) - 1.0f;
+}
 
+// kAggregate: only the state of a piece that starts from zero, and its decay
+enum Mode { kAggregate, kPlain, kGated };
+// kSigned: the input weight w may be negative (Delta without softplus)
+template <int N, Mode kMode, bool kSigned>
+__global__ __launch_bounds__(256, 2) void ssd_varlen_kernel(VArgs a) {
+  using L = Lds<N>;
+  constexpr bool kAgg = kMode == kAggregate, kGate = kMode == kGated;
+  constexpr int NT = N / 32, NS = N / 16;   // S tiles of a unit, k slices over the states
+  extern __shared__ __align__(16) uint16_t sm[];
   const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h32 = lane >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int HS = a.H * a.S;
-  const int hs = blockIdx.x % HS;
-  const int64_t item = blockIdx.x / HS;
-  const int h = hs / a.S, pslice = (hs % a.S) * P, g = h / (a.H / a.G);
+  uint16_t* Bs = sm;
+  uint16_t* Cs = Bs + kQ * L::kRowB;
+  uint16_t* Xs = Cs + kQ * L::kRowC + w * L::kX;
+  float4* Gs = reinterpret_cast<float4*>(Cs + kQ * L::kRowC + kWaves * L::kX);   // [tile][q][lane]
+  float* cum2 = reinterpret_cast<float*>(Gs) + 3 * 1024 + w * L::kTerms;
+  float* cumw = cum2 + kQ;
+  float* scl = cumw + kQ;
+  uint32_t* sgn = reinterpret_cast<uint32_t*>(scl + kQ);
+  lds_poison(sm, (int)L::bytes());
 
-  // the sequence and its tokens of this workgroup
-  const int64_t s = uniform64(item);
-  const int64_t t_first = seq_offset(a.seq, s), t_end = seq_offset(a.seq, s + 1);
-  if (t_first >= t_end) return;   // a sequence without tokens leaves its slot as it is
-  const int64_t slot = seq_slot(a.seq, s);
-  float* const slot_state = slot < 0 ? nullptr : a.state + ((slot * a.H + h) * a.HP + pslice) * N;
-  const bool started = slot >= 0 && seq_position(a.seq, s) > 0;
+  // the piece, and the wave's unit
+  const int quads = a.G * a.nquad;
+  const int64_t v = uniform64(blockIdx.x / quads);
+  const int gk = blockIdx.x % quads, g = gk / a.nquad;
+  const Packed& q = a.seq;
+  const int64_t piece = a.piece;
+  const int64_t s = uniform64(piece ? last_not_above(q.nseq, v, [&](int64_t i) { return seq_offset(q, i) / piece + i; }) : v);
+  if (s < 0) return;
+  const int64_t start = seq_offset(q, s), stop = seq_offset(q, s + 1);
+  const int64_t k0 = piece ? v - (start / piece + s) : 0;
+  const int64_t t_first = start + k0 * piece;
+  const int64_t t_end = piece ? min(stop, t_first + piece) : stop;
+  if (t_first >= t_end) return;   // no such piece; a sequence without tokens leaves its slot as it is
+  const bool last = t_end == stop, alone = last && k0 == 0;
+  if (kAgg && last) return;       // nothing follows it
   const int64_t nchunk = (t_end - t_first + kQ - 1) / kQ;
 
+  const int tiles = a.HP / 32, upg = (a.H / a.G) * tiles;   // units per head, per group
+  const int ug = (gk % a.nquad) * kWaves + w;
+  const bool live = ug < upg;                               // the group's last workgroup may have fewer
+  const int u = g * upg + (live ? ug : 0);
+  const int h = u / tiles, p0 = (u % tiles) * 32;
+  const int64_t slot = kAgg ? -1 : seq_slot(q, s);
+  const bool started = slot >= 0 && seq_position(q, s) > 0;
+  const int64_t unit_state = ((int64_t)h * a.HP + p0) * N, row_state = (int64_t)a.H * a.HP * N;
+
   const float Ah = -expf(a.A_log[h]);
+  const float A2 = Ah * 1.4426950408889634f, iA = 1.0f / Ah;   // iA is not used where Ah = 0
   const float Dh = a.D ? a.D[h] : 0.0f;
   const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
-  const uint16_t* xg = a.x + (int64_t)h * a.HP + pslice;
-  const uint16_t* zg = a.z ? a.z + (int64_t)h * a.HP + pslice : nullptr;
-  uint16_t* yg = a.y + (int64_t)h * a.HP + pslice;
-  const int64_t y_stride = (int64_t)a.H * a.HP;
+  const int64_t ch = (int64_t)h * a.HP + p0;
   const uint16_t* Bg = a.B + (int64_t)g * N;
   const uint16_t* Cg = a.C + (int64_t)g * N;
+  const int y_stride = a.H * a.HP;
 
-  // Tokens t0 .. t0 + 63 of an array with `stride` elements per token, `width` of which are this
-  // workgroup's: a buffer that ends with the last of them inside the sequence, so that loads past
-  // it give 0 and stores past it are dropped.
-  auto rows = [&](const uint16_t* base, int64_t t0, int64_t stride, int width) {
-    const int64_t left = t_end - t0, n = left < kQ ? left : kQ;
-    const int64_t bytes = left <= 0 ? 0 : ((n - 1) * stride + width) * 2;
-    return make_rsrc(base + (left <= 0 ? 0 : t0 * stride), (int)bytes);
+  // Tokens t0 .. t0 + 63 of an array with `stride` elements per token, `width` of which are read: a
+  // buffer that ends with the last of them inside the piece, so that loads past it give 0 and
+  // stores past it are dropped.
+  auto rows = [&](const uint16_t* base, int64_t t0, int stride, int width) {
+    const int n = (int)min(t_end - t0, (int64_t)kQ);
+    return make_rsrc(base + (n <= 0 ? 0 : t0 * stride), n <= 0 ? 0 : ((n - 1) * stride + width) * 2);
   };
   auto ld16 = [&](__amdgpu_buffer_rsrc_t r, int off) -> uint4 {
     return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
   };
 
-  // staging pieces: B rows of N / 8 16-byte pieces, x rows of P / 8
-  constexpr int kBr = kQ * (N / 8) / 256, kXr = kQ * (P / 8) / 256;
-  static_assert(kBr >= 1 && kXr >= 1, "a piece per thread at least");
-  uint4 bq[kBr], xq[kXr];
+  // a value that the compiler takes as new each time: what is added to it is formed where it is used, not
+  // kept in a register over the loop
+  auto anew = [](int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+  };
+  constexpr int kR = kQ * (N / 8) / 256;   // 16-byte pieces of B (and C) per thread, 256 / (N / 8) rows apart
+  const int bc_row = tid / (N / 8), bc_col = (tid % (N / 8)) * 8;
+  const int b_off = (bc_row * a.b_stride + bc_col) * 2, c_off = (bc_row * a.c_stride + bc_col) * 2;
+  const int x_off = ((lane / 4) * a.x_stride + (lane % 4) * 8) * 2;
+  uint4 bq[kR], cq[kAgg ? 1 : kR], xq[4];
   uint32_t dtq = 0;
-  auto load_tiles = [&](int64_t t0) {
-    const auto rb = rows(Bg, t0, a.b_stride, N), rx = rows(xg, t0, a.x_stride, P);
+  auto load_bc = [&](int64_t t0) {
+    const auto rb = rows(Bg, t0, a.b_stride, N), rc = rows(Cg, t0, a.c_stride, N);
+    const int bo = anew(b_off), co = anew(c_off);
 #pragma unroll
-    for (int r = 0; r < kBr; ++r) {
-      const int e = tid + 256 * r;
-      bq[r] = ld16(rb, ((e / (N / 8)) * (int)a.b_stride + (e % (N / 8)) * 8) * 2);
+    for (int r = 0; r < kR; ++r) {
+      bq[r] = ld16(rb, bo + r * (2048 / N) * a.b_stride * 2);
+      if constexpr (!kAgg) cq[r] = ld16(rc, co + r * (2048 / N) * a.c_stride * 2);
     }
+  };
+  auto load_x = [&](int64_t t0) {
+    const auto rx = rows(a.x + ch, t0, a.x_stride, 32);
+    const int xo = anew(x_off);
 #pragma unroll
-    for (int r = 0; r < kXr; ++r) {
-      const int e = tid + 256 * r;
-      xq[r] = ld16(rx, ((e / (P / 8)) * (int)a.x_stride + (e % (P / 8)) * 8) * 2);
-    }
+    for (int r = 0; r < 4; ++r) xq[r] = ld16(rx, xo + r * 16 * a.x_stride * 2);
+    dtq = __builtin_amdgcn_raw_buffer_load_b16(rows(a.dt + h, t0, a.dt_stride, 1), lane * a.dt_stride * 2, 0, 0);
   };
   auto store_tiles = [&]() {
+    uint16_t* const bo = Bs + anew(bc_row * L::kRowB + bc_col);
+    // states 16 s + {0-3, 8-11 | 4-7, 12-15}: a lane half's eight in one 16-byte read
+    uint16_t* const co = Cs + anew(bc_row * L::kRowC + (bc_col & ~15) + (bc_col & 8) / 2);
 #pragma unroll
-    for (int r = 0; r < kBr; ++r) {
-      const int e = tid + 256 * r;
-      *reinterpret_cast<uint4*>(Bs + (e / (N / 8)) * L::kRowB + (e % (N / 8)) * 8) = bq[r];
-    }
-#pragma unroll
-    for (int r = 0; r < kXr; ++r) {
-      const int e = tid + 256 * r;
-      *reinterpret_cast<uint4*>(Xs + (e / (P / 8)) * L::kRowX + (e % (P / 8)) * 8) = xq[r];
-    }
-  };
-  constexpr int kDtWave = 3;
-  auto load_dt = [&](int64_t t0) {
-    if (w == kDtWave) dtq = __builtin_amdgcn_raw_buffer_load_b16(rows(a.dt + h, t0, a.dt_stride, 1), lane * (int)a.dt_stride * 2, 0, 0);
-  };
-  // one wave turns a chunk's dt into its decay terms; past the end a = 1 and w = 0
-  auto dt_terms = [&](int64_t t0, int set) {
-    if (w != kDtWave) return;
-    const float v = bf(dtq) + bias;
-    float delta = a.softplus ? softplus_log2e(v) * 0.6931471805599453f : v;
-    delta = t0 + lane < t_end ? delta : 0.0f;
-    const float la = delta * Ah;
-    const float wj = a.euler ? delta : Ah != 0.0f ? expm1f(la) / Ah : delta;
-    const float cum = wave_prefix_sum(la);
-    const float rev = wave_prefix_sum(__shfl(la, 63 - lane));   // from the chunk's end
-    const float from = __shfl(rev, 63 - lane);                  // token lane .. the last
-    const float next = __shfl_down(from, 1);                    // every lane takes part
-    const float behind = lane == 63 ? 0.0f : next;              // lane + 1 .. the last
-    float* o = terms + set * L::kTerms;
-    o[lane] = cum;
-    o[kQ + lane] = expf(cum);
-    o[2 * kQ + lane] = expf(behind) * wj;
-    o[3 * kQ + lane] = wj;
-    if (lane == 63) atots[set] = expf(cum);
-  };
-
-  // ---- roles: p-tile pb; the wave's tokens ib of Y, and its n-tiles of S ----
-  const int pb = w % PB, ib = w / PB;
-  const bool has_y = ib < 2;
-  const bool has_s = (w / PB) * TPW < N / 32;
-  const int nb = (w / PB) * TPW;
-  const int i_tok = (ib & 1) * 32 + l32;   // this lane's token of Y^T
-
-  f32x16 S[TPW];
-#pragma unroll
-  for (int k = 0; k < TPW; ++k)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (has_s && started)
-        v = *reinterpret_cast<const float4*>(slot_state + (int64_t)(pb * 32 + l32) * N + (nb + k) * 32 + 8 * q + 4 * h32);
-      S[k][4 * q] = v.x; S[k][4 * q + 1] = v.y; S[k][4 * q + 2] = v.z; S[k][4 * q + 3] = v.w;
-    }
-  // S^T to LDS as hi (truncated) and lo (the rest, rounded)
-  auto write_S = [&]() {
-    if (!has_s) return;
-#pragma unroll
-    for (int k = 0; k < TPW; ++k)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float v0 = S[k][4 * q], v1 = S[k][4 * q + 1], v2 = S[k][4 * q + 2], v3 = S[k][4 * q + 3];
-        const int o = (pb * 32 + l32) * L::kRowS + (nb + k) * 32 + 8 * q + 4 * h32;
-        *reinterpret_cast<uint2*>(Sh + o) = make_uint2(hi16x2(v0, v1), hi16x2(v2, v3));
-        *reinterpret_cast<uint2*>(Sl + o) =
-            make_uint2(pack_bf16x2(v0 - trunc16(v0), v1 - trunc16(v1)), pack_bf16x2(v2 - trunc16(v2), v3 - trunc16(v3)));
+    for (int r = 0; r < kR; ++r) {
+      *reinterpret_cast<uint4*>(bo + r * (2048 / N) * L::kRowB) = bq[r];
+      if constexpr (!kAgg) {
+        *reinterpret_cast<uint2*>(co + r * (2048 / N) * L::kRowC) = make_uint2(cq[r].x, cq[r].y);
+        *reinterpret_cast<uint2*>(co + r * (2048 / N) * L::kRowC + 8) = make_uint2(cq[r].z, cq[r].w);
       }
-  };
-
-  // C of the wave's tokens: slice s is states 16 s + 8 h .. + 7
-  bf16x8 cf[NS];
-  auto load_c = [&](int64_t t0) {
-    if (!has_y) return;
-    const auto rc = rows(Cg, t0, a.c_stride, N);
-    const int off = (i_tok * (int)a.c_stride + 8 * h32) * 2;
+    }
+    uint16_t* const xo = Xs + anew((lane / 4) * L::kRowX + (lane % 4) * 8);
 #pragma unroll
-    for (int k = 0; k < NS; ++k) cf[k] = __builtin_bit_cast(bf16x8, ld16(rc, off + 32 * k));
+    for (int r = 0; r < 4; ++r) *reinterpret_cast<uint4*>(xo + r * 16 * L::kRowX) = xq[r];
+  };
+  // a chunk's decay terms from its dt, one token per lane, in powers of two; past the end a = 1 and
+  // w = 0.  Returns the sum of log2 a.
+  auto decay_terms = [&](int64_t t0) -> float {
+    const float r = bf(dtq) + bias;
+    float delta = a.softplus ? softplus_log2e(r) * 0.6931471805599453f : r;
+    delta = t0 + lane < t_end ? delta : 0.0f;
+    const float la2 = delta * A2;
+    const float wj = a.euler || Ah == 0.0f ? delta : expm1_small(delta * Ah) * iA;
+    const float cum = wave_prefix_sum(la2);
+    const float rev = wave_prefix_sum(__shfl(la2, 63 - lane));   // from the chunk's end
+    const float from = __shfl(rev, 63 - lane);                   // token lane .. the last
+    const float next = __shfl_down(from, 1);                     // every lane takes part
+    const float behind = lane == 63 ? 0.0f : next;               // lane + 1 .. the last
+    scl[lane] = __builtin_amdgcn_exp2f(behind) * wj;
+    if constexpr (!kAgg) {
+      cum2[lane] = cum;
+      cumw[lane] = cum - __builtin_amdgcn_logf(fabsf(wj));   // +inf where w = 0
+      if constexpr (kSigned) sgn[lane] = __float_as_uint(wj) & 0x80000000u;
+    }
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(cum), 63));
   };
 
-  load_tiles(t_first);
-  load_dt(t_first);
-  load_c(t_first);
-  dt_terms(t_first, 0);
-  load_dt(t_first + kQ);
+  f32x16 S[NT];
+  const float* from = kAgg ? nullptr : !alone ? a.ws_state + v * row_state + unit_state
+                    : started ? a.state + slot * row_state + unit_state : nullptr;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (from) f = *reinterpret_cast<const float4*>(from + (int64_t)l32 * N + n * 32 + 8 * k + 4 * h32);
+      S[n][4 * k] = f.x; S[n][4 * k + 1] = f.y; S[n][4 * k + 2] = f.z; S[n][4 * k + 3] = f.w;
+    }
 
+  // rows 8 k + 4 h + {0, 1} and {2, 3} of a diagonal tile that are not behind the lane's column
+  uint32_t causal[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int j = 8 * (k / 2) + 2 * (k & 1) + 4 * h32;
+    causal[k] = (j <= l32 ? 0xffffu : 0u) | (j + 1 <= l32 ? 0xffff0000u : 0u);
+  }
+
+  load_bc(t_first);
+  load_x(t_first);
+  float total = 0.0f;
   for (int64_t c = 0; c < nchunk; ++c) {
     const int64_t t0 = t_first + c * kQ;
-    const int set = (int)(c & 1);
-    const float* cum = terms + set * L::kTerms;
-    const float* ecum = cum + kQ;
-    const float* scl = ecum + kQ;
-    const float* wv = scl + kQ;
+    if (c) lds_barrier();   // every wave has read the previous chunk's B, C and B C^T
     store_tiles();
-    write_S();
+    const float sum = decay_terms(t0);
+    total += sum;
     lds_barrier();
-    // the next chunk's tiles, and this one's gate
-    load_tiles(t0 + kQ);
-    uint4 zq[2] = {};
-    const int yo = (i_tok * (int)y_stride + pb * 32 + 8 * h32) * 2;
-    if (has_y && zg) {
-      const auto rz = rows(zg, t0, a.z_stride, P);
-      const int zo = (i_tok * (int)a.z_stride + pb * 32 + 8 * h32) * 2;
-      zq[0] = ld16(rz, zo);
-      zq[1] = ld16(rz, zo + 32);
-    }
-    dt_terms(t0 + kQ, set ^ 1);
-    load_dt(t0 + 2 * kQ);
-
-    bf16x8 xf[4];
+    load_x(t0 + kQ);
+    if (kAgg) load_bc(t0 + kQ);
+    uint4 zq[2][2];
+    if constexpr (kGate) {
+        const auto rz = rows(a.z + ch, t0, a.z_stride, 32);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) xf[k] = opnd_acc_order(Xs, L::kRowX, k, pb * 32, lane);
-    if (has_y) {
-      // S_in^T C^T, columns scaled by e^cum
-      f32x16 y = {};
-#pragma unroll
-      for (int k = 0; k < NS; ++k) {
-        const int o = (pb * 32 + l32) * L::kRowS + 16 * k + 8 * h32;
-        y = mfma(lds_b8(Sl + o), cf[k], y);
-        y = mfma(lds_b8(Sh + o), cf[k], y);
+        for (int i = 0; i < 2; ++i) {
+          const int zo = (anew(l32) * a.z_stride + 8 * h32 + i * 32 * a.z_stride) * 2;
+          zq[i][0] = ld16(rz, zo);
+          zq[i][1] = ld16(rz, zo + 32);
+        }
       }
-      const float ei = ecum[i_tok], ci = cum[i_tok];
-#pragma unroll
-      for (int r = 0; r < 16; ++r) y[r] *= ei;
-#pragma unroll
-      for (int jb = 0; jb < 2; ++jb) {
-        if (jb > ib) break;
+
+    f32x16 y[2] = {};
+    if constexpr (!kAgg) {
+      // (B C^T) tiles (j, i) = (0, 0), (0, 1), (1, 1), one wave each
+      if (w < 3) {
+        const uint16_t* br = Bs + ((w == 2) * 32 + l32) * L::kRowB + 4 * h32;
+        const uint16_t* cr = Cs + ((w > 0) * 32 + l32) * L::kRowC + 8 * h32;
         f32x16 m = {};
 #pragma unroll
-        for (int k = 0; k < NS; ++k) m = mfma(lds_b8(Bs + (jb * 32 + l32) * L::kRowB + 16 * k + 8 * h32), cf[k], m);
-        uint32_t mw[8];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int j0 = jb * 32 + 8 * q + 4 * h32;
-          const float4 cj = *reinterpret_cast<const float4*>(cum + j0);
-          const float4 wj = *reinterpret_cast<const float4*>(wv + j0);
-          const float cja[4] = {cj.x, cj.y, cj.z, cj.w}, wja[4] = {wj.x, wj.y, wj.z, wj.w};
-          float v[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            // exp(-200) is 0 in fp32: the tokens behind i
-            const float d = jb < ib || j0 + r <= i_tok ? ci - cja[r] : -200.0f;
-            v[r] = m[4 * q + r] * __expf(d) * wja[r];
-          }
-          mw[2 * q] = pack_bf16x2(v[0], v[1]);
-          mw[2 * q + 1] = pack_bf16x2(v[2], v[3]);
+        for (int k = 0; k < NS; ++k) {
+          const uint2 b0 = *reinterpret_cast<const uint2*>(br + 16 * k), b1 = *reinterpret_cast<const uint2*>(br + 16 * k + 8);
+          m = mfma(__builtin_bit_cast(bf16x8, make_uint4(b0.x, b0.y, b1.x, b1.y)), lds_b8(cr + 16 * k), m);
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          y = mfma(xf[2 * jb + k], __builtin_bit_cast(bf16x8, make_uint4(mw[4 * k], mw[4 * k + 1], mw[4 * k + 2], mw[4 * k + 3])), y);
+        for (int k = 0; k < 4; ++k) Gs[(w * 4 + k) * 64 + lane] = make_float4(m[4 * k], m[4 * k + 1], m[4 * k + 2], m[4 * k + 3]);
       }
-      // + D x, gate, and out: channels 8 q + 4 h .. + 3 of the lane's token
-      uint32_t zw[8];
-      const uint32_t zr[8] = {zq[0].x, zq[0].y, zq[0].z, zq[0].w, zq[1].x, zq[1].y, zq[1].z, zq[1].w};
+      if (live) {
+        // S_in^T C^T over both token tiles
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < NS; ++k) {
+          uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint32_t lo = zr[4 * k + j], up = zr[4 * k + 2 + j];
-          swap32(lo, up);
-          zw[4 * k + j] = lo;
-          zw[4 * k + 2 + j] = up;
-        }
-      uint32_t o[8];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint2 xv = *reinterpret_cast<const uint2*>(Xs + i_tok * L::kRowX + pb * 32 + 8 * q + 4 * h32);
-        const uint32_t xw[2] = {xv.x, xv.y};
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float v0 = fmaf(Dh, bf16_lo(xw[j]), y[4 * q + 2 * j]), v1 = fmaf(Dh, bf16_hi(xw[j]), y[4 * q + 2 * j + 1]);
-          if (zg) {
-            v0 *= silu(bf16_lo(zw[2 * q + j]));
-            v1 *= silu(bf16_hi(zw[2 * q + j]));
+          for (int j = 0; j < 4; ++j) {
+            const float v0 = S[k / 2][8 * (k & 1) + 2 * j], v1 = S[k / 2][8 * (k & 1) + 2 * j + 1];
+            hi[j] = hi16x2(v0, v1);
+            lo[j] = pack_bf16x2(v0 - trunc16(v0), v1 - trunc16(v1));
           }
-          o[2 * q + j] = pack_bf16x2(v0, v1);
+          const bf16x8 sh = __builtin_bit_cast(bf16x8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+          const bf16x8 sl = __builtin_bit_cast(bf16x8, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+          const bf16x8 c0 = lds_b8(Cs + l32 * L::kRowC + 16 * k + 8 * h32);
+          const bf16x8 c1 = lds_b8(Cs + (32 + l32) * L::kRowC + 16 * k + 8 * h32);
+          y[0] = mfma(sl, c0, y[0]);
+          y[1] = mfma(sl, c1, y[1]);
+          y[0] = mfma(sh, c0, y[0]);
+          y[1] = mfma(sh, c1, y[1]);
         }
-      }
-      const auto ry = rows(yg, t0, y_stride, P);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        swap32(o[4 * k], o[4 * k + 2]);
-        swap32(o[4 * k + 1], o[4 * k + 3]);
-        typedef __attribute__((ext_vector_type(4))) unsigned u32x4;
-        __builtin_amdgcn_raw_buffer_store_b128(u32x4{o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]}, ry, yo + 32 * k, 0, 0);
       }
     }
-    load_c(t0 + kQ);
-    if (has_s) {
-      const float at = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(atots[set])));
+    __builtin_amdgcn_sched_barrier(0);   // the phases' registers do not fit side by side
+    bf16x8 xf[4];
+    if (live) {
 #pragma unroll
-      for (int k = 0; k < TPW; ++k)
+      for (int k = 0; k < 4; ++k) xf[k] = opnd_acc_order(Xs, L::kRowX, k, 0, lane);
+      const float at = __builtin_amdgcn_exp2f(sum);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) S[k][r] *= at;
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) S[n][r] *= at;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float4 s0 = *reinterpret_cast<const float4*>(scl + 16 * k + 4 * h32);
@@ -379,43 +358,186 @@ __global__ __launch_bounds__(256, 2) void ssd_varlen_kernel(VArgs a) {
         const bf16x8 xh = __builtin_bit_cast(bf16x8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
         const bf16x8 xm = __builtin_bit_cast(bf16x8, make_uint4(mid[0], mid[1], mid[2], mid[3]));
         const bf16x8 xl = __builtin_bit_cast(bf16x8, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        bf16x8 bt[NT];
 #pragma unroll
-        for (int n = 0; n < TPW; ++n) {
-          const bf16x8 bt = opnd_acc_order(Bs, L::kRowB, k, (nb + n) * 32, lane);
-          S[n] = mfma(bt, xl, S[n]);
-          S[n] = mfma(bt, xm, S[n]);
-          S[n] = mfma(bt, xh, S[n]);
+        for (int n = 0; n < NT; ++n) bt[n] = opnd_acc_order(Bs, L::kRowB, k, n * 32, lane);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) S[n] = mfma(bt[n], xl, S[n]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) S[n] = mfma(bt[n], xm, S[n]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) S[n] = mfma(bt[n], xh, S[n]);
+      }
+    }
+    if constexpr (!kAgg) {
+      __builtin_amdgcn_sched_barrier(0);
+      load_bc(t0 + kQ);
+      lds_barrier();   // B C^T
+      if (!live) continue;
+      const auto ry = rows(a.y + ch, t0, y_stride, 32);
+      const uint16_t* const xrow = Xs + anew(l32 * L::kRowX + 4 * h32);
+      const float4* const gl = Gs + anew(lane);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int tok = i * 32 + l32;
+        const float ci = cum2[tok], ei = __builtin_amdgcn_exp2f(ci);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) y[i][r] *= ei;
+#pragma unroll
+        for (int jb = 0; jb <= i; ++jb) {
+          uint32_t mw[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int j0 = jb * 32 + 8 * k + 4 * h32;
+            const float4 gv = gl[((i + jb) * 4 + k) * 64];
+            const float4 cj = *reinterpret_cast<const float4*>(cumw + j0);
+            const float ga[4] = {gv.x, gv.y, gv.z, gv.w}, cja[4] = {cj.x, cj.y, cj.z, cj.w};
+            float f[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) f[r] = ga[r] * __builtin_amdgcn_exp2f(ci - cja[r]);
+            if constexpr (kSigned) {
+              const uint4 sj = *reinterpret_cast<const uint4*>(sgn + j0);
+              const uint32_t sa[4] = {sj.x, sj.y, sj.z, sj.w};
+#pragma unroll
+              for (int r = 0; r < 4; ++r) f[r] = __uint_as_float(__float_as_uint(f[r]) ^ sa[r]);
+            }
+            // on the diagonal: tokens behind i, whose bits may be anything, become 0
+            mw[2 * k] = pack_bf16x2(f[0], f[1]) & (jb == i ? causal[2 * k] : ~0u);
+            mw[2 * k + 1] = pack_bf16x2(f[2], f[3]) & (jb == i ? causal[2 * k + 1] : ~0u);
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            y[i] = mfma(xf[2 * jb + k], __builtin_bit_cast(bf16x8, make_uint4(mw[4 * k], mw[4 * k + 1], mw[4 * k + 2], mw[4 * k + 3])), y[i]);
+        }
+        // + D x, gate, and out: channels 8 k + 4 h .. + 3 of the lane's token
+        uint32_t zw[8] = {zq[i][0].x, zq[i][0].y, zq[i][0].z, zq[i][0].w, zq[i][1].x, zq[i][1].y, zq[i][1].z, zq[i][1].w};
+        if constexpr (kGate) {
+          swap32(zw[0], zw[2]);
+          swap32(zw[1], zw[3]);
+          swap32(zw[4], zw[6]);
+          swap32(zw[5], zw[7]);
+        }
+        uint32_t o[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint2 xv = *reinterpret_cast<const uint2*>(xrow + i * 32 * L::kRowX + 8 * k);
+          const uint32_t xw[2] = {xv.x, xv.y};
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float v0 = fmaf(Dh, bf16_lo(xw[j]), y[i][4 * k + 2 * j]), v1 = fmaf(Dh, bf16_hi(xw[j]), y[i][4 * k + 2 * j + 1]);
+            if constexpr (kGate) {
+              v0 *= silu(bf16_lo(zw[2 * k + j]));
+              v1 *= silu(bf16_hi(zw[2 * k + j]));
+            }
+            o[2 * k + j] = pack_bf16x2(v0, v1);
+          }
+        }
+        const int yo = (anew(l32) * y_stride + 8 * h32 + i * 32 * y_stride) * 2;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          swap32(o[4 * k], o[4 * k + 2]);
+          swap32(o[4 * k + 1], o[4 * k + 3]);
+          typedef __attribute__((ext_vector_type(4))) unsigned u32x4;
+          __builtin_amdgcn_raw_buffer_store_b128(u32x4{o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]}, ry, yo + 32 * k, 0, 0);
         }
       }
     }
-    lds_barrier();   // the tiles, S and the terms of this chunk have been read
   }
 
-  if (slot_state && has_s) {
+  if (!live) return;
+  float* to = kAgg ? a.ws_state + v * row_state + unit_state
+            : last && slot >= 0 ? a.state + slot * row_state + unit_state : nullptr;
+  if (kAgg && lane == 0 && p0 == 0) a.ws_decay[v * a.H + h] = total;
+  if (!to) return;
 #pragma unroll
-    for (int k = 0; k < TPW; ++k)
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<float4*>(slot_state + (int64_t)(pb * 32 + l32) * N + (nb + k) * 32 + 8 * q + 4 * h32) =
-            make_float4(S[k][4 * q], S[k][4 * q + 1], S[k][4 * q + 2], S[k][4 * q + 3]);
+    for (int k = 0; k < 4; ++k)
+      *reinterpret_cast<float4*>(to + (int64_t)l32 * N + n * 32 + 8 * k + 4 * h32) =
+          make_float4(S[n][4 * k], S[n][4 * k + 1], S[n][4 * k + 2], S[n][4 * k + 3]);
+}
+
+// The fold over a sequence's pieces: entry k of its part of ws_state, piece k's own state, becomes the
+// state that enters piece k.  A thread per sequence and four states.
+__global__ __launch_bounds__(256) void ssd_fold_kernel(VArgs a, int N) {
+  const Packed& q = a.seq;
+  const int64_t row_state = (int64_t)a.H * a.HP * N;
+  const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (e >= row_state) return;
+  const int h = (int)(e / ((int64_t)a.HP * N));
+  for (int64_t s = blockIdx.y; s < q.nseq; s += gridDim.y) {
+    const int64_t start = seq_offset(q, s), len = seq_offset(q, s + 1) - start;
+    if (len <= a.piece) continue;   // one piece (or none): it starts from its slot
+    const int64_t slot = seq_slot(q, s), v0 = start / a.piece + s, n = (len + a.piece - 1) / a.piece;
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (slot >= 0 && seq_position(q, s) > 0) f = *reinterpret_cast<const float4*>(a.state + slot * row_state + e);
+    float4* ws = reinterpret_cast<float4*>(a.ws_state + v0 * row_state + e);
+    const int64_t step = row_state / 4;
+    const float* decay = a.ws_decay + v0 * a.H + h;
+    // the last piece has no state of its own
+    float4 next = ws[0];
+    float d = decay[0];
+    for (int64_t k = 0; k < n; ++k) {
+      const float4 own = next;
+      const float at = exp2f(d);
+      if (k + 2 < n) {
+        next = ws[(k + 1) * step];
+        d = decay[(k + 1) * a.H];
+      }
+      ws[k * step] = f;
+      f.x = fmaf(at, f.x, own.x);
+      f.y = fmaf(at, f.y, own.y);
+      f.z = fmaf(at, f.z, own.z);
+      f.w = fmaf(at, f.w, own.w);
+    }
   }
 }
 
-template <int N, int P>
-hipError_t run(VArgs a, const SsdVarlenPlan& p, hipStream_t s) {
-  a.S = a.HP / P;
-  const size_t lds = Lds<N, P>::bytes();
-  hipError_t e = hipFuncSetAttribute((const void*)ssd_varlen_kernel<N, P>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+template <int N, Mode kMode, bool kSigned>
+hipError_t launch(const VArgs& a, dim3 grid, hipStream_t s) {
+  const size_t lds = Lds<N>::bytes();
+  hipError_t e = hipFuncSetAttribute((const void*)ssd_varlen_kernel<N, kMode, kSigned>,
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((ssd_varlen_kernel<N, P>), dim3((unsigned)(p.pieces * a.H * a.S)), dim3(256), lds, s, a);
+  hipLaunchKernelGGL((ssd_varlen_kernel<N, kMode, kSigned>), grid, dim3(256), lds, s, a);
   return hipGetLastError();
 }
 
+template <int N>
+hipError_t run(const VArgs& a, const SsdVarlenPlan& p, hipStream_t s) {
+  const dim3 grid((unsigned)(p.pieces * p.quads));
+  if (p.piece) {
+    hipError_t e = launch<N, kAggregate, true>(a, grid, s);
+    if (e != hipSuccess) return e;
+    const int64_t blocks = ((int64_t)a.H * a.HP * N / 4 + 255) / 256;
+    hipLaunchKernelGGL(ssd_fold_kernel, dim3((unsigned)blocks, (unsigned)std::min<int64_t>(65535, a.seq.nseq)), dim3(256), 0, s, a, N);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (a.softplus) return a.z ? launch<N, kGated, false>(a, grid, s) : launch<N, kPlain, false>(a, grid, s);
+  return a.z ? launch<N, kGated, true>(a, grid, s) : launch<N, kPlain, true>(a, grid, s);
+}
+
+// workgroups of a group's units
+int64_t quads_of(int64_t nheads, int64_t headdim, int64_t ngroups) { return (nheads / ngroups * (headdim / 32) + kWaves - 1) / kWaves; }
+
 }  // namespace
 
-SsdVarlenPlan make_ssd_varlen_plan(int64_t nseq, int64_t total, int64_t nheads, int64_t headdim, int64_t dstate) {
+SsdVarlenPlan make_ssd_varlen_plan(int64_t nseq, int64_t total, int64_t nheads, int64_t headdim, int64_t dstate,
+                                   int64_t ngroups) {
   SsdVarlenPlan p{};
-  p.pieces = nseq;
+  p.quads = quads_of(nheads, headdim, ngroups) * ngroups;
+  // two rounds of two workgroups per CU, pieces of 256 tokens at least
+  const int64_t want = std::max<int64_t>(256, (total * p.quads / 1024 + kQ - 1) / kQ * kQ);
+  if (want < total) {
+    p.piece = want;
+    p.pieces = total / want + nseq;   // piece numbers end below that
+    const size_t state = (size_t)p.pieces * nheads * headdim * dstate * 4;
+    p.off_decay = (state + 255) / 256 * 256;
+    p.ws_total = p.off_decay + ((size_t)p.pieces * nheads * 4 + 255) / 256 * 256;
+  } else {
+    p.pieces = nseq;
+  }
   return p;
 }
 
@@ -426,11 +548,16 @@ hipError_t launch_ssd_varlen(const SsdVarlenArgs& p, const SsdVarlenPlan& plan, 
   a.x = static_cast<const uint16_t*>(p.x); a.dt = static_cast<const uint16_t*>(p.dt); a.A_log = p.A_log;
   a.B = static_cast<const uint16_t*>(p.B); a.C = static_cast<const uint16_t*>(p.C); a.D = p.D;
   a.z = static_cast<const uint16_t*>(p.z); a.dt_bias = p.dt_bias; a.state = p.state; a.y = static_cast<uint16_t*>(p.y);
-  a.x_stride = p.x_stride; a.dt_stride = p.dt_stride; a.b_stride = p.b_stride; a.c_stride = p.c_stride; a.z_stride = p.z_stride;
+  a.x_stride = (int)p.x_stride; a.dt_stride = (int)p.dt_stride; a.b_stride = (int)p.b_stride;
+  a.c_stride = (int)p.c_stride; a.z_stride = (int)p.z_stride;
   a.H = (int)p.nheads; a.HP = (int)p.headdim; a.G = (int)p.ngroups; a.softplus = p.softplus; a.euler = p.euler;
-  const bool p32 = p.headdim % 64 != 0;
-  if (p.dstate == 128) return p32 ? run<128, 32>(a, plan, stream) : run<128, 64>(a, plan, stream);
-  return p32 ? run<64, 32>(a, plan, stream) : run<64, 64>(a, plan, stream);
+  a.nquad = (int)(plan.quads / p.ngroups);
+  a.piece = plan.piece;
+  if (plan.piece) {
+    a.ws_state = static_cast<float*>(p.workspace);
+    a.ws_decay = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + plan.off_decay);
+  }
+  return p.dstate == 128 ? run<128>(a, plan, stream) : run<64>(a, plan, stream);
 }
 
 }  // namespace mscan

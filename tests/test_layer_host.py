@@ -71,9 +71,10 @@ def test_ssd_refusals(lib, bad, code):
 
 def test_ssd_workspace(lib):
     f = lib.mamba_ssd_fwd_varlen_workspace_size
-    assert f(0, 10, 4, 64, 128) == BAD and f(1, 10, 4, 48, 128) == BAD and f(1, 10, 4, 64, 32) == BAD
+    assert f(0, 10, 4, 64, 128, 1) == BAD and f(1, 10, 4, 48, 128, 1) == BAD and f(1, 10, 4, 64, 32, 1) == BAD
+    assert f(1, 10, 4, 64, 128, 3) == BAD
     # where a workspace is needed, one that is missing, short or badly aligned is refused
-    need = f(1, 1 << 20, 4, 64, 128)
+    need = f(1, 1 << 20, 4, 64, 128, 1)
     assert need != BAD
     if need:
         big = dict(nseq=1, total=1 << 20)
