@@ -419,6 +419,8 @@ int mamba_ssd_conv_fwd_varlen(const void* x, const float* weight, const float* b
  *   B, C       (total_len, ngroups, dstate)  bf16
  *   A_log, D, dt_bias (nheads)               f32    D, dt_bias may be NULL
  *   state      (nslots, nheads, headdim, dstate) f32   IN/OUT; NULL with slots and positions NULL
+ *   max_len    the longest sequence's length where the host knows it, else 0: long sequences are cut into
+ *              pieces that run at once, which short ones do without.  Only speed depends on it
  *   workspace  at least mamba_ssd_fwd_varlen_workspace_size(...) bytes, 256-byte aligned; contents on
  *              entry ignored, on exit undefined (may be NULL where that size is 0)
  * Supported: io_dtype MAMBA_SCAN_BF16, headdim a multiple of 32 up to 256, dstate 64 or 128, ngroups a
@@ -429,13 +431,13 @@ int mamba_ssd_conv_fwd_varlen(const void* x, const float* weight, const float* b
 int mamba_ssd_fwd_varlen(const void* x, const void* dt, const float* A_log, const void* B, const void* C,
                          const float* D, const void* z, const float* dt_bias, const int64_t* cu_seqlens, float* state,
                          const int64_t* slots, const int64_t* positions, void* y, int64_t nseq, int64_t total_len,
-                         int64_t nheads, int64_t headdim, int64_t dstate, int64_t ngroups, int64_t nslots,
-                         int64_t x_stride, int64_t dt_stride, int64_t B_stride, int64_t C_stride, int64_t z_stride,
+                         int64_t nheads, int64_t headdim, int64_t dstate, int64_t ngroups, int64_t max_len,
+                         int64_t nslots, int64_t x_stride, int64_t dt_stride, int64_t B_stride, int64_t C_stride, int64_t z_stride,
                          int io_dtype, int flags, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace mamba_ssd_fwd_varlen needs (may be 0); (size_t)-1 for rejected sizes. */
 size_t mamba_ssd_fwd_varlen_workspace_size(int64_t nseq, int64_t total_len, int64_t nheads, int64_t headdim,
-                                           int64_t dstate, int64_t ngroups);
+                                           int64_t dstate, int64_t ngroups, int64_t max_len);
 
 /*
  * One token per request through the layer's core: the convolution of mamba_ssd_conv_fwd_varlen (with

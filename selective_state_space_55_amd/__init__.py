@@ -91,9 +91,9 @@ def load_library():
     lib.mamba_ssd_conv_fwd_varlen.restype = I
     lib.mamba_ssd_conv_fwd_varlen.argtypes = [P] * 8 + [I64] * 6 + [I, I, P]
     lib.mamba_ssd_fwd_varlen.restype = I
-    lib.mamba_ssd_fwd_varlen.argtypes = [P] * 13 + [I64] * 12 + [I, I, P, SZ, P]
+    lib.mamba_ssd_fwd_varlen.argtypes = [P] * 13 + [I64] * 13 + [I, I, P, SZ, P]
     lib.mamba_ssd_fwd_varlen_workspace_size.restype = SZ
-    lib.mamba_ssd_fwd_varlen_workspace_size.argtypes = [I64] * 6
+    lib.mamba_ssd_fwd_varlen_workspace_size.argtypes = [I64] * 7
     lib.mamba_ssd_step.restype = I
     lib.mamba_ssd_step.argtypes = [P] * 13 + [I64] * 10 + [I, I, P]
     lib.mamba_rms_norm_fwd.restype = I
@@ -642,10 +642,18 @@ def _token_stride(name: str, t: torch.Tensor, shape, dtype, device) -> int:
     return st[0] if shape[0] > 1 else -(-width // 8) * 8
 
 
+def _current_handle(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the same without the Stream object, where torch has it (0.1 against 1.9 us a call)
+_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", _current_handle)
+
+
 def _handle(device: torch.device, stream) -> int:
     """The HIP stream of a call: its stream argument (already current) or the current stream."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        return _current_handle(device.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -704,8 +712,8 @@ def ssd_conv_fwd_varlen(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: torch
 
 
 def ssd_fwd_varlen_workspace_size(nseq: int, total_len: int, nheads: int, headdim: int, dstate: int,
-                                  ngroups: int = 1) -> int:
-    n = load_library().mamba_ssd_fwd_varlen_workspace_size(nseq, total_len, nheads, headdim, dstate, ngroups)
+                                  ngroups: int = 1, max_seqlen: int = 0) -> int:
+    n = load_library().mamba_ssd_fwd_varlen_workspace_size(nseq, total_len, nheads, headdim, dstate, ngroups, max_seqlen)
     if n == ctypes.c_size_t(-1).value:
         raise ValueError("mamba_ssd_fwd_varlen_workspace_size: sizes rejected")
     return int(n)
@@ -716,12 +724,13 @@ def ssd_fwd_varlen(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, B: to
                    cu_seqlens: torch.Tensor, D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
                    dt_bias: Optional[torch.Tensor] = None, state: Optional[torch.Tensor] = None,
                    slots: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
-                   dt_softplus: bool = True, *, out: Optional[torch.Tensor] = None,
+                   dt_softplus: bool = True, *, max_seqlen: int = 0, out: Optional[torch.Tensor] = None,
                    workspace: Optional[torch.Tensor] = None, discretization: str = "zoh", stream=None) -> torch.Tensor:
     """ssd_fwd over packed sequences.  x, z (total, H, P), dt (total, H), B, C (total, G, N) in bfloat16, heads in
     G groups that share B and C; tokens may lie apart (slices of a wider row), each contiguous; x, B, C and
     z 16-byte aligned.  cu_seqlens (nseq + 1,) int64 on the device.  state (nslots, H, P, N) float32 is
-    updated IN PLACE by slot, as conv_state in ssd_conv_fwd_varlen.  Returns y (total, H, P); rows outside every
+    updated IN PLACE by slot, as conv_state in ssd_conv_fwd_varlen.  max_seqlen, the longest sequence's length where
+    the host knows it, only serves the choice of launches.  Returns y (total, H, P); rows outside every
     sequence are not written."""
     lib = load_library()
     if x.dim() != 3:
@@ -750,13 +759,14 @@ def ssd_fwd_varlen(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, B: to
         if slots is None or positions is None:
             raise ValueError("state needs slots and positions")
     y = out if out is not None else torch.empty((total, H, P), dtype=iot, device=dev)
-    ws, ws_ptr, ws_bytes = _scratch(ssd_fwd_varlen_workspace_size(nseq, total, H, P, N, G), workspace, dev)
+    ws, ws_ptr, ws_bytes = _scratch(ssd_fwd_varlen_workspace_size(nseq, total, H, P, N, G, max_seqlen), workspace, dev)
     rc = lib.mamba_ssd_fwd_varlen(
         x.data_ptr(), dt.data_ptr(), _need("A_log", A_log, (H,), f32, dev), B.data_ptr(), C.data_ptr(),
         _need("D", D, (H,), f32, dev), None if z is None else z.data_ptr(), _need("dt_bias", dt_bias, (H,), f32, dev),
         _need("cu_seqlens", cu_seqlens, (nseq + 1,), i64, dev), _need("state", state, (nslots, H, P, N), f32, dev),
         _need("slots", slots, (nseq,), i64, dev), _need("positions", positions, (nseq,), i64, dev),
-        _need("out", y, (total, H, P), iot, dev), nseq, total, H, P, N, G, nslots, xs, ds, bs, cs, zs, io,
+        _need("out", y, (total, H, P), iot, dev), nseq, total, H, P, N, G, max_seqlen, nslots,
+        xs, ds, bs, cs, zs, io,
         _flags(dt_softplus, discretization), ws_ptr, ws_bytes, _handle(dev, stream))
     _check("mamba_ssd_fwd_varlen", rc)
     return y
@@ -840,7 +850,7 @@ def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
             raise ValueError("residual must have x's dtype or float32")
         rt = residual.dtype
         if ro is None:
-            ro = torch.empty(shape, dtype=rt, device=dev)
+            ro = torch.empty_like(residual)
     elif ro is not None:
         raise ValueError("residual_out needs residual")
     if residual is None:
@@ -856,7 +866,7 @@ def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
         ss = shape[:-1] if quant == "row" else shape[:-1] + ((dim + 31) // 32,)
         if scales is None:
             scales = torch.empty(ss, dtype=st, device=dev)
-    y = out if out is not None else torch.empty(shape, dtype=yt, device=dev)
+    y = out if out is not None else torch.empty_like(x) if quant is None else torch.empty(shape, dtype=yt, device=dev)
     rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev) if return_rstd else None
     rc = lib.mamba_rms_norm_fwd(
         _need("x", x, shape, iot, dev), _need("residual", residual, shape, rt, dev),
@@ -901,10 +911,10 @@ def rms_norm_bwd(dy: torch.Tensor, r: torch.Tensor, weight: torch.Tensor, rstd: 
     if rio != io and rio != F32:
         raise ValueError("r must have dy's dtype or float32")
     f32, rt = torch.float32, r.dtype
-    dx = torch.empty(shape, dtype=iot, device=dev)
+    dx = torch.empty_like(dy)
     apart = d_residual is not None and rio != io
-    dres = torch.empty(shape, dtype=f32, device=dev) if apart else None
-    dw = torch.empty((dim,), dtype=f32, device=dev)
+    dres = torch.empty_like(d_residual) if apart else None
+    dw = torch.empty_like(weight)
     ws, ws_ptr, ws_bytes = _scratch(rms_norm_bwd_workspace_size(rows, dim), workspace, dev)
     rc = lib.mamba_rms_norm_bwd(
         _need("dy", dy, shape, iot, dev), _need("r", r, shape, rt, dev), _need("weight", weight, (dim,), f32, dev),

@@ -504,35 +504,36 @@ int mamba_ssd_conv_fwd_varlen(const void* x, const float* weight, const float* b
 }
 
 static int check_ssd_varlen_sizes(int64_t nseq, int64_t total_len, int64_t nheads, int64_t headdim, int64_t dstate,
-                                  int64_t ngroups, mscan::SsdVarlenPlan* plan) {
-  if (nseq < 1 || total_len < 0) return MAMBA_SCAN_ERR_SHAPE;
+                                  int64_t ngroups, int64_t max_len, mscan::SsdVarlenPlan* plan) {
+  if (nseq < 1 || total_len < 0 || max_len < 0) return MAMBA_SCAN_ERR_SHAPE;
   int st = check_ssd_heads(nheads, headdim, dstate, ngroups);
   if (st != MAMBA_SCAN_OK) return st;
   int64_t t;
-  if (nseq > INT32_MAX || !mul_ok(total_len, nheads * headdim, &t) || !mul_ok(t, 4, &t)) return MAMBA_SCAN_ERR_SHAPE;
-  *plan = mscan::make_ssd_varlen_plan(nseq, total_len, nheads, headdim, dstate, ngroups);
+  if (nseq > INT32_MAX || !mul_ok(total_len, nheads * headdim, &t) || !mul_ok(t, 4, &t) || t > ((int64_t)1 << 61))
+    return MAMBA_SCAN_ERR_SHAPE;
+  *plan = mscan::make_ssd_varlen_plan(nseq, total_len, nheads, headdim, dstate, ngroups, max_len);
   // grid: (piece, group of heads, four units of 32 channels), 256 work-items each
   if (!mul_ok(plan->pieces, plan->quads, &t) || !launch_ok(t, 256)) return MAMBA_SCAN_ERR_UNSUPPORTED;
   return MAMBA_SCAN_OK;
 }
 
 size_t mamba_ssd_fwd_varlen_workspace_size(int64_t nseq, int64_t total_len, int64_t nheads, int64_t headdim,
-                                           int64_t dstate, int64_t ngroups) {
+                                           int64_t dstate, int64_t ngroups, int64_t max_len) {
   mscan::SsdVarlenPlan plan;
-  if (check_ssd_varlen_sizes(nseq, total_len, nheads, headdim, dstate, ngroups, &plan) != MAMBA_SCAN_OK) return (size_t)-1;
+  if (check_ssd_varlen_sizes(nseq, total_len, nheads, headdim, dstate, ngroups, max_len, &plan) != MAMBA_SCAN_OK) return (size_t)-1;
   return plan.ws_total;
 }
 
 int mamba_ssd_fwd_varlen(const void* x, const void* dt, const float* A_log, const void* B, const void* C,
                          const float* D, const void* z, const float* dt_bias, const int64_t* cu_seqlens, float* state,
                          const int64_t* slots, const int64_t* positions, void* y, int64_t nseq, int64_t total_len,
-                         int64_t nheads, int64_t headdim, int64_t dstate, int64_t ngroups, int64_t nslots,
-                         int64_t x_stride, int64_t dt_stride, int64_t B_stride, int64_t C_stride, int64_t z_stride,
+                         int64_t nheads, int64_t headdim, int64_t dstate, int64_t ngroups, int64_t max_len,
+                         int64_t nslots, int64_t x_stride, int64_t dt_stride, int64_t B_stride, int64_t C_stride, int64_t z_stride,
                          int io_dtype, int flags, void* workspace, size_t workspace_bytes, void* stream) {
   if (io_dtype != MAMBA_SCAN_F32 && io_dtype != MAMBA_SCAN_BF16) return MAMBA_SCAN_ERR_DTYPE;
   if (io_dtype != MAMBA_SCAN_BF16) return MAMBA_SCAN_ERR_UNSUPPORTED;   // bf16 operands only
   mscan::SsdVarlenPlan plan;
-  int st = check_ssd_varlen_sizes(nseq, total_len, nheads, headdim, dstate, ngroups, &plan);
+  int st = check_ssd_varlen_sizes(nseq, total_len, nheads, headdim, dstate, ngroups, max_len, &plan);
   if (st != MAMBA_SCAN_OK) return st;
   if (flags & ~(MAMBA_SCAN_FLAG_SOFTPLUS | MAMBA_SCAN_FLAG_EULER)) return MAMBA_SCAN_ERR_UNSUPPORTED;
   int64_t t;

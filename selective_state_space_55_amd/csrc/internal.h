@@ -246,14 +246,16 @@ hipError_t launch_ssd_step(const SsdStepArgs& a, hipStream_t stream);
 
 // Multi-head SSM over packed sequences with a state per slot (ssd_varlen.hip), bf16 io.
 struct SsdVarlenPlan {
-  int64_t piece;       // tokens per piece, a multiple of 64; 0: every sequence is one piece
-  int64_t pieces;      // piece numbers (some of them empty), at least nseq
+  int shift;           // pieces of 2^shift tokens, at least 64
+  bool cut;            // a sequence may have more than one piece: two more passes and a workspace
+  int64_t pieces;      // piece numbers (some of them name no piece)
   int64_t quads;       // workgroups per piece
   size_t off_decay;    // workspace: (pieces, H, P, N) fp32 states, then (pieces, H) fp32
   size_t ws_total;
 };
+// longest: a bound of the sequences' lengths, 0: unknown
 SsdVarlenPlan make_ssd_varlen_plan(int64_t nseq, int64_t total, int64_t nheads, int64_t headdim, int64_t dstate,
-                                   int64_t ngroups);
+                                   int64_t ngroups, int64_t longest);
 
 struct SsdVarlenArgs {
   const void* x;          // (total, H, P)

@@ -24,29 +24,51 @@ __device__ __forceinline__ int64_t seq_offset(const Packed& p, int64_t s) {
   return v < 0 ? 0 : v > p.total ? p.total : v;
 }
 
-// The last s in [0, nseq) with key(s) <= target, -1 if there is none; keys do
-// not fall.  Whole wave, target uniform: a wave looks at 64 keys at a time.
-template <typename Key>
-__device__ __forceinline__ int64_t last_not_above(int64_t nseq, int64_t target, Key key) {
-  const int lane = threadIdx.x & 63;
-  int64_t lo = 0, n = nseq;
-  while (n > 64) {
-    const int64_t step = (n + 63) / 64;
-    const int64_t i = lo + lane * step;
-    const int c = __popcll(__ballot(lane * step < n && key(i) <= target));
-    if (c == 0) return -1;
-    const int64_t off = (c - 1) * step;
-    lo += off;
-    n = min(step, n - off);
-  }
-  const int c = __popcll(__ballot(lane < n && key(lo + lane) <= target));
-  return c == 0 ? -1 : lo + c - 1;
-}
-
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
   const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
   return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
+// v of one lane (uniform) of the wave
+__device__ __forceinline__ int64_t lane64(int64_t v, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)((uint64_t)v >> 32), lane);
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
+// A run of 2^shift tokens of a sequence, numbered (cu[s] >> shift) + s + k for run k of sequence s: the
+// numbers of one sequence's runs end before the next one's begin, so that a wave finds its run without
+// a prefix sum over the lengths.  Some numbers (at most nseq) name no run.
+struct Run {
+  int64_t s;            // sequence, -1: no run has this number
+  int64_t start, stop;  // its tokens
+  int64_t k;            // the run's number in it
+};
+
+// number is uniform; whole waves.  Looks at 64 offsets at a time.
+__device__ __forceinline__ Run find_run(const Packed& p, int64_t number, int shift) {
+  const int lane = threadIdx.x & 63;
+  int64_t lo = 0, n = p.nseq;
+  while (n > 63) {
+    const int64_t step = (n + 62) / 63, i = lo + lane * step;
+    const bool in = lane * step < n && (seq_offset(p, i) >> shift) + i <= number;
+    const int c = __popcll(__ballot(in));
+    if (c == 0) return Run{-1, 0, 0, 0};
+    lo += (c - 1) * step;
+    n = min(step, n - (c - 1) * step);
+  }
+  // offsets lo .. lo + n, the last of them where the last sequence stops
+  const int64_t v = seq_offset(p, lo + min((int64_t)lane, n));
+  const int c = __popcll(__ballot(lane < n && (v >> shift) + lo + lane <= number));
+  if (c == 0) return Run{-1, 0, 0, 0};
+  Run r;
+  r.s = lo + c - 1;
+  r.start = lane64(v, c - 1);
+  r.stop = lane64(v, c);
+  r.k = number - ((r.start >> shift) + r.s);
+  if (r.k < 0 || r.start + (r.k << shift) >= r.stop) r.s = -1;   // (k < 0 only where offsets fall)
+  return r;
 }
 
 // the slot of sequence s, -1 if it has none

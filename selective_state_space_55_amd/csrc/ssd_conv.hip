@@ -14,7 +14,7 @@
 // up to kRun tokens of one sequence, a lane W channels of it (8: one 16-byte
 // access, or 1 where rows are not 16-byte aligned), so its K - 1 previous inputs
 // stay in registers.  Runs are counted from each sequence's start (run k of
-// sequence s has number cu[s] / kRun + s + k, of which some are empty), so only a
+// sequence s has number cu[s] / kRun + s + k; see packed.h), so only a
 // sequence's first run looks at the ring: it reads the rows behind it and then
 // writes the new ones, and no other wave has to be waited for.
 #include "internal.h"
@@ -26,7 +26,7 @@
 namespace mscan {
 namespace {
 
-constexpr int kRun = 8;   // tokens a thread walks
+constexpr int kRunShift = 3, kRun = 1 << kRunShift;   // tokens a wave walks
 
 struct CArgs {
   Packed seq;
@@ -51,12 +51,9 @@ template <typename IoT, int W, int K>
 __global__ __launch_bounds__(256) void ssd_conv_kernel(CArgs a) {
   const int lane = threadIdx.x & 63;
   const Packed& q = a.seq;
-  const int64_t run = uniform64((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6));
-  const int64_t s = uniform64(last_not_above(q.nseq, run, [&](int64_t i) { return seq_offset(q, i) / kRun + i; }));
-  if (s < 0) return;   // whole waves
-  const int64_t start = seq_offset(q, s), end = seq_offset(q, s + 1);
-  const int64_t k0 = run - (start / kRun + s), t0 = start + k0 * kRun;
-  if (t0 >= end) return;
+  const Run r = find_run(q, uniform64((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)), kRunShift);
+  if (r.s < 0) return;   // whole waves
+  const int64_t s = r.s, start = r.start, end = r.stop, k0 = r.k, t0 = start + k0 * kRun;
   const int64_t c = ((int64_t)blockIdx.y * 64 + lane) * W;
   if (c >= a.width) return;
   const IoT* x = static_cast<const IoT*>(a.x) + c;

@@ -184,6 +184,7 @@ def test_norm_residual_in_place_and_shapes():
 # ---------------------------------------------------------------- packed convolution
 
 LENS = [[1], [5], [1, 1, 1], [3, 0, 2, 64], [0, 7, 8, 9, 0], [16, 17, 1, 2, 3, 130], [2] * 70, [300]]
+MANY = [1, 0, 2] * 1400   # more sequences than two levels of 63 look through
 
 
 def packed(lens):
@@ -212,6 +213,18 @@ def test_conv(lens, width, K, gap, io):
     u = mscan.ssd_conv_fwd_varlen(apart(x, gap), dev(w), dev(i64(cu)), bias=dev(b), conv_state=rd, slots=dev(slots),
                                   positions=dev(pos))
     close("u", u, u64, HALF[io] * u64.abs() + F32 * size)
+    assert torch.equal(rd.cpu().double(), ring64)
+
+
+def test_conv_many_sequences():
+    r = Rng(4)
+    n, cu = len(MANY), packed(MANY)
+    x, w = r(cu[-1], 8), r(8, 4)
+    ring, slots, pos = r(n, 4, 8), r.slots(n, n), i64([i % 5 for i in range(n)])
+    u64, ring64 = layer.conv_varlen(x, w, cu, None, ring, slots, pos)
+    rd = dev(ring.clone())
+    u = mscan.ssd_conv_fwd_varlen(dev(x), dev(w), dev(i64(cu)), conv_state=rd, slots=dev(slots), positions=dev(pos))
+    close("u", u, u64, 2.0 ** -24 * u64.abs() + F32 * 4 * x.abs().max() * w.abs().max())
     assert torch.equal(rd.cpu().double(), ring64)
 
 
@@ -336,6 +349,42 @@ def test_ssd_rows_outside_are_left():
     assert torch.equal(out[90:].cpu(), torch.full((10, 2, 64), 3.0).bfloat16())
     ref = layer.ssd_varlen(c["x"], c["dt"], c["A_log"], c["B"], c["C"], [10, 40, 90])
     check_ssd([50], out, None, ref)
+
+
+def test_ssd_max_seqlen_is_only_a_hint():
+    """Told that sequences are short (or shorter than they are), nothing is cut; the results are those of whole
+    sequences, within the tolerance of either."""
+    r = Rng(16)
+    lens = [200, 70, 1]
+    c = ssd_case(r, lens, 2, 64, 128, 1)
+    state, slots, pos = r(4, 2, 64, 128), i64([3, 0, 1]), i64([7, 0, 2])
+    got = []
+    for hint in (0, 200, 64, 1):
+        y, sd, ref = run_ssd(c, lens, state, slots, pos, True, True, False, max_seqlen=hint)
+        check_ssd(lens, y, sd, ref)
+        got.append((y, sd))
+    assert torch.equal(got[2][0], got[3][0]) and torch.equal(got[2][1], got[3][1])
+
+
+def test_ssd_many_sequences():
+    r = Rng(14)
+    lens = MANY[:300]
+    c = ssd_case(r, lens, 1, 32, 64, 1)
+    slots, pos = r.slots(300, 302), i64([i % 3 for i in range(300)])
+    y, sd, ref = run_ssd(c, lens, r(302, 1, 32, 64), slots, pos, True, True, False)
+    check_ssd(lens, y, sd, ref)
+
+
+def test_ssd_bad_offsets_stay_in_bounds():
+    """Offsets that are no offsets give some numbers, within the arrays, and other slots stay as they are."""
+    r = Rng(15)
+    c = {k: v.to(DEV) for k, v in ssd_case(r, [700], 2, 64, 64, 1).items()}
+    for cu in ([-7, 300, 9999], [500, 100, 600], [1 << 40, -(1 << 40), 5], [690, 3, 690]):
+        state = torch.full((3, 2, 64, 64), 2.0, device=DEV)
+        mscan.ssd_fwd_varlen(c["x"], c["dt"], c["A_log"], c["B"], c["C"], dev(i64(cu)), state=state, slots=dev(i64([0, 7])),
+                             positions=dev(i64([0, 0])))
+        torch.cuda.synchronize()
+        assert torch.equal(state[1:].cpu(), torch.full((2, 2, 64, 64), 2.0))
 
 
 def test_ssd_equals_the_fixed_length_forward():

@@ -48,15 +48,15 @@ def test_conv_refusals(lib, bad, code):
 
 
 def ssd(lib, x=P, dt=P, A=P, B=P, C=P, D=None, z=None, bias=None, cu=P, state=P, slots=P, pos=P, y=P, nseq=2, total=100,
-        H=4, hd=64, N=128, G=1, nslots=4, xs=256, ds=4, bs=128, cs=128, zs=256, io=1, flags=1, ws=P, wsb=1 << 40):
-    return lib.mamba_ssd_fwd_varlen(x, dt, A, B, C, D, z, bias, cu, state, slots, pos, y, nseq, total, H, hd, N, G, nslots,
+        H=4, hd=64, N=128, G=1, ml=0, nslots=4, xs=256, ds=4, bs=128, cs=128, zs=256, io=1, flags=1, ws=P, wsb=1 << 40):
+    return lib.mamba_ssd_fwd_varlen(x, dt, A, B, C, D, z, bias, cu, state, slots, pos, y, nseq, total, H, hd, N, G, ml, nslots,
                                     xs, ds, bs, cs, zs, io, flags, ws, wsb, None)
 
 
 @pytest.mark.parametrize("bad,code", [
     (dict(x=None), ENULL), (dict(dt=None), ENULL), (dict(A=None), ENULL), (dict(B=None), ENULL), (dict(y=None), ENULL),
     (dict(cu=None), ENULL), (dict(slots=None), ENULL), (dict(pos=None), ENULL), (dict(state=None), ENULL),
-    (dict(nseq=0), ESHAPE), (dict(total=-1), ESHAPE), (dict(H=0), ESHAPE), (dict(G=0), ESHAPE), (dict(nslots=-1), ESHAPE),
+    (dict(nseq=0), ESHAPE), (dict(total=-1), ESHAPE), (dict(H=0), ESHAPE), (dict(G=0), ESHAPE), (dict(nslots=-1), ESHAPE), (dict(ml=-1), ESHAPE),
     (dict(xs=248), ESHAPE), (dict(ds=3), ESHAPE), (dict(bs=120), ESHAPE), (dict(z=P, zs=0), ESHAPE),
     (dict(G=3), EUNSUP), (dict(hd=48, xs=192), EUNSUP), (dict(hd=288, xs=1152), EUNSUP), (dict(N=96), EUNSUP),
     (dict(io=0), EUNSUP), (dict(flags=4), EUNSUP), (dict(xs=(1 << 24) + 8), EUNSUP), (dict(nseq=1 << 30), EUNSUP),
@@ -71,11 +71,12 @@ def test_ssd_refusals(lib, bad, code):
 
 def test_ssd_workspace(lib):
     f = lib.mamba_ssd_fwd_varlen_workspace_size
-    assert f(0, 10, 4, 64, 128, 1) == BAD and f(1, 10, 4, 48, 128, 1) == BAD and f(1, 10, 4, 64, 32, 1) == BAD
-    assert f(1, 10, 4, 64, 128, 3) == BAD
+    assert f(0, 10, 4, 64, 128, 1, 0) == BAD and f(1, 10, 4, 48, 128, 1, 0) == BAD and f(1, 10, 4, 64, 32, 1, 0) == BAD
+    assert f(1, 10, 4, 64, 128, 3, 0) == BAD and f(1, 10, 4, 64, 128, 1, -1) == BAD
     # where a workspace is needed, one that is missing, short or badly aligned is refused
-    need = f(1, 1 << 20, 4, 64, 128, 1)
-    assert need != BAD
+    need = f(1, 1 << 20, 4, 64, 128, 1, 0)
+    assert 0 < need < BAD
+    assert f(1, 1 << 20, 4, 64, 128, 1, 64) == 0   # known to be short: not cut
     if need:
         big = dict(nseq=1, total=1 << 20)
         assert ssd(lib, ws=None, **big) == EWS
