@@ -481,7 +481,7 @@ int mamba_ssd_step(const void* xbc, const void* dt, const float* A_log, const fl
  *                             scale.  Row scale: largest magnitude / 448; block scale: the smallest power of two
  *                             that keeps the block's magnitudes within 448; 1 where all values are 0
  *   rstd         (rows)       f32             OUT, NULL: not written
- * Sizes: rows >= 0, dim >= 1; the launch's work-items (at most rows * 256) below 2^32.  A row with a NaN or an
+ * Sizes: rows >= 0, dim >= 1; the launch's work-items (at most rows * 1024) below 2^32.  A row with a NaN or an
  * Inf has NaNs in y.
  */
 int mamba_rms_norm_fwd(const void* x, const void* residual, const float* weight, float eps, void* residual_out,

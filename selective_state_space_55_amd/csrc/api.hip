@@ -480,7 +480,7 @@ int mamba_ssd_conv_fwd_varlen(const void* x, const float* weight, const float* b
   int64_t t;
   if (!mul_ok(nslots, width, &t) || !mul_ok(t, 16, &t) || !mul_ok(nseq, 32, &t)) return MAMBA_SCAN_ERR_SHAPE;
   // grid: runs of tokens x groups of (at least) 64 channels
-  if (!launch_ok((mscan::ssd_conv_runs(nseq, total_len) + 3) / 4, 256) || (width + 63) / 64 > 65535)
+  if (!mul_ok((mscan::ssd_conv_runs(nseq, total_len) + 3) / 4, (width + 63) / 64, &t) || !launch_ok(t, 256))
     return MAMBA_SCAN_ERR_UNSUPPORTED;
   if (!weight || !cu_seqlens || !pool_args_ok(conv_state, slots, positions)) return MAMBA_SCAN_ERR_NULL;
   if (total_len > 0 && (!x || !u)) return MAMBA_SCAN_ERR_NULL;
@@ -624,9 +624,9 @@ static int check_norm(int64_t rows, int64_t dim, int io_dtype, int residual_dtyp
   if (residual_dtype != io_dtype && residual_dtype != MAMBA_SCAN_F32) return MAMBA_SCAN_ERR_DTYPE;
   if (rows < 0 || dim < 1) return MAMBA_SCAN_ERR_SHAPE;
   int64_t t;
-  if (!mul_ok(rows + 512, dim + 1, &t) || !mul_ok(t, 4, &t)) return MAMBA_SCAN_ERR_SHAPE;
+  if (!mul_ok(rows + 1024, dim + 1, &t) || !mul_ok(t, 4, &t)) return MAMBA_SCAN_ERR_SHAPE;
   // grids: at most a workgroup per row; 64 work-items a column
-  if (!launch_ok(rows, 256) || !launch_ok((dim + 15) / 16, 1024)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  if (!launch_ok(rows, 1024) || !launch_ok((dim + 15) / 16, 1024)) return MAMBA_SCAN_ERR_UNSUPPORTED;
   return MAMBA_SCAN_OK;
 }
 

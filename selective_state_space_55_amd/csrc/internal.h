@@ -200,7 +200,7 @@ struct NormArgs {
   void* workspace;
 };
 
-int64_t norm_bwd_parts(int64_t rows);   // workgroups whose partial dweight (dim fp32) the workspace holds
+int64_t norm_bwd_parts(int64_t rows);   // workgroups, at most, whose partial dweight (dim fp32) the workspace holds
 hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t stream);
 hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t stream);
 

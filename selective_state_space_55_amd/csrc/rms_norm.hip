@@ -27,6 +27,7 @@ namespace mscan {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int threads_of(int T) { return T > kThreads ? T : kThreads; }   // of a workgroup, with T lanes per row
 constexpr float kFp8Max = 448.0f;
 
 struct NArgs {
@@ -67,14 +68,16 @@ __device__ __forceinline__ float wave_max(float v) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
-// over the T lanes of a row; red: one float per wave (T = 256), each call its own
+// over the T lanes of a row, T a wave or a whole workgroup; red: T / 64 floats, each call its own
 template <int T, bool kMax>
 __device__ __forceinline__ float row_reduce(float v, float* red) {
   v = kMax ? wave_max(v) : wave_sum(v);
-  if constexpr (T == kThreads) {
+  if constexpr (T > 64) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
-    v = kMax ? fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])) : (red[0] + red[1]) + (red[2] + red[3]);
+    v = red[0];
+#pragma unroll
+    for (int i = 1; i < T / 64; ++i) v = kMax ? fmaxf(v, red[i]) : v + red[i];
   }
   return v;
 }
@@ -110,6 +113,23 @@ __device__ __forceinline__ void store_w(void* p, int64_t i, const float (&f)[W])
     Io<T>::store1(q, f[0]);
 }
 
+// load_w for data that the kernel reads once and no one soon after: 32768 rows of 2560 take 117 us with
+// these loads and 127 with plain ones (the gradient, whose stores are larger, 210 against 202)
+template <typename T, int W>
+__device__ __forceinline__ void load_once(const void* p, int64_t i, float (&f)[W]) {
+  if constexpr (W == 8) {
+    typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+    const u32x4* q = reinterpret_cast<const u32x4*>(static_cast<const T*>(p) + i);
+    if constexpr (sizeof(T) == 2)
+      Io<T>::to_f32(__builtin_bit_cast(typename Io<T>::V8, __builtin_nontemporal_load(q)), f);
+    else
+      Io<T>::to_f32(typename Io<T>::V8{__builtin_bit_cast(float4, __builtin_nontemporal_load(q)),
+                                       __builtin_bit_cast(float4, __builtin_nontemporal_load(q + 1))}, f);
+  } else {
+    load_w<T, W>(p, i, f);
+  }
+}
+
 template <int W>
 __device__ __forceinline__ void store_fp8(void* p, int64_t i, const float (&f)[W]) {
   uint8_t* q = static_cast<uint8_t*>(p) + i;
@@ -135,18 +155,18 @@ __device__ __forceinline__ int block_exp(float top) {
 }
 
 template <typename IoT, int W, int T, int V>
-__global__ __launch_bounds__(kThreads) void rms_norm_fwd_kernel(NArgs a) {
-  __shared__ float red[8];
-  const int64_t row = (int64_t)blockIdx.x * (kThreads / T) + threadIdx.x / T;
+__global__ __launch_bounds__(threads_of(T)) void rms_norm_fwd_kernel(NArgs a) {
+  __shared__ float red[2][16];
+  const int64_t row = (int64_t)blockIdx.x * (threads_of(T) / T) + threadIdx.x / T;
   const int t = threadIdx.x % T;
-  if (row >= a.rows) return;   // whole waves (T = 64) or no workgroup at all (T = 256)
+  if (row >= a.rows) return;   // whole waves (T = 64) or no workgroup at all
   const int64_t base = row * a.dim;
   const int nvec = (int)(a.dim / W);
   float r[V][W];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     if (v * T + t < nvec) {
-      load_w<IoT, W>(a.x, base + (int64_t)(v * T + t) * W, r[v]);
+      load_once<IoT, W>(a.x, base + (int64_t)(v * T + t) * W, r[v]);
     } else {
 #pragma unroll
       for (int j = 0; j < W; ++j) r[v][j] = 0.0f;
@@ -161,9 +181,9 @@ __global__ __launch_bounds__(kThreads) void rms_norm_fwd_kernel(NArgs a) {
       for (int j = 0; j < W; ++j) s[v][j] = 0.0f;
       if (v * T + t < nvec) {
         if (a.res_f32)
-          load_w<float, W>(a.res, i, s[v]);
+          load_once<float, W>(a.res, i, s[v]);
         else
-          load_w<IoT, W>(a.res, i, s[v]);
+          load_once<IoT, W>(a.res, i, s[v]);
       }
     }
 #pragma unroll
@@ -184,7 +204,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_fwd_kernel(NArgs a) {
   for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int j = 0; j < W; ++j) ss = fmaf(r[v][j], r[v][j], ss);
-  ss = row_reduce<T, false>(ss, red);
+  ss = row_reduce<T, false>(ss, red[0]);
   const float rstd = 1.0f / sqrtf(ss / (float)a.dim + a.eps);
   if (a.rstd && t == 0) a.rstd[row] = rstd;
   float top = 0.0f;
@@ -216,13 +236,17 @@ __global__ __launch_bounds__(kThreads) void rms_norm_fwd_kernel(NArgs a) {
     }
   }
   if (a.out == kNormRow8) {
-    const float s = row_scale(row_reduce<T, true>(top, red + 4));
+    const float s = row_scale(row_reduce<T, true>(top, red[1]));
+    const float inv = 1.0f / s;
     if (t == 0) static_cast<float*>(a.scales)[row] = s;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (v * T + t >= nvec) continue;
 #pragma unroll
-      for (int j = 0; j < W; ++j) r[v][j] /= s;
+      for (int j = 0; j < W; ++j) {
+        const float q = r[v][j] * inv;
+        r[v][j] = fmaf(fmaf(-q, s, r[v][j]), inv, q);   // r / s, correctly rounded but for rare last bits
+      }
       store_fp8<W>(a.y, base + (int64_t)(v * T + t) * W, r[v]);
     }
   }
@@ -287,9 +311,9 @@ __global__ __launch_bounds__(kThreads) void rms_norm_fwd_long_kernel(NArgs a) {
 // them at a time) and keeps its columns' dweight sums in registers; the partial sums of the
 // workgroups are added up by dweight_kernel in a fixed order.
 template <typename IoT, int W, int T, int V>
-__global__ __launch_bounds__(kThreads) void rms_norm_bwd_kernel(NArgs a) {
-  constexpr int kR = kThreads / T;   // rows at a time
-  __shared__ float red[2][4];
+__global__ __launch_bounds__(threads_of(T)) void rms_norm_bwd_kernel(NArgs a) {
+  constexpr int kR = threads_of(T) / T;   // rows at a time
+  __shared__ float red[2][16];
   __shared__ float sum[T == 64 ? V * 64 * W : 1];
   const int t = threadIdx.x % T;
   const int nvec = (int)(a.dim / W);
@@ -435,37 +459,49 @@ __global__ __launch_bounds__(1024) void dweight_kernel(const float* part, float*
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// the shapes a row is run in; 0: the long-row kernels
-enum { kLong, kWave1, kWave2, kWave4, kWave8, kGroup4, kGroup8, kOddWave, kOddGroup8, kOddGroup32 };
+// The shapes a row is run in.  Aligned rows: a wave per row while it holds the row in a few registers, then a
+// workgroup (forward, 16384 rows of 4096: 159 us against 171 with a wave of 8 accesses; gradient, which holds
+// three rows' worth: 200 against 242, and at 2560 130 against 159 with 5 accesses).  Rows off 16-byte alignment go
+// element by element, at most 8 per lane (8192 rows of 5001, forward: 149 us; with up to 32 per lane 323).
+enum { kLong, kWave1, kWave2, kWave3, kWave4, kWave5, kGroup2, kGroup4, kGroup8, kOddWave, kOddGroup, kOddGroup2, kOddGroup4 };
 
-int row_shape(int64_t dim, bool vec) {
+int row_shape(int64_t dim, bool vec, bool backward) {
   if (vec) {
     if (dim <= 512) return kWave1;
     if (dim <= 1024) return kWave2;
+    if (dim <= 1536) return kWave3;
     if (dim <= 2048) return kWave4;
-    if (dim <= 4096) return kWave8;
+    if (dim <= 2560 && !backward) return kWave5;
+    if (dim <= 4096) return kGroup2;
     if (dim <= 8192) return kGroup4;
     return dim <= 16384 ? kGroup8 : kLong;
   }
   if (dim <= 512) return kOddWave;
-  if (dim <= 2048) return kOddGroup8;
-  return dim <= 8192 ? kOddGroup32 : kLong;
+  if (dim <= 2048) return kOddGroup;
+  if (dim <= 4096) return kOddGroup2;
+  return dim <= 8192 ? kOddGroup4 : kLong;
 }
 
-int rows_at_a_time(int shape) { return (shape >= kWave1 && shape <= kWave8) || shape == kOddWave ? 4 : 1; }
+bool wave_per_row(int shape) { return (shape >= kWave1 && shape <= kWave5) || shape == kOddWave; }
 
-#define MSCAN_NORM_SHAPES(KERNEL, GRID)                                                                       \
-  switch (shape) {                                                                                            \
-    case kWave1: hipLaunchKernelGGL((KERNEL<IoT, 8, 64, 1>), GRID, dim3(kThreads), 0, s, a); break;           \
-    case kWave2: hipLaunchKernelGGL((KERNEL<IoT, 8, 64, 2>), GRID, dim3(kThreads), 0, s, a); break;           \
-    case kWave4: hipLaunchKernelGGL((KERNEL<IoT, 8, 64, 4>), GRID, dim3(kThreads), 0, s, a); break;           \
-    case kWave8: hipLaunchKernelGGL((KERNEL<IoT, 8, 64, 8>), GRID, dim3(kThreads), 0, s, a); break;           \
-    case kGroup4: hipLaunchKernelGGL((KERNEL<IoT, 8, 256, 4>), GRID, dim3(kThreads), 0, s, a); break;         \
-    case kGroup8: hipLaunchKernelGGL((KERNEL<IoT, 8, 256, 8>), GRID, dim3(kThreads), 0, s, a); break;         \
-    case kOddWave: hipLaunchKernelGGL((KERNEL<IoT, 1, 64, 8>), GRID, dim3(kThreads), 0, s, a); break;         \
-    case kOddGroup8: hipLaunchKernelGGL((KERNEL<IoT, 1, 256, 8>), GRID, dim3(kThreads), 0, s, a); break;      \
-    case kOddGroup32: hipLaunchKernelGGL((KERNEL<IoT, 1, 256, 32>), GRID, dim3(kThreads), 0, s, a); break;    \
-    default: return hipErrorInvalidValue;                                                                     \
+#define MSCAN_NORM_SHAPE(SHAPE, KERNEL, GRID, W, T, V)                                                     \
+  case SHAPE:                                                                                              \
+    hipLaunchKernelGGL((KERNEL<IoT, W, T, V>), GRID, dim3(threads_of(T)), 0, s, a);                        \
+    break;
+#define MSCAN_NORM_SHAPES(KERNEL, GRID)                 \
+  switch (shape) {                                      \
+    MSCAN_NORM_SHAPE(kWave1, KERNEL, GRID, 8, 64, 1)    \
+    MSCAN_NORM_SHAPE(kWave2, KERNEL, GRID, 8, 64, 2)    \
+    MSCAN_NORM_SHAPE(kWave3, KERNEL, GRID, 8, 64, 3)    \
+    MSCAN_NORM_SHAPE(kWave4, KERNEL, GRID, 8, 64, 4)    \
+    MSCAN_NORM_SHAPE(kGroup2, KERNEL, GRID, 8, 256, 2)  \
+    MSCAN_NORM_SHAPE(kGroup4, KERNEL, GRID, 8, 256, 4)  \
+    MSCAN_NORM_SHAPE(kGroup8, KERNEL, GRID, 8, 256, 8)  \
+    MSCAN_NORM_SHAPE(kOddWave, KERNEL, GRID, 1, 64, 8)  \
+    MSCAN_NORM_SHAPE(kOddGroup, KERNEL, GRID, 1, 256, 8)   \
+    MSCAN_NORM_SHAPE(kOddGroup2, KERNEL, GRID, 1, 512, 8)  \
+    MSCAN_NORM_SHAPE(kOddGroup4, KERNEL, GRID, 1, 1024, 8) \
+    default: return hipErrorInvalidValue;               \
   }
 
 template <typename IoT>
@@ -475,14 +511,16 @@ hipError_t run_fwd(const NormArgs& p, hipStream_t s) {
   a.rstd = p.rstd; a.rows = p.rows; a.dim = p.dim; a.eps = p.eps; a.res_f32 = p.res_f32; a.out = p.out;
   const bool vec = p.dim % 8 == 0 && aligned16(p.x) && aligned16(p.residual) && aligned16(p.weight) &&
                    aligned16(p.residual_out) && aligned16(p.y);
-  const int shape = row_shape(p.dim, vec);
+  const int shape = row_shape(p.dim, vec, false);
   if (shape == kLong) {
     hipLaunchKernelGGL(rms_norm_fwd_long_kernel<IoT>, dim3((unsigned)p.rows), dim3(kThreads), 0, s, a);
     return hipGetLastError();
   }
-  const int at = rows_at_a_time(shape);
-  const dim3 grid((unsigned)((p.rows + at - 1) / at));
-  MSCAN_NORM_SHAPES(rms_norm_fwd_kernel, grid)
+  const dim3 grid((unsigned)(wave_per_row(shape) ? (p.rows + 3) / 4 : p.rows));
+  if (shape == kWave5)
+    hipLaunchKernelGGL((rms_norm_fwd_kernel<IoT, 8, 64, 5>), grid, dim3(kThreads), 0, s, a);
+  else
+    MSCAN_NORM_SHAPES(rms_norm_fwd_kernel, grid)
   return hipGetLastError();
 }
 
@@ -493,8 +531,8 @@ hipError_t run_bwd(const NormArgs& p, hipStream_t s) {
   a.y = p.y; a.part = static_cast<float*>(p.workspace); a.rows = p.rows; a.dim = p.dim; a.res_f32 = p.res_f32;
   const bool vec = p.dim % 8 == 0 && aligned16(p.x) && aligned16(p.residual) && aligned16(p.weight) &&
                    aligned16(p.dres) && aligned16(p.residual_out) && aligned16(p.y);
-  const int shape = row_shape(p.dim, vec);
-  const int64_t parts = norm_bwd_parts(p.rows);
+  const int shape = row_shape(p.dim, vec, true);
+  const int64_t parts = wave_per_row(shape) ? std::min<int64_t>((p.rows + 3) / 4, 512) : norm_bwd_parts(p.rows);
   if (p.rows == 0) {
     // no rows: dweight_kernel writes zeros
   } else if (shape == kLong) {
@@ -514,7 +552,7 @@ hipError_t run_bwd(const NormArgs& p, hipStream_t s) {
 
 }  // namespace
 
-int64_t norm_bwd_parts(int64_t rows) { return std::min<int64_t>((rows + 3) / 4, 512); }
+int64_t norm_bwd_parts(int64_t rows) { return std::min<int64_t>(rows, 1024); }
 
 hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t stream) {
   return a.io_bf16 ? run_fwd<uint16_t>(a, stream) : run_fwd<float>(a, stream);

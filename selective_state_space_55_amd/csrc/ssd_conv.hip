@@ -26,7 +26,9 @@
 namespace mscan {
 namespace {
 
-constexpr int kRunShift = 3, kRun = 1 << kRunShift;   // tokens a wave walks
+// tokens a wave walks: 32768 x 4352 bf16 takes 129 us with 8, 190 with 4 (taps and history are read too
+// often for them) and 209 with 16 (twice the registers, half the waves)
+constexpr int kRunShift = 3, kRun = 1 << kRunShift;
 
 struct CArgs {
   Packed seq;
@@ -37,49 +39,58 @@ struct CArgs {
   void* u;
   int64_t width, xstride;
   int silu;
+  unsigned ngroups;   // groups of 64 lanes of channels
 };
 
+// W elements as they lie in memory
 template <typename IoT, int W>
-__device__ __forceinline__ void to_f32(const IoT* p, float (&f)[W]) {
-  if constexpr (W == 8)
-    Io<IoT>::to_f32(Io<IoT>::load8(p), f);
-  else
-    f[0] = Io<IoT>::load1(p);
-}
+struct Raw {
+  typename Io<IoT>::V8 v;
+  __device__ __forceinline__ void load(const IoT* p) { v = Io<IoT>::load8(p); }
+  __device__ __forceinline__ void zero() { v = Io<IoT>::zero(); }
+  __device__ __forceinline__ void f32(float (&f)[W]) const { Io<IoT>::to_f32(v, f); }
+};
+template <typename IoT>
+struct Raw<IoT, 1> {
+  IoT v;
+  __device__ __forceinline__ void load(const IoT* p) { v = *p; }
+  __device__ __forceinline__ void zero() { v = IoT(0); }
+  __device__ __forceinline__ void f32(float (&f)[1]) const { f[0] = Io<IoT>::load1(&v); }
+};
 
 template <typename IoT, int W, int K>
 __global__ __launch_bounds__(256) void ssd_conv_kernel(CArgs a) {
   const int lane = threadIdx.x & 63;
   const Packed& q = a.seq;
-  const Run r = find_run(q, uniform64((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)), kRunShift);
+  const Run r = find_run(q, uniform64((int64_t)(blockIdx.x / a.ngroups) * 4 + (threadIdx.x >> 6)), kRunShift);
   if (r.s < 0) return;   // whole waves
   const int64_t s = r.s, start = r.start, end = r.stop, k0 = r.k, t0 = start + k0 * kRun;
-  const int64_t c = ((int64_t)blockIdx.y * 64 + lane) * W;
+  const int64_t c = ((int64_t)(blockIdx.x % a.ngroups) * 64 + lane) * W;
   if (c >= a.width) return;
   const IoT* x = static_cast<const IoT*>(a.x) + c;
   IoT* u = static_cast<IoT*>(a.u) + c;
   IoT* ring = static_cast<IoT*>(a.ring) + c;
 
-  // v[0 .. K-2]: the inputs behind the run, v[K-1 ..]: the run's own
-  float v[K - 1 + kRun][W], w[K][W], b[W];
+  // v[0 .. K-2]: the inputs behind the run, v[K-1 ..]: the run's own, all loads before the first use
+  Raw<IoT, W> v[K - 1 + kRun];
+  float w[W][K], b[W];
 #pragma unroll
-  for (int i = 0; i < kRun; ++i) to_f32<IoT, W>(x + min(t0 + i, end - 1) * a.xstride, v[K - 1 + i]);
+  for (int i = 0; i < kRun; ++i) v[K - 1 + i].load(x + min(t0 + i, end - 1) * a.xstride);
   const int64_t slot = k0 ? -1 : seq_slot(q, s);
   const int64_t pos = slot < 0 ? 0 : seq_position(q, s);
 #pragma unroll
   for (int i = 0; i < K - 1; ++i) {
     const int64_t p = pos - (K - 1) + i;
-#pragma unroll
-    for (int j = 0; j < W; ++j) v[i][j] = 0.0f;
+    v[i].zero();
     if (k0)
-      to_f32<IoT, W>(x + (t0 - (K - 1) + i) * a.xstride, v[i]);
+      v[i].load(x + (t0 - (K - 1) + i) * a.xstride);
     else if (slot >= 0 && p >= 0)
-      to_f32<IoT, W>(ring + (slot * K + p % K) * a.width, v[i]);
+      v[i].load(ring + (slot * K + p % K) * a.width);
   }
 #pragma unroll
   for (int j = 0; j < W; ++j) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) w[k][j] = a.w[(c + j) * K + k];
+    for (int k = 0; k < K; ++k) w[j][k] = a.w[(c + j) * K + k];
     b[j] = a.bias ? a.bias[c + j] : 0.0f;
   }
   if (slot >= 0) {   // the sequence's first run: the rows of its last tokens
@@ -92,15 +103,19 @@ __global__ __launch_bounds__(256) void ssd_conv_kernel(CArgs a) {
     }
   }
   const int n = (int)min((int64_t)kRun, end - t0);
+  float f[K][W];   // the last K inputs, in turn
+#pragma unroll
+  for (int i = 0; i < K - 1; ++i) v[i].f32(f[i]);
 #pragma unroll
   for (int i = 0; i < kRun; ++i) {
     if (i >= n) break;
+    v[i + K - 1].f32(f[(i + K - 1) % K]);
     float out[W];
 #pragma unroll
     for (int j = 0; j < W; ++j) {
       float acc = b[j];
 #pragma unroll
-      for (int k = 0; k < K; ++k) acc = fmaf(w[k][j], v[i + k][j], acc);
+      for (int k = 0; k < K; ++k) acc = fmaf(w[j][k], f[(i + k) % K][j], acc);
       out[j] = a.silu ? silu(acc) : acc;
     }
     if constexpr (W == 8)
@@ -111,8 +126,10 @@ __global__ __launch_bounds__(256) void ssd_conv_kernel(CArgs a) {
 }
 
 template <typename IoT, int W>
-hipError_t run(const CArgs& a, int K, hipStream_t s) {
-  const dim3 grid((unsigned)((ssd_conv_runs(a.seq.nseq, a.seq.total) + 3) / 4), (unsigned)((a.width + 64 * W - 1) / (64 * W)));
+hipError_t run(CArgs a, int K, hipStream_t s) {
+  a.ngroups = (unsigned)((a.width + 64 * W - 1) / (64 * W));
+  // channel groups of a run next to each other, so that what is read at a time is whole rows (136 us the other way round)
+  const dim3 grid((unsigned)((ssd_conv_runs(a.seq.nseq, a.seq.total) + 3) / 4 * a.ngroups));
   switch (K) {
     case 2: hipLaunchKernelGGL((ssd_conv_kernel<IoT, W, 2>), grid, dim3(256), 0, s, a); break;
     case 3: hipLaunchKernelGGL((ssd_conv_kernel<IoT, W, 3>), grid, dim3(256), 0, s, a); break;

@@ -47,6 +47,16 @@ struct StArgs {
   int softplus, euler;
 };
 
+// A step reads and writes each state once and the next step comes a whole batch later: without a place in the
+// caches 256 rows of 80 heads x 64 x 128 take 248 us, with one 267
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ float4 load_once(const float* p) {
+  return __builtin_bit_cast(float4, __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p)));
+}
+__device__ __forceinline__ void store_once(float* p, float4 v) {
+  __builtin_nontemporal_store(__builtin_bit_cast(f32x4, v), reinterpret_cast<f32x4*>(p));
+}
+
 template <typename IoT, int N, int NI, int K>
 __global__ __launch_bounds__(256) void ssd_step_kernel(StArgs a) {
   constexpr int LN = N / 4;          // lanes per channel
@@ -71,7 +81,7 @@ __global__ __launch_bounds__(256) void ssd_step_kernel(StArgs a) {
   float* st = a.state + ((slot * a.H + h) * a.P + p0 + pr) * N + n4;
   float4 s[NI];
 #pragma unroll
-  for (int i = 0; i < NI; ++i) s[i] = *reinterpret_cast<const float4*>(st + (int64_t)i * kRows * N);
+  for (int i = 0; i < NI; ++i) s[i] = load_once(st + (int64_t)i * kRows * N);
 
   // the convolution of 2 N + PS channels
   const IoT* xr = static_cast<const IoT*>(a.xbc) + row * a.xbc_stride;
@@ -112,7 +122,7 @@ __global__ __launch_bounds__(256) void ssd_step_kernel(StArgs a) {
     v.y += fmaf(m, v.y, wx * b.y);
     v.z += fmaf(m, v.z, wx * b.z);
     v.w += fmaf(m, v.w, wx * b.w);
-    *reinterpret_cast<float4*>(st + (int64_t)i * kRows * N) = v;
+    store_once(st + (int64_t)i * kRows * N, v);
     float y = fmaf(cc.x, v.x, fmaf(cc.y, v.y, fmaf(cc.z, v.z, cc.w * v.w)));
 #pragma unroll
     for (int o = LN / 2; o; o >>= 1) y += __shfl_xor(y, o);

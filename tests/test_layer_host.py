@@ -41,7 +41,7 @@ def conv(lib, x=P, w=P, b=None, cu=P, ring=P, slots=P, pos=P, u=P, nseq=2, total
     (dict(xs=63), ESHAPE), (dict(total=1 << 60), ESHAPE), (dict(K=1), EUNSUP), (dict(K=5), EUNSUP), (dict(io=2), EDTYPE),
     (dict(x=P + 1), EALIGN), (dict(io=0, u=P + 2), EALIGN), (dict(w=P + 2), EALIGN), (dict(cu=P + 4), EALIGN),
     (dict(slots=P + 4), EALIGN), (dict(pos=P + 4), EALIGN), (dict(total=1 << 33), EUNSUP),
-    (dict(width=1 << 23, xs=1 << 23), EUNSUP),
+    (dict(width=1 << 31, xs=1 << 31), EUNSUP),
 ])
 def test_conv_refusals(lib, bad, code):
     assert conv(lib, **bad) == code
