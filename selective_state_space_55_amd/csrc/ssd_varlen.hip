@@ -79,7 +79,7 @@ struct Lds {
   static constexpr int kB = kQ * kRowB, kC = kAgg ? 0 : kQ * kRowC, kX = kQ * kRowX;   // kX: a wave's x tile
   static constexpr int kG = kAgg ? 0 : 3 * 1024;             // the causal tiles of B C^T
   static constexpr int kTerms = kAgg ? kQ : 4 * kQ;          // a wave's 2^(cum_Q - cum) w | cum | wgt | sign of w
-  static constexpr size_t bytes() { return 2 * (size_t)(kB + kC + kWaves * kX) + 4 * (size_t)(kG + kWaves * kTerms); }
+  static constexpr size_t bytes() { return 2 * (size_t)(kB + kC + kWaves * kX) + 4 * (size_t)(kG + kWaves * kTerms + kWaves); }
 };
 
 // k slice s of 16 tokens in the order an accumulator holds its rows: lane half h gets tokens
@@ -116,7 +116,11 @@ __device__ __forceinline__ float expm1_small(float x) {
   return fabsf(x) < 0.5f ? p : __expf(x) - 1.0f;
 }
 
-// kAggregate: only the state of a piece that starts from zero, and its decay
+// kAggregate: only the state that a full piece would end with from zero, and its decay.  Its chunks are
+// taken last to first, each token weighted by all that follows it in the piece, until what is left has decayed
+// below 2^-kGone (2^-24 of the sum is already past fp32): a head that forgets within a chunk or two reads no more
+// than that (28-sequence mix: 96 -> 78 us).
+constexpr float kGone = 96.0f;
 enum Mode { kAggregate, kPlain, kGated };
 // kSigned: the input weight w may be negative (Delta without softplus)
 template <int N, Mode kMode, bool kSigned>
@@ -133,14 +137,24 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
   float4* Gs = reinterpret_cast<float4*>(Cs + L::kC + kWaves * L::kX);   // [tile][q][lane]
   float* scl = reinterpret_cast<float*>(Gs) + L::kG + w * L::kTerms;
   float* cum2 = scl + kQ;
+  int* gone = reinterpret_cast<int*>(Gs) + L::kG + kWaves * L::kTerms;   // kAgg: waves that need no earlier chunk
   float* wgt = cum2 + kQ;
   uint32_t* sgn = reinterpret_cast<uint32_t*>(wgt + kQ);
   lds_poison(sm, (int)L::bytes());
 
-  // the piece, and the wave's unit
+  // the wave's unit, and the piece
   const int quads = a.G * a.nquad;
   const int64_t v = blockIdx.x / quads;
   const int gk = blockIdx.x % quads, g = gk / a.nquad;
+  const int tiles = a.HP / 32, upg = (a.H / a.G) * tiles;   // units per head, per group
+  const int ug = (gk % a.nquad) * kWaves + w;
+  const bool live = ug < upg;                               // the group's last workgroup may have fewer
+  const int u = g * upg + (live ? ug : 0);
+  const int h = u / tiles, p0 = (u % tiles) * 32;
+  const float Ah = -expf(a.A_log[h]);
+  const float A2 = Ah * 1.4426950408889634f, iA = 1.0f / Ah;   // iA is not used where Ah = 0
+  const float Dh = a.D ? a.D[h] : 0.0f;
+  const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
   const Packed& q = a.seq;
   const Run run = find_run(q, v, a.shift);
   if (run.s < 0) return;   // no such piece; a sequence without tokens leaves its slot as it is
@@ -150,19 +164,8 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
   if (kAgg && last) return;       // nothing follows it
   const int64_t nchunk = (t_end - t_first + kQ - 1) / kQ;
 
-  const int tiles = a.HP / 32, upg = (a.H / a.G) * tiles;   // units per head, per group
-  const int ug = (gk % a.nquad) * kWaves + w;
-  const bool live = ug < upg;                               // the group's last workgroup may have fewer
-  const int u = g * upg + (live ? ug : 0);
-  const int h = u / tiles, p0 = (u % tiles) * 32;
-  const int64_t slot = kAgg ? -1 : seq_slot(q, s);
-  const bool started = slot >= 0 && seq_position(q, s) > 0;
   const int64_t unit_state = ((int64_t)h * a.HP + p0) * N, row_state = (int64_t)a.H * a.HP * N;
 
-  const float Ah = -expf(a.A_log[h]);
-  const float A2 = Ah * 1.4426950408889634f, iA = 1.0f / Ah;   // iA is not used where Ah = 0
-  const float Dh = a.D ? a.D[h] : 0.0f;
-  const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
   const int64_t ch = (int64_t)h * a.HP + p0;
   const uint16_t* Bg = a.B + (int64_t)g * N;
   const uint16_t* Cg = a.C + (int64_t)g * N;
@@ -230,9 +233,9 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
   // (where hardly anything survives 32 tokens) each element takes its own exponential, from wgt = cum_j - log2 w_j.
   float mid = 0.0f;
   bool mild = false;
-  // a chunk's decay terms from its dt, one token per lane, in powers of two; past the end a = 1 and
+  // a chunk's decay terms from its dt (later: log2 of the decay behind the chunk, where that is wanted), one token per lane, in powers of two; past the end a = 1 and
   // w = 0.  Returns the sum of log2 a.
-  auto decay_terms = [&](int64_t t0) -> float {
+  auto decay_terms = [&](int64_t t0, float later) -> float {
     const float r = bf(dtq) + bias;
     float delta = a.softplus ? softplus_log2e(r) * 0.6931471805599453f : r;
     delta = t0 + lane < t_end ? delta : 0.0f;
@@ -243,7 +246,7 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
     const float from = __shfl(rev, 63 - lane);                   // token lane .. the last
     const float next = __shfl_down(from, 1);                     // every lane takes part
     const float behind = lane == 63 ? 0.0f : next;               // lane + 1 .. the last
-    scl[lane] = __builtin_amdgcn_exp2f(behind) * wj;
+    scl[lane] = __builtin_amdgcn_exp2f(kAgg ? behind + later : behind) * wj;
     const float end = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(cum), 63));
     if constexpr (!kAgg) {
       mid = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(cum), 31));
@@ -259,6 +262,11 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
     return end;
   };
 
+  // the first chunk's loads, before those that wait for the slot
+  load_bc(kAgg ? t_end - kQ : t_first);
+  load_x(kAgg ? t_end - kQ : t_first);
+  const int64_t slot = kAgg ? -1 : seq_slot(q, s);
+  const bool started = slot >= 0 && seq_position(q, s) > 0;
   f32x16 S[NT];
   const float* from = kAgg ? nullptr : !alone ? a.ws_state + v * row_state + unit_state
                     : started ? a.state + slot * row_state + unit_state : nullptr;
@@ -279,19 +287,24 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
     causal[k] = (j <= l32 ? 0xffffu : 0u) | (j + 1 <= l32 ? 0xffff0000u : 0u);
   }
 
-  load_bc(t_first);
-  load_x(t_first);
-  float total = 0.0f;
+  // (without softplus a decay may grow again)
+  auto forgotten = [&](float later) { return a.softplus && later < -kGone; };
+
+  float total = 0.0f;   // log2 of the decay over the chunks so far
   for (int64_t c = 0; c < nchunk; ++c) {
-    const int64_t t0 = t_first + c * kQ;
+    const int64_t t0 = kAgg ? t_end - (c + 1) * kQ : t_first + c * kQ;
+    const int64_t t_next = kAgg ? t0 - kQ : t0 + kQ;
     if (c) lds_barrier();   // every wave has read the previous chunk's B, C and B C^T
+    if constexpr (kAgg) {
+      if (c && gone[0] + gone[1] + gone[2] + gone[3] == kWaves) break;
+    }
     store_tiles();
-    const float sum = decay_terms(t0);
+    const float sum = decay_terms(t0, total);
     total += sum;
-    const float at = __builtin_amdgcn_exp2f(sum);
+    const float at = kAgg ? 1.0f : __builtin_amdgcn_exp2f(sum);
     lds_barrier();
-    load_x(t0 + kQ);
-    if (kAgg) load_bc(t0 + kQ);
+    if (!kAgg || c + 1 < nchunk) load_x(t_next);
+    if (kAgg && c + 1 < nchunk) load_bc(t_next);
     uint4 zq[2][2];
     if constexpr (kGate) {
         const auto rz = rows(a.z + ch, t0, a.z_stride, 32);
@@ -344,15 +357,9 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
     }
     __builtin_amdgcn_sched_barrier(0);   // the phases' registers do not fit side by side
     bf16x8 xf[4];
-    if (live) {
+    if (live && !(kAgg && forgotten(total - sum))) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) xf[k] = opnd_acc_order(Xs, L::kRowX, k, 0, lane);
-      if constexpr (kAgg) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) S[n][r] *= at;
-      }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float4 s0 = *reinterpret_cast<const float4*>(scl + 16 * k + 4 * h32);
@@ -383,9 +390,12 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
         for (int n = 0; n < NT; ++n) S[n] = mfma(bt[n], xh, S[n]);
       }
     }
+    if constexpr (kAgg) {
+      if (lane == 0) gone[w] = !live || forgotten(total);
+    }
     if constexpr (!kAgg) {
       __builtin_amdgcn_sched_barrier(0);
-      load_bc(t0 + kQ);
+      load_bc(t_next);
       lds_barrier();   // B C^T
       if (!live) continue;
       const auto ry = rows(a.y + ch, t0, y_stride, 32);
@@ -503,10 +513,10 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
 // state that enters piece k.  A thread per sequence and four states.
 __global__ __launch_bounds__(256) void ssd_fold_kernel(VArgs a, int N) {
   const Packed& q = a.seq;
-  const int64_t row_state = (int64_t)a.H * a.HP * N;
-  const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  const uint32_t row_state = (uint32_t)a.H * a.HP * N;   // at most 2^24 channels x 128 states
+  const uint32_t e = (blockIdx.x * 256 + threadIdx.x) * 4;
   if (e >= row_state) return;
-  const int h = (int)(e / ((int64_t)a.HP * N));
+  const int h = (int)(e / (uint32_t)(a.HP * N));
   for (int64_t s = blockIdx.y; s < q.nseq; s += gridDim.y) {
     const int64_t start = seq_offset(q, s), len = seq_offset(q, s + 1) - start;
     const int64_t n = (len + ((int64_t)1 << a.shift) - 1) >> a.shift, v0 = (start >> a.shift) + s;
@@ -517,21 +527,23 @@ __global__ __launch_bounds__(256) void ssd_fold_kernel(VArgs a, int N) {
     float4* ws = reinterpret_cast<float4*>(a.ws_state + v0 * row_state + e);
     const int64_t step = row_state / 4;
     const float* decay = a.ws_decay + v0 * a.H + h;
-    // the last piece has no state of its own
-    float4 next = ws[0];
-    float d = decay[0];
-    for (int64_t k = 0; k < n; ++k) {
-      const float4 own = next;
-      const float at = exp2f(d);
-      if (k + 2 < n) {
-        next = ws[(k + 1) * step];
-        d = decay[(k + 1) * a.H];
+    // the last piece has no state of its own; eight at a time, so that a short chain costs one trip to memory
+    for (int64_t k0 = 0; k0 < n; k0 += 8) {
+      float4 own[8];
+      float at[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        own[k] = k0 + k + 1 < n ? ws[(k0 + k) * step] : f;
+        at[k] = k0 + k + 1 < n ? exp2f(decay[(k0 + k) * a.H]) : 0.0f;
       }
-      ws[k * step] = f;
-      f.x = fmaf(at, f.x, own.x);
-      f.y = fmaf(at, f.y, own.y);
-      f.z = fmaf(at, f.z, own.z);
-      f.w = fmaf(at, f.w, own.w);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (k0 + k < n) ws[(k0 + k) * step] = f;
+        f.x = fmaf(at[k], f.x, own[k].x);
+        f.y = fmaf(at[k], f.y, own[k].y);
+        f.z = fmaf(at[k], f.z, own[k].z);
+        f.w = fmaf(at[k], f.w, own[k].w);
+      }
     }
   }
 }
