@@ -427,6 +427,8 @@ int mamba_ssd_conv_fwd_varlen(const void* x, const float* weight, const float* b
  * divisor of nheads, strides up to 2^24 (others MAMBA_SCAN_ERR_UNSUPPORTED); x, B, C, z, y and state
  * 16-byte aligned, the strides of x, B, C and z multiples of 8.  Products of bf16 operands with fp32
  * accumulation; the state's own update carries fp32's accuracy (the scaled x in three bf16 parts).
+ * Where long sequences are cut, an input whose weight has decayed below 2^-96 by the end of its piece
+ * need not reach the pieces after it.
  */
 int mamba_ssd_fwd_varlen(const void* x, const void* dt, const float* A_log, const void* B, const void* C,
                          const float* D, const void* z, const float* dt_bias, const int64_t* cu_seqlens, float* state,
@@ -481,7 +483,7 @@ int mamba_ssd_step(const void* xbc, const void* dt, const float* A_log, const fl
  *                             scale.  Row scale: largest magnitude / 448; block scale: the smallest power of two
  *                             that keeps the block's magnitudes within 448; 1 where all values are 0
  *   rstd         (rows)       f32             OUT, NULL: not written
- * Sizes: rows >= 0, dim >= 1; the launch's work-items (at most rows * 1024) below 2^32.  A row with a NaN or an
+ * Sizes: rows >= 0, dim >= 1, eps >= 0 (else MAMBA_SCAN_ERR_UNSUPPORTED); the launch's work-items (at most rows * 1024) below 2^32.  A row with a NaN or an
  * Inf has NaNs in y.
  */
 int mamba_rms_norm_fwd(const void* x, const void* residual, const float* weight, float eps, void* residual_out,

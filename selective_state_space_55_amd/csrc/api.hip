@@ -636,6 +636,7 @@ int mamba_rms_norm_fwd(const void* x, const void* residual, const float* weight,
   int st = check_norm(rows, dim, io_dtype, residual_dtype);
   if (st != MAMBA_SCAN_OK) return st;
   if (out_format < MAMBA_NORM_OUT_IO || out_format > MAMBA_NORM_OUT_MX8) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  if (!(eps >= 0.0f)) return MAMBA_SCAN_ERR_UNSUPPORTED;
   if (!weight || (rows > 0 && (!x || !y || (out_format != MAMBA_NORM_OUT_IO && !scales)))) return MAMBA_SCAN_ERR_NULL;
   if (rows > 0 && (residual == nullptr) != (residual_out == nullptr)) return MAMBA_SCAN_ERR_NULL;
   const size_t esz = io_dtype == MAMBA_SCAN_BF16 ? 2 : 4, rsz = residual_dtype == MAMBA_SCAN_BF16 ? 2 : 4;

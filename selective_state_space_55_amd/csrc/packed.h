@@ -3,7 +3,7 @@
 //
 // Offsets, slots and positions are the caller's device memory, which the host
 // cannot check: offsets are clamped to [0, total], a slot outside [0, nslots)
-// means "no slot" and a negative position counts as 0, so a bad array gives
+// means "no slot", a negative position counts as 0 and one past 2^62 as that, so a bad array gives
 // wrong results but no access out of bounds.
 #pragma once
 
@@ -82,7 +82,7 @@ __device__ __forceinline__ int64_t seq_slot(const Packed& p, int64_t s) {
 __device__ __forceinline__ int64_t seq_position(const Packed& p, int64_t s) {
   if (!p.slots) return 0;
   const int64_t v = p.positions[s];
-  return v < 0 ? 0 : v;
+  return v < 0 ? 0 : min(v, (int64_t)1 << 62);   // room for the call's tokens
 }
 
 }  // namespace mscan

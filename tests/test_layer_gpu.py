@@ -242,9 +242,9 @@ def test_conv_bad_offsets_stay_in_bounds():
     """Offsets that are no offsets give some numbers, within the arrays, and rings of other slots stay."""
     r = Rng(10)
     x, w = dev(r(30, 64, dtype=torch.bfloat16), r(64, 4))
-    for cu in ([-7, 12, 99], [20, 10, 30], [1 << 40, -(1 << 40), 5]):
+    for cu, pos in (([-7, 12, 99], 0), ([20, 10, 30], 0), ([1 << 40, -(1 << 40), 5], 0), ([0, 15, 30], (1 << 63) - 1)):
         ring = torch.full((3, 4, 64), 2.0, dtype=torch.bfloat16, device=DEV)
-        mscan.ssd_conv_fwd_varlen(x, w, dev(i64(cu)), conv_state=ring, slots=dev(i64([0, 7])), positions=dev(i64([0, 0])))
+        mscan.ssd_conv_fwd_varlen(x, w, dev(i64(cu)), conv_state=ring, slots=dev(i64([0, 7])), positions=dev(i64([pos, 0])))
         torch.cuda.synchronize()
         assert torch.equal(ring[1:].cpu(), torch.full((2, 4, 64), 2.0, dtype=torch.bfloat16))
 
@@ -326,6 +326,18 @@ def test_ssd_small_and_large_steps(delta, dt_std, x_std):
     c["x"] = (c["x"].float() * x_std).bfloat16()
     say(f"ssd steps {delta}")
     y, sd, ref = run_ssd(c, lens, r(2, 3, 64, 128), i64([1, 0]), i64([9, 0]), True, True, False)
+    check_ssd(lens, y, sd, ref)
+
+
+@pytest.mark.parametrize("N,gated", [(128, True), (64, False)])
+def test_ssd_steps_of_either_sign(N, gated):
+    """Without softplus a step may be negative: its token grows the state and has a negative weight."""
+    lens = [300, 65, 2]
+    r = Rng(17)
+    c = ssd_case(r, lens, 3, 64, N, 1)
+    c["dt"], c["dt_bias"] = (c["dt"].float() * 0.01).bfloat16(), c["dt_bias"] * 0
+    c["A_log"] = c["A_log"] * 0.5
+    y, sd, ref = run_ssd(c, lens, r(4, 3, 64, N), i64([3, 1, 0]), i64([1, 0, 4]), gated, False, False)
     check_ssd(lens, y, sd, ref)
 
 
@@ -573,6 +585,33 @@ def test_layer_graph_replays_equal_eager():
             assert torch.equal(out[keep], want[keep])
             for a, b in zip(eager, graphed):
                 assert torch.equal(a, b)
+
+
+def test_binding_refuses_what_the_kernels_do_not_take():
+    r = Rng(18)
+    c = {k: v.to(DEV) for k, v in ssd_case(r, [20], 2, 64, 128, 1).items()}
+    cu, one = dev(i64([0, 20])), dev(i64([0]))
+    ssd = lambda **k: mscan.ssd_fwd_varlen(**{**dict(x=c["x"], dt=c["dt"], A_log=c["A_log"], B=c["B"], C=c["C"], cu_seqlens=cu), **k})
+    conv = lambda **k: mscan.ssd_conv_fwd_varlen(**{**dict(x=c["x"].flatten(1), weight=torch.zeros(128, 4, device=DEV), cu_seqlens=cu), **k})
+    norm = lambda **k: mscan.rms_norm_fwd(**{**dict(x=c["x"].flatten(1), weight=torch.ones(128, device=DEV)), **k})
+    ssd(), conv(), norm()
+    state = torch.zeros(1, 2, 64, 128, device=DEV)
+    for call, bad in [
+        (ssd, dict(x=c["x"].float())), (ssd, dict(x=c["x"].transpose(1, 2))), (ssd, dict(B=c["B"][:10])), (ssd, dict(cu_seqlens=cu.int())),
+        (ssd, dict(state=state)), (ssd, dict(state=state, slots=one)), (ssd, dict(state=state.double(), slots=one, positions=one)),
+        (ssd, dict(D=torch.zeros(3, device=DEV))), (ssd, dict(discretization="bilinear")), (ssd, dict(out=c["x"][:5])),
+        (conv, dict(x=c["x"].flatten(1).half())), (conv, dict(weight=torch.zeros(64, 4, device=DEV))),
+        (conv, dict(weight=torch.zeros(128, 5, device=DEV))), (conv, dict(conv_state=torch.zeros(1, 4, 128, device=DEV))),
+        (conv, dict(x=c["x"].flatten(1).t())), (norm, dict(x=c["x"].flatten(1)[:, ::2])), (norm, dict(quant="int8")),
+        (norm, dict(residual=torch.zeros(20, 128, device=DEV).half())), (norm, dict(residual=torch.zeros(19, 128, device=DEV))),
+        (norm, dict(weight=torch.ones(128))), (norm, dict(scales=torch.zeros(20, device=DEV))), (norm, dict(eps=-1.0)),
+        (norm, dict(residual_out=torch.zeros(20, 128, device=DEV))),
+    ]:
+        with pytest.raises((ValueError, TypeError, mscan.MambaScanError)):
+            call(**bad)
+    z = torch.zeros(20, 2 * 64 + 4, dtype=torch.bfloat16, device=DEV)[:, :128].unflatten(1, (2, 64))   # rows off 16 bytes
+    with pytest.raises(mscan.MambaScanError):
+        ssd(z=z)
 
 
 def test_side_streams_at_once():

@@ -103,8 +103,8 @@ def test_step_refusals(lib, bad, code):
     assert step(lib, **bad) == code
 
 
-def norm(lib, x=P, res=None, w=P, ro=None, y=P, sc=None, rstd=None, rows=3, dim=64, io=1, rio=1, out=0):
-    return lib.mamba_rms_norm_fwd(x, res, w, 1e-5, ro, y, sc, rstd, rows, dim, io, rio, out, None)
+def norm(lib, x=P, res=None, w=P, ro=None, y=P, sc=None, rstd=None, rows=3, dim=64, io=1, rio=1, out=0, eps=1e-5):
+    return lib.mamba_rms_norm_fwd(x, res, w, eps, ro, y, sc, rstd, rows, dim, io, rio, out, None)
 
 
 def norm_bwd(lib, dy=P, r=P, w=P, rstd=P, dres=None, dx=P, dr=None, dw=P, rows=3, dim=64, io=1, rio=1, ws=P, wsb=1 << 40):
@@ -114,7 +114,8 @@ def norm_bwd(lib, dy=P, r=P, w=P, rstd=P, dres=None, dx=P, dr=None, dw=P, rows=3
 @pytest.mark.parametrize("call,bad,code", [
     (norm, dict(x=None), ENULL), (norm, dict(w=None), ENULL), (norm, dict(y=None), ENULL), (norm, dict(out=1), ENULL),
     (norm, dict(res=P), ENULL), (norm, dict(ro=P), ENULL), (norm, dict(rows=-1), ESHAPE), (norm, dict(dim=0), ESHAPE),
-    (norm, dict(io=3), EDTYPE), (norm, dict(io=0, rio=1), EDTYPE), (norm, dict(out=3, sc=P), EUNSUP),
+    (norm, dict(io=3), EDTYPE), (norm, dict(io=0, rio=1), EDTYPE), (norm, dict(out=3, sc=P), EUNSUP), (norm, dict(eps=-1e-5), EUNSUP),
+    (norm, dict(eps=float("nan")), EUNSUP),
     (norm, dict(rows=1 << 40), EUNSUP), (norm, dict(x=P + 1), EALIGN), (norm, dict(rio=0, res=P + 2, ro=P), EALIGN),
     (norm, dict(out=1, sc=P + 2), EALIGN), (norm, dict(rstd=P + 2), EALIGN),
     (norm_bwd, dict(dy=None), ENULL), (norm_bwd, dict(rstd=None), ENULL), (norm_bwd, dict(dw=None), ENULL),
