@@ -37,22 +37,25 @@ __device__ __forceinline__ int64_t lane64(int64_t v, int lane) {
   return (int64_t)(((uint64_t)hi << 32) | lo);
 }
 
-// A run of 2^shift tokens of a sequence, numbered (cu[s] >> shift) + s + k for run k of sequence s: the
-// numbers of one sequence's runs end before the next one's begin, so that a wave finds its run without
-// a prefix sum over the lengths.  Some numbers (at most nseq) name no run.
+// A run of 2^shift tokens of a sequence (its last one may be shorter).  Runs are numbered so that a wave
+// finds the one of a number without a prefix sum over the lengths:
+//   every run   run k of sequence s is (cu[s] >> shift) + s + k, all below (total >> shift) + nseq
+//   full runs   that another one follows: (cu[s] >> shift) + k, all below total >> shift
+// The numbers of one sequence end before the next one's begin; some name no run.
 struct Run {
   int64_t s;            // sequence, -1: no run has this number
   int64_t start, stop;  // its tokens
   int64_t k;            // the run's number in it
 };
 
-// number is uniform; whole waves.  Looks at 64 offsets at a time.
+// The run of a uniform number; whole waves.  Looks at 64 offsets at a time.
+template <bool kFull>
 __device__ __forceinline__ Run find_run(const Packed& p, int64_t number, int shift) {
   const int lane = threadIdx.x & 63;
   int64_t lo = 0, n = p.nseq;
   while (n > 63) {
     const int64_t step = (n + 62) / 63, i = lo + lane * step;
-    const bool in = lane * step < n && (seq_offset(p, i) >> shift) + i <= number;
+    const bool in = lane * step < n && (seq_offset(p, i) >> shift) + (kFull ? 0 : i) <= number;
     const int c = __popcll(__ballot(in));
     if (c == 0) return Run{-1, 0, 0, 0};
     lo += (c - 1) * step;
@@ -60,14 +63,15 @@ __device__ __forceinline__ Run find_run(const Packed& p, int64_t number, int shi
   }
   // offsets lo .. lo + n, the last of them where the last sequence stops
   const int64_t v = seq_offset(p, lo + min((int64_t)lane, n));
-  const int c = __popcll(__ballot(lane < n && (v >> shift) + lo + lane <= number));
+  const int c = __popcll(__ballot(lane < n && (v >> shift) + (kFull ? 0 : lo + lane) <= number));
   if (c == 0) return Run{-1, 0, 0, 0};
   Run r;
   r.s = lo + c - 1;
   r.start = lane64(v, c - 1);
   r.stop = lane64(v, c);
-  r.k = number - ((r.start >> shift) + r.s);
-  if (r.k < 0 || r.start + (r.k << shift) >= r.stop) r.s = -1;   // (k < 0 only where offsets fall)
+  r.k = number - ((r.start >> shift) + (kFull ? 0 : r.s));
+  // (k < 0 only where offsets fall)
+  if (r.k < 0 || r.start + ((r.k + (kFull ? 1 : 0)) << shift) >= r.stop) r.s = -1;
   return r;
 }
 

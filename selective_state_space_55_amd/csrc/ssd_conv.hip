@@ -62,7 +62,7 @@ template <typename IoT, int W, int K>
 __global__ __launch_bounds__(256) void ssd_conv_kernel(CArgs a) {
   const int lane = threadIdx.x & 63;
   const Packed& q = a.seq;
-  const Run r = find_run(q, uniform64((int64_t)(blockIdx.x / a.ngroups) * 4 + (threadIdx.x >> 6)), kRunShift);
+  const Run r = find_run<false>(q, uniform64((int64_t)(blockIdx.x / a.ngroups) * 4 + (threadIdx.x >> 6)), kRunShift);
   if (r.s < 0) return;   // whole waves
   const int64_t s = r.s, start = r.start, end = r.stop, k0 = r.k, t0 = start + k0 * kRun;
   const int64_t c = ((int64_t)(blockIdx.x % a.ngroups) * 64 + lane) * W;

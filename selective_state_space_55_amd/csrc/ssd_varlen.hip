@@ -144,7 +144,7 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
 
   // the wave's unit, and the piece
   const int quads = a.G * a.nquad;
-  const int64_t v = blockIdx.x / quads;
+  const int64_t number = blockIdx.x / quads;
   const int gk = blockIdx.x % quads, g = gk / a.nquad;
   const int tiles = a.HP / 32, upg = (a.H / a.G) * tiles;   // units per head, per group
   const int ug = (gk % a.nquad) * kWaves + w;
@@ -156,12 +156,12 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
   const float Dh = a.D ? a.D[h] : 0.0f;
   const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
   const Packed& q = a.seq;
-  const Run run = find_run(q, v, a.shift);
+  const Run run = find_run<kAgg>(q, number, a.shift);
   if (run.s < 0) return;   // no such piece; a sequence without tokens leaves its slot as it is
   const int64_t s = run.s, t_first = run.start + (run.k << a.shift);
   const int64_t t_end = min(run.stop, t_first + ((int64_t)1 << a.shift));   // (no overflow: shift <= 62, t_first 0 .. total)
   const bool last = t_end == run.stop, alone = last && run.k == 0;
-  if (kAgg && last) return;       // nothing follows it
+  const int64_t v = (run.start >> a.shift) + s + run.k;   // the piece's part of the workspace
   const int64_t nchunk = (t_end - t_first + kQ - 1) / kQ;
 
   const int64_t unit_state = ((int64_t)h * a.HP + p0) * N, row_state = (int64_t)a.H * a.HP * N;
@@ -510,40 +510,40 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
 }
 
 // The fold over a sequence's pieces: entry k of its part of ws_state, piece k's own state, becomes the
-// state that enters piece k.  A thread per sequence and four states.
+// state that enters piece k.  A thread per cut sequence and four states; a cut sequence is found by its
+// first piece's number among the full pieces, so that the grid does not grow with the uncut ones.
 __global__ __launch_bounds__(256) void ssd_fold_kernel(VArgs a, int N) {
   const Packed& q = a.seq;
   const uint32_t row_state = (uint32_t)a.H * a.HP * N;   // at most 2^24 channels x 128 states
   const uint32_t e = (blockIdx.x * 256 + threadIdx.x) * 4;
-  if (e >= row_state) return;
+  const bool in = e < row_state;   // (whole waves look for the sequence)
   const int h = (int)(e / (uint32_t)(a.HP * N));
-  for (int64_t s = blockIdx.y; s < q.nseq; s += gridDim.y) {
-    const int64_t start = seq_offset(q, s), len = seq_offset(q, s + 1) - start;
-    const int64_t n = (len + ((int64_t)1 << a.shift) - 1) >> a.shift, v0 = (start >> a.shift) + s;
-    if (n <= 1) continue;   // one piece (or none): it starts from its slot
-    const int64_t slot = seq_slot(q, s);
-    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (slot >= 0 && seq_position(q, s) > 0) f = *reinterpret_cast<const float4*>(a.state + slot * row_state + e);
-    float4* ws = reinterpret_cast<float4*>(a.ws_state + v0 * row_state + e);
-    const int64_t step = row_state / 4;
-    const float* decay = a.ws_decay + v0 * a.H + h;
-    // the last piece has no state of its own; eight at a time, so that a short chain costs one trip to memory
-    for (int64_t k0 = 0; k0 < n; k0 += 8) {
-      float4 own[8];
-      float at[8];
+  const Run run = find_run<true>(q, blockIdx.y, a.shift);
+  if (run.s < 0 || run.k != 0) return;
+  const int64_t s = run.s, v0 = (run.start >> a.shift) + s, slot = seq_slot(q, s);
+  const int64_t n = (run.stop - run.start + ((int64_t)1 << a.shift) - 1) >> a.shift;
+  float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (slot >= 0 && seq_position(q, s) > 0 && in) f = *reinterpret_cast<const float4*>(a.state + slot * row_state + e);
+  if (!in) return;
+  float4* ws = reinterpret_cast<float4*>(a.ws_state + v0 * row_state + e);
+  const int64_t step = row_state / 4;
+  const float* decay = a.ws_decay + v0 * a.H + h;
+  // the last piece has no state of its own; eight at a time, so that a short chain costs one trip to memory
+  for (int64_t k0 = 0; k0 < n; k0 += 8) {
+    float4 own[8];
+    float at[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        own[k] = k0 + k + 1 < n ? ws[(k0 + k) * step] : f;
-        at[k] = k0 + k + 1 < n ? exp2f(decay[(k0 + k) * a.H]) : 0.0f;
-      }
+    for (int k = 0; k < 8; ++k) {
+      own[k] = k0 + k + 1 < n ? ws[(k0 + k) * step] : f;
+      at[k] = k0 + k + 1 < n ? exp2f(decay[(k0 + k) * a.H]) : 0.0f;
+    }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (k0 + k < n) ws[(k0 + k) * step] = f;
-        f.x = fmaf(at[k], f.x, own[k].x);
-        f.y = fmaf(at[k], f.y, own[k].y);
-        f.z = fmaf(at[k], f.z, own[k].z);
-        f.w = fmaf(at[k], f.w, own[k].w);
-      }
+    for (int k = 0; k < 8; ++k) {
+      if (k0 + k < n) ws[(k0 + k) * step] = f;
+      f.x = fmaf(at[k], f.x, own[k].x);
+      f.y = fmaf(at[k], f.y, own[k].y);
+      f.z = fmaf(at[k], f.z, own[k].z);
+      f.w = fmaf(at[k], f.w, own[k].w);
     }
   }
 }
@@ -562,10 +562,11 @@ template <int N>
 hipError_t run(const VArgs& a, const SsdVarlenPlan& p, hipStream_t s) {
   const dim3 grid((unsigned)(p.pieces * p.quads));
   if (p.cut) {
-    hipError_t e = launch<N, kAggregate, true>(a, grid, s);
+    const unsigned full = (unsigned)(a.seq.total >> a.shift);   // pieces that another one follows, at most
+    hipError_t e = launch<N, kAggregate, true>(a, dim3((unsigned)(full * p.quads)), s);
     if (e != hipSuccess) return e;
     const int64_t blocks = ((int64_t)a.H * a.HP * N / 4 + 255) / 256;
-    hipLaunchKernelGGL(ssd_fold_kernel, dim3((unsigned)blocks, (unsigned)std::min<int64_t>(65535, a.seq.nseq)), dim3(256), 0, s, a, N);
+    hipLaunchKernelGGL(ssd_fold_kernel, dim3((unsigned)blocks, full), dim3(256), 0, s, a, N);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
