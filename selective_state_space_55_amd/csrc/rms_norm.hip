@@ -16,7 +16,9 @@
 // element), so what bounds them is HBM; a row stays in registers between the
 // sum of squares and its use.  W elements per access (8, or 1 for rows that are
 // not 16-byte aligned), T lanes per row (a wave, so that the sum needs no LDS,
-// or a 256-thread workgroup for long rows) and V accesses per lane.
+// or a 256-thread workgroup for long rows) and V accesses per lane.  32768 rows of 2560, bf16 to e4m3 with a
+// scale per row: 117 us, 5.0 TB/s; the gradient of 32768 rows of 2048, bf16 with an fp32 residual: 198 us + 5
+// for dweight, 5.3 TB/s (a copy of 1 GiB: 4.8); 16 rows: 5 us.
 #include "internal.h"
 #include "io.h"
 #include "mfma.h"
@@ -438,7 +440,7 @@ __global__ __launch_bounds__(kThreads) void dweight_long_kernel(NArgs a) {
 }
 
 // dweight[c] = sum of part[0 .. n)[c]: 16 columns a workgroup, 64 threads a column, so that a thread has few
-// loads and all of them are in flight (512 parts x 2048 columns: 4.7 us; with four threads a column 39.7 us)
+// loads and all of them are in flight (512 parts x 2048 columns: 4.8 us; with four threads a column 39.7 us)
 __global__ __launch_bounds__(1024) void dweight_kernel(const float* part, float* dw, int n, int64_t dim) {
   __shared__ float red[64][17];
   const int col = threadIdx.x & 15, g = threadIdx.x >> 4;

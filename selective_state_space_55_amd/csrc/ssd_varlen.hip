@@ -35,6 +35,17 @@
 // the GPU: a first pass forms each piece's own state (from zero) and its decay, a fold turns those
 // into the state that enters each piece (the associative (a, b) operator), and the main pass
 // starts from it.
+//
+// What bounds it: instruction issue.  A chunk of a unit (N = 128, gated) is 1100 vector instructions (a
+// quarter of them the splits of S and of the scaled x, 300 the gate and the epilogue, 64 exponentials and
+// reciprocals at a quarter of the rate), 92 MFMAs of 32 cycles and 126 LDS accesses.  Two waves on a SIMD take
+// 17,000 cycles for a chunk each, of which 10,300 issue vector instructions and 5,900 run MFMAs; the clock
+// falls from 2.3 to 1.8 GHz under it (64 heads, 8 sequences of 1024 tokens, a wave per SIMD: 97 us; 16, two waves
+// per SIMD: 168).  A third wave per SIMD would need 168 registers (S
+// alone is 64) and 53 KB of LDS.  28 sequences, 32768 tokens, 64 heads of 64, N = 128, gated: 435 us, of them
+// the main pass 350 (1.13 GB, 3.2 TB/s; B and C are read again by each XCD), the pieces' own states 70, the
+// fold 22; one prompt of 20000 tokens, 32 heads of 128, N = 64: 225 us; one of 509, 24 heads of 64: 29 us,
+// three short launches.
 #include "internal.h"
 #include "io.h"
 #include "mfma.h"
@@ -119,7 +130,7 @@ __device__ __forceinline__ float expm1_small(float x) {
 // kAggregate: only the state that a full piece would end with from zero, and its decay.  Its chunks are
 // taken last to first, each token weighted by all that follows it in the piece, until what is left has decayed
 // below 2^-kGone (2^-24 of the sum is already past fp32): a head that forgets within a chunk or two reads no more
-// than that (28-sequence mix: 96 -> 78 us).
+// than that (28-sequence mix: 70 us, first to last and all of them 96).
 constexpr float kGone = 96.0f;
 enum Mode { kAggregate, kPlain, kGated };
 // kSigned: the input weight w may be negative (Delta without softplus)
@@ -580,11 +591,11 @@ int64_t quads_of(int64_t nheads, int64_t headdim, int64_t ngroups) { return (nhe
 }  // namespace
 
 // Pieces: as many tokens as share them out over two rounds of two workgroups per CU, a power of two
-// (so that a piece number needs no division).  32768 tokens of 28 sequences, 32 workgroups a piece: 473 us in
-// pieces of 1024, 500 in 512, 518 in 2048; 20000 tokens of one sequence: 230 us in 512, 250 in 1024; 509 tokens,
-// 12 workgroups a piece: 30 us in 64, 44 in 256.  Where the sequences fill the GPU by themselves and are
+// (so that a piece number needs no division).  32768 tokens of 28 sequences, 32 workgroups a piece: 435 us in
+// pieces of 1024, 467 in 512, 508 in 2048; 20000 tokens of one sequence, 32 a piece: 225 us in 512, 251 in 256,
+// 238 in 1024; 509 tokens, 12 workgroups a piece: 29 us in 64, 32 in 128, 44 in 256.  Where the sequences fill the GPU by themselves and are
 // that short on average, or are known to be, they are not cut: 16 sequences of 256 tokens, 32 workgroups
-// each, 53 us whole and 83 in pieces of 128.
+// each, 57 us whole and 104 in pieces of 128.
 SsdVarlenPlan make_ssd_varlen_plan(int64_t nseq, int64_t total, int64_t nheads, int64_t headdim, int64_t dstate,
                                    int64_t ngroups, int64_t longest) {
   SsdVarlenPlan p{};
