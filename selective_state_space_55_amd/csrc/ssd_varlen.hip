@@ -79,7 +79,7 @@ struct VArgs {
   int softplus, euler;
 };
 
-constexpr float kMild = 96.0f;
+constexpr float kMild = 96.0f, kLeast = -256.0f;
 constexpr int kWaves = 4;   // units of 32 channels per workgroup
 
 template <int N, bool kAgg>
@@ -250,7 +250,8 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
     const float r = bf(dtq) + bias;
     float delta = a.softplus ? softplus_log2e(r) * 0.6931471805599453f : r;
     delta = t0 + lane < t_end ? delta : 0.0f;
-    const float la2 = delta * A2;
+    // 2^kLeast takes any fp32 state to nothing; a larger decay would only cost the sums behind it their last bits
+    const float la2 = fmaxf(delta * A2, kLeast);
     const float wj = a.euler || Ah == 0.0f ? delta : expm1_small(delta * Ah) * iA;
     const float cum = wave_prefix_sum(la2);
     const float rev = wave_prefix_sum(__shfl(la2, 63 - lane));   // from the chunk's end

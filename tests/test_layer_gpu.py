@@ -329,6 +329,18 @@ def test_ssd_small_and_large_steps(delta, dt_std, x_std):
     check_ssd(lens, y, sd, ref)
 
 
+@pytest.mark.parametrize("huge", [300.0, 20000.0, float("inf")])
+def test_ssd_tokens_that_forget_everything(huge):
+    """A token whose decay is 0 starts the state anew; it costs the tokens behind it no accuracy."""
+    lens = [200, 70]
+    r = Rng(23)
+    c = ssd_case(r, lens, 3, 64, 128, 1, (0.001, 0.01))
+    c["dt"][5::37] = huge
+    c["D"] = c["D"] * 0
+    y, sd, ref = run_ssd(c, lens, r(2, 3, 64, 128), i64([1, 0]), i64([9, 0]), True, True, False)
+    check_ssd(lens, y, sd, ref)
+
+
 @pytest.mark.parametrize("N,gated", [(128, True), (64, False)])
 def test_ssd_steps_of_either_sign(N, gated):
     """Without softplus a step may be negative: its token grows the state and has a negative weight."""
@@ -612,6 +624,37 @@ def test_binding_refuses_what_the_kernels_do_not_take():
     z = torch.zeros(20, 2 * 64 + 4, dtype=torch.bfloat16, device=DEV)[:, :128].unflatten(1, (2, 64))   # rows off 16 bytes
     with pytest.raises(mscan.MambaScanError):
         ssd(z=z)
+
+
+def test_pools_and_tokens_past_32_bits():
+    """Pools and token arrays of more than 2^31 elements give what small ones give."""
+    r = Rng(31)
+    H, P, N, K, io = 16, 64, 128, 4, torch.bfloat16
+    width = H * P + 2 * N
+    s = {k: dev(v) for k, v in step_case(r, 2, H, P, N, 1, K, io).items()}
+    far = (1 << 31) // (H * P * N) + 1          # the state pool's entry that starts past 2^31 elements
+    ring, state, pos, small = r(2, K, width, dtype=io), r(2, H, P, N), dev(i64([7, 2])), dev(i64([0, 1]))
+    big, slots = torch.empty(far + 2, H, P, N, device=DEV), dev(i64([far + 1, far]))
+    rings = torch.empty(far + 2, K, width, dtype=io, device=DEV)
+    c = {k: dev(v) for k, v in ssd_case(r, [130, 3], H, P, N, 1).items() if k != "dt_bias"}
+    cu, apart_by = dev(i64([0, 130, 133])), 1 << 24
+    x_far = torch.empty(133 * apart_by, dtype=io, device=DEV).view(133, apart_by)[:, :H * P]
+    x_far.copy_(c["x"].flatten(1))
+    got = []
+    for pool, rp, sl in ((dev(state), dev(ring), small), (big, rings, slots)):
+        pool[sl], rp[sl] = dev(state), dev(ring)
+        say(f"pool of {pool.numel()} elements")
+        y = mscan.ssd_step(s["xbc"], s["dt"], s["A_log"], s["conv_weight"], rp, pool, pos, slots=sl, D=s["D"], z=s["z"],
+                           dt_bias=s["dt_bias"], conv_bias=s["conv_bias"])
+        x = c["x"] if pool is not big else x_far.unflatten(1, (H, P))
+        y2 = mscan.ssd_fwd_varlen(x, c["dt"], c["A_log"], c["B"], c["C"], cu, D=c["D"], z=c["z"], state=pool, slots=sl, positions=pos)
+        u = mscan.ssd_conv_fwd_varlen(x.flatten(1), torch.ones(H * P, K, device=DEV), cu)
+        torch.cuda.synchronize()
+        got.append((y, y2, u, pool[sl], rp[sl]))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    del big, x_far, rings, x, got
+    torch.cuda.empty_cache()
 
 
 def test_side_streams_at_once():
