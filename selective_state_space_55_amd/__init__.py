@@ -700,6 +700,9 @@ def ssd_conv_fwd_varlen(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: torch
         nslots = conv_state.shape[0] if conv_state.dim() == 3 else -1
         if slots is None or positions is None:
             raise ValueError("conv_state needs slots and positions")
+    if out is not None and total and out.data_ptr() < x.data_ptr() + ((total - 1) * xs + width) * x.element_size() and \
+            x.data_ptr() < out.data_ptr() + total * width * out.element_size():
+        raise ValueError("out must not overlap x, whose earlier tokens later ones read")
     u = out if out is not None else torch.empty((total, width), dtype=iot, device=dev)
     rc = lib.mamba_ssd_conv_fwd_varlen(
         x.data_ptr(), _need("weight", weight, (width, K), f32, dev), _need("bias", bias, (width,), f32, dev),

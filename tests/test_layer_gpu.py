@@ -657,6 +657,16 @@ def test_pools_and_tokens_past_32_bits():
     torch.cuda.empty_cache()
 
 
+def test_conv_refuses_to_write_over_its_input():
+    x, w, cu = torch.zeros(20, 64, dtype=torch.bfloat16, device=DEV), torch.zeros(64, 4, device=DEV), dev(i64([0, 20]))
+    both = torch.zeros(40, 64, dtype=torch.bfloat16, device=DEV)
+    for a, out in ((x, x), (both[:20], both[10:30]), (both[10:30], both[:20])):
+        with pytest.raises(ValueError):
+            mscan.ssd_conv_fwd_varlen(a, w, cu, out=out)
+    mscan.ssd_conv_fwd_varlen(both[:20], w, cu, out=both[20:])
+    torch.cuda.synchronize()
+
+
 def test_side_streams_at_once():
     """Two prompts batches on two streams at the same time, each with its own workspace, equal what they give alone."""
     r = Rng(13)
