@@ -634,12 +634,12 @@ def _token_stride(name: str, t: torch.Tensor, shape, dtype, device) -> int:
     if t.shape != shape or t.dtype != dtype or t.device != device:
         _req(name, t, shape, dtype, device)
     st = t.stride()
-    if st[-1] == 1 and (len(st) == 2 or st[1] == shape[2]) and shape[0] > 1:
-        return st[0]
-    if shape[0] and not t[0].is_contiguous():
+    if not (st[-1] == 1 and (len(st) == 2 or st[1] == shape[2])) and shape[0] and not t[0].is_contiguous():
         raise ValueError(f"{name}: the elements of a token must be contiguous")
+    if shape[0] > 1:
+        return st[0]
     width = shape[1] if len(shape) == 2 else shape[1] * shape[2]
-    return st[0] if shape[0] > 1 else -(-width // 8) * 8
+    return -(-width // 8) * 8
 
 
 def _current_handle(index: int) -> int:
