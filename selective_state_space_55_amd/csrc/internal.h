@@ -250,7 +250,7 @@ struct SsdVarlenPlan {
   bool cut;            // a sequence may have more than one piece: two more passes and a workspace
   int64_t pieces;      // piece numbers (some of them name no piece)
   int64_t quads;       // workgroups per piece
-  size_t off_decay;    // workspace: (pieces, H, P, N) fp32 states, then (pieces, H) fp32
+  size_t off_decay;    // workspace: (parts, H, P, N) fp32 states, then (parts, H) fp32
   size_t ws_total;
 };
 // longest: a bound of the sequences' lengths, 0: unknown

@@ -72,12 +72,17 @@ struct VArgs {
   uint16_t* y;
   int x_stride, dt_stride, b_stride, c_stride, z_stride;
   int shift;          // pieces of 2^shift tokens
-  float* ws_state;    // (pieces, H, P, N): a piece's own state, then the state that enters it
-  float* ws_decay;    // (pieces, H): sum of log a over a piece
+  float* ws_state;    // (parts, H, P, N): a piece's own state, then the state that enters it
+  float* ws_decay;    // (parts, H): sum of log a over a piece
   int H, HP, G;       // heads, head dim, groups
   int nquad;          // workgroups per group of heads
   int softplus, euler;
 };
+
+// The workspace's parts of a cut sequence s that starts in block b of 2^shift tokens: one per piece from here
+// on.  They end before the next cut sequence's begin, whose block is at least one and as many as there are full
+// pieces further; all are below blocks + min(sequences, blocks), so that short sequences take none.
+__device__ __forceinline__ int64_t part_of(int64_t b, int64_t s) { return b + min(b, s); }
 
 constexpr float kMild = 96.0f, kLeast = -256.0f;
 constexpr int kWaves = 4;   // units of 32 channels per workgroup
@@ -172,7 +177,7 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
   const int64_t s = run.s, t_first = run.start + (run.k << a.shift);
   const int64_t t_end = min(run.stop, t_first + ((int64_t)1 << a.shift));   // (no overflow: shift <= 62, t_first 0 .. total)
   const bool last = t_end == run.stop, alone = last && run.k == 0;
-  const int64_t v = (run.start >> a.shift) + s + run.k;   // the piece's part of the workspace
+  const int64_t v = part_of(run.start >> a.shift, s) + run.k;   // the piece's part of the workspace
   const int64_t nchunk = (t_end - t_first + kQ - 1) / kQ;
 
   const int64_t unit_state = ((int64_t)h * a.HP + p0) * N, row_state = (int64_t)a.H * a.HP * N;
@@ -532,7 +537,7 @@ __global__ __launch_bounds__(256) void ssd_fold_kernel(VArgs a, int N) {
   const int h = (int)(e / (uint32_t)(a.HP * N));
   const Run run = find_run<true>(q, blockIdx.y, a.shift);
   if (run.s < 0 || run.k != 0) return;
-  const int64_t s = run.s, v0 = (run.start >> a.shift) + s, slot = seq_slot(q, s);
+  const int64_t s = run.s, v0 = part_of(run.start >> a.shift, s), slot = seq_slot(q, s);
   const int64_t n = (run.stop - run.start + ((int64_t)1 << a.shift) - 1) >> a.shift;
   float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
   if (slot >= 0 && seq_position(q, s) > 0 && in) f = *reinterpret_cast<const float4*>(a.state + slot * row_state + e);
@@ -611,9 +616,9 @@ SsdVarlenPlan make_ssd_varlen_plan(int64_t nseq, int64_t total, int64_t nheads, 
   if (!p.cut) p.shift = 62;   // every sequence is one piece, however long it is
   p.pieces = (total >> p.shift) + nseq;   // piece numbers end below that
   if (p.cut) {
-    const size_t state = (size_t)p.pieces * nheads * headdim * dstate * 4;
-    p.off_decay = (state + 255) / 256 * 256;
-    p.ws_total = p.off_decay + ((size_t)p.pieces * nheads * 4 + 255) / 256 * 256;
+    const size_t parts = (size_t)((total >> p.shift) + std::min(nseq, total >> p.shift));
+    p.off_decay = (parts * nheads * headdim * dstate * 4 + 255) / 256 * 256;
+    p.ws_total = p.off_decay + (parts * nheads * 4 + 255) / 256 * 256;
   }
   return p;
 }

@@ -364,6 +364,17 @@ def test_ssd_new_requests_ignore_what_their_slot_holds():
     assert torch.equal(y, y2) and torch.equal(sd, sd2)
 
 
+@pytest.mark.parametrize("lens", [[1] * 300 + [1500] + [1] * 200 + [640, 65, 129] + [2] * 100, [64, 65, 64, 130, 1, 128, 129] * 4 + [1000]],
+                         ids=["long_among_short", "around_a_piece"])
+def test_ssd_short_and_cut_sequences_in_one_call(lens):
+    r = Rng(len(lens))
+    c = ssd_case(r, lens, 2, 64, 64, 1, (0.0001, 0.01))
+    n = len(lens)
+    state, slots, pos = r(n, 2, 64, 64), r.slots(n, n), i64([[3, 0, 90][i % 3] for i in range(n)])
+    y, sd, ref = run_ssd(c, lens, state, slots, pos, True, True, False)
+    check_ssd(lens, y, sd, ref)
+
+
 def test_ssd_rows_outside_are_left():
     r = Rng(7)
     c = ssd_case(r, [100], 2, 64, 64, 1)

@@ -84,6 +84,13 @@ def test_ssd_workspace(lib):
         assert ssd(lib, ws=P + 128, **big) == EWS
 
 
+def test_ssd_workspace_does_not_grow_with_short_sequences(lib):
+    f = lib.mamba_ssd_fwd_varlen_workspace_size
+    state = 64 * 64 * 128 * 4
+    # one prompt of 4096 tokens beside 4000 single ones: as many states as the tokens have pieces of 64, twice
+    assert state * 32 <= f(4001, 8096, 64, 64, 128, 1, 0) <= (state + 64 * 4) * 2 * (8096 // 64) + 512
+
+
 def step(lib, xbc=P, dt=P, A=P, cw=P, cb=None, ring=P, state=P, slots=P, pos=P, D=None, z=None, bias=None, y=P, batch=3,
          H=4, hd=64, N=128, G=1, K=4, nslots=4, xs=512, ds=4, zs=256, io=1, flags=1):
     return lib.mamba_ssd_step(xbc, dt, A, cw, cb, ring, state, slots, pos, D, z, bias, y, batch, H, hd, N, G, K, nslots, xs, ds,
