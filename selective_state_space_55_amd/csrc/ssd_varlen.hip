@@ -19,10 +19,11 @@
 // one sequence, whose chunks it walks.  The order of an MFMA's k index is free as long as both
 // operands agree, so what an accumulator holds (lane = column, rows in runs of four) is an operand
 // as it stands, and neither S nor M passes through LDS:
-//   S^T C^T  S (lane = channel, k = state, in accumulator order), split into bf16 hi + lo (~2^-17),
+//   S^T C^T  S (lane = channel, k = state, in accumulator order), split into bf16 hi + lo (2^-15 at the most),
 //            times C, whose LDS rows are stored in that order
 //   M        (B C^T)[j][i], lane = token i, comes from LDS once per workgroup; masked and decayed, it
-//            is the right operand of X^T M^T
+//            is the right operand of X^T M^T, in bf16 hi + lo as S (one bf16 part alone, 2^-8 of each term, would add
+//            an error like that of y's own rounding; the second costs 4% of the time)
 //   X, B     as the operands of X^T M^T and of the state update, by transposing LDS reads in
 //            accumulator order of the tokens; the scaled x is split into three bf16 parts by
 //            truncation (8 bits each: exact), so that the state keeps fp32's accuracy over a long prompt
@@ -422,19 +423,24 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
       for (int i = 0; i < 2; ++i) {
         const int tok = i * 32 + l32;
         const float ci = cum2[tok], ei = __builtin_amdgcn_exp2f(ci);
-        auto add_x = [&](int jb, const uint32_t (&mw)[8]) {
+        // + X^T M^T, eight rows of M at a time, in two bf16 parts (all of a tile's at once do not fit the registers); on
+        // the diagonal, tokens behind i, whose bits may be anything, become 0
+        uint32_t mh[4], ml[4];
+        auto add_x = [&](int jb, int k, const float (&f)[4]) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            y[i] = mfma(xf[2 * jb + k], __builtin_bit_cast(bf16x8, make_uint4(mw[4 * k], mw[4 * k + 1], mw[4 * k + 2], mw[4 * k + 3])), y[i]);
-        };
-        // on the diagonal, tokens behind i, whose bits may be anything, become 0
-        auto pack4 = [&](uint32_t (&mw)[8], int k, bool diagonal, const float (&f)[4]) {
-          mw[2 * k] = pack_bf16x2(f[0], f[1]) & (diagonal ? causal[2 * k] : ~0u);
-          mw[2 * k + 1] = pack_bf16x2(f[2], f[3]) & (diagonal ? causal[2 * k + 1] : ~0u);
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t mask = jb == i ? causal[2 * k + j] : ~0u;
+            const float v0 = f[2 * j], v1 = f[2 * j + 1];
+            mh[2 * (k & 1) + j] = hi16x2(v0, v1) & mask;
+            ml[2 * (k & 1) + j] = pack_bf16x2(v0 - trunc16(v0), v1 - trunc16(v1)) & mask;
+          }
+          if (k & 1) {
+            y[i] = mfma(xf[2 * jb + k / 2], __builtin_bit_cast(bf16x8, make_uint4(ml[0], ml[1], ml[2], ml[3])), y[i]);
+            y[i] = mfma(xf[2 * jb + k / 2], __builtin_bit_cast(bf16x8, make_uint4(mh[0], mh[1], mh[2], mh[3])), y[i]);
+          }
         };
         if (mild) {
           auto tile = [&](int jb, float each) {
-            uint32_t mw[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const float4 gv = gl[((i + jb) * 4 + k) * 64];
@@ -444,9 +450,8 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
 #pragma unroll
                 for (int r = 0; r < 4; ++r) f[r] *= each;
               }
-              pack4(mw, k, jb == i, f);
+              add_x(jb, k, f);
             }
-            add_x(jb, mw);
           };
           tile(0, 1.0f);
 #pragma unroll
@@ -457,7 +462,6 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
           for (int r = 0; r < 16; ++r) y[i][r] *= ei;
 #pragma unroll
           for (int jb = 0; jb <= i; ++jb) {
-            uint32_t mw[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int j0 = jb * 32 + 8 * k + 4 * h32;
@@ -473,9 +477,8 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
 #pragma unroll
                 for (int r = 0; r < 4; ++r) f[r] = __uint_as_float(__float_as_uint(f[r]) ^ sa[r]);
               }
-              pack4(mw, k, jb == i, f);
+              add_x(jb, k, f);
             }
-            add_x(jb, mw);
           }
         }
         // + D x, gate, and out: channels 8 k + 4 h .. + 3 of the lane's token
