@@ -36,3 +36,25 @@ def test_ssd_rounds_nothing_but_its_output(case):
     n = len(lens)
     y, _, ref = run_ssd(c, lens, r(n, H, P, N), r.slots(n, n), i64([[5, 0, 1][i % 3] for i in range(n)]), gated, softplus, False)
     close("y", y, ref[0], 2.0 ** -8 * ref[0].abs() + 2.0 ** -13 * ref[2])
+
+
+# ---------------------------------------------------------------- packed SSM: large products
+
+
+@pytest.mark.parametrize("scale", [4, 20, 36])
+@pytest.mark.parametrize("log2_decay", [8, 30, 47, 49, 63, 65, 92, 95, 97, 200])
+def test_ssd_large_products_at_any_decay(log2_decay, scale):
+    """Terms x (C.B) w of up to 2^22, 2^54 and 2^86 and a decay of 2^-log2_decay over each 32 tokens: the outputs are far inside
+    fp32's range, so no factor that a chunk is computed with may leave it either."""
+    lens = [200, 64]
+    r = Rng(log2_decay)
+    c = ssd_case(r, lens, 3, 64, 128, 1)
+    c["A_log"] = torch.log(torch.tensor([16.0, 4.0, 1.0]))
+    delta = log2_decay * 0.6931471805599453 / 32 / torch.tensor([16.0, 4.0, 1.0])
+    c["dt"], c["dt_bias"] = c["dt"] * 0, torch.log(torch.expm1(delta))
+    c["x"] = c["x"] * 2.0 ** scale
+    c["B"], c["C"] = c["B"] * 2.0 ** (scale / 2 + 4), c["C"] * 2.0 ** (scale / 2 + 4)
+    say(f"ssd decay 2^-{log2_decay} products of 2^{2 * scale + 11}")
+    for gated in (False, True):
+        y, sd, ref = run_ssd(c, lens, r(2, 3, 64, 128), i64([1, 0]), i64([9, 0]), gated, True, False)
+        check_ssd(lens, y, sd, ref)
