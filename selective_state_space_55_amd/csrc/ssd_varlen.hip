@@ -418,6 +418,22 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
       load_bc(t_next);
       lds_barrier();   // B C^T
       if (!live) continue;
+      // A NaN or infinity in a token's x makes all of its channel's state NaN, so one state per channel tells of it.
+      // In M's products it would meet the zeros in front of the token; it is taken out of them and put back below.
+      const bool bad = __ballot(!(fabsf(S[0][0]) < INFINITY)) != 0;
+      if (bad) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint4 v = __builtin_bit_cast(uint4, xf[k]);
+          uint32_t xw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if ((xw[j] & 0x7f80u) == 0x7f80u) xw[j] &= 0xffff0000u;
+            if ((xw[j] & 0x7f800000u) == 0x7f800000u) xw[j] &= 0xffffu;
+          }
+          xf[k] = __builtin_bit_cast(bf16x8, make_uint4(xw[0], xw[1], xw[2], xw[3]));
+        }
+      }
       const auto ry = rows(a.y + ch, t0, y_stride, 32);
       const uint16_t* const xrow = Xs + anew(l32 * L::kRowX + 4 * h32);
       const float4* const gl = Gs + anew(lane);
@@ -480,6 +496,17 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
                 for (int r = 0; r < 4; ++r) f[r] = __uint_as_float(__float_as_uint(f[r]) ^ sa[r]);
               }
               add_x(jb, k, f);
+            }
+          }
+        }
+        if (bad) {   // NaN from a non-finite token on
+          for (int j = 0; j < 32 * i + 32; ++j) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint2 xv = *reinterpret_cast<const uint2*>(Xs + j * L::kRowX + 4 * h32 + 8 * k);
+              const float xj[4] = {bf16_lo(xv.x), bf16_hi(xv.x), bf16_lo(xv.y), bf16_hi(xv.y)};
+#pragma unroll
+              for (int r = 0; r < 4; ++r) y[i][4 * k + r] = fmaf(j <= tok ? xj[r] : 0.0f, 0.0f, y[i][4 * k + r]);
             }
           }
         }

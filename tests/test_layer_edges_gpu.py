@@ -58,3 +58,64 @@ def test_ssd_large_products_at_any_decay(log2_decay, scale):
     for gated in (False, True):
         y, sd, ref = run_ssd(c, lens, r(2, 3, 64, 128), i64([1, 0]), i64([9, 0]), gated, True, False)
         check_ssd(lens, y, sd, ref)
+
+
+# ---------------------------------------------------------------- packed SSM: non-finite tokens
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("steps,softplus", [((0.001, 0.1), True), ((2.0, 6.0), True), ((0.001, 0.1), False)], ids=["mild", "steep", "signed"])
+def test_ssd_a_bad_token_reaches_no_earlier_one(steps, softplus, bad):
+    """A NaN or infinity in x of one channel: that channel's earlier tokens, the other channels and the other sequence are
+    what they are without it, to the last bit; its own token and the later ones are not finite."""
+    lens, H, P, N = [150, 90], 2, 64, 128
+    r = Rng(3)
+    c = ssd_case(r, lens, H, P, N, 1, steps)
+    if not softplus:
+        c["dt"], c["dt_bias"] = (c["dt"].float() * 0.01).bfloat16(), c["dt_bias"] * 0
+    clean = mscan_ssd(c, lens, softplus)
+    for at in (0, 20, 31, 32, 45, 63, 64, 149):
+        x = c["x"].clone()
+        x[at, 1, 40] = bad
+        y, state = mscan_ssd(dict(c, x=x), lens, softplus)
+        want = clean[0].clone()
+        want[at:150, 1, 40] = float("nan")
+        lost = torch.isnan(want)
+        assert torch.equal(y[~lost], want[~lost]), at
+        assert not torch.isfinite(y[lost].float()).any(), at
+        assert not torch.isfinite(state[0, 1, 40]).any() and torch.equal(state[1], clean[1][1])
+        state[0, 1, 40] = clean[1][0, 1, 40]
+        assert torch.equal(state, clean[1])
+
+
+@pytest.mark.parametrize("what", ["B", "C", "dt", "z"])
+@pytest.mark.parametrize("steps", [(0.001, 0.1), (2.0, 6.0)], ids=["mild", "steep"])
+def test_ssd_a_bad_token_of_any_input(steps, what):
+    """NaN in B (later tokens of all heads), dt (later tokens of a head), C or z (its own token)."""
+    lens, H, P, N = [150, 90], 2, 64, 128
+    r = Rng(4)
+    c = ssd_case(r, lens, H, P, N, 1, steps)
+    clean = mscan_ssd(c, lens, True)
+    for at in (20, 45, 149):
+        t = c[what].clone()
+        t[at, -1] = float("nan")
+        y, state = mscan_ssd(dict(c, **{what: t}), lens, True)
+        want, keep = clean[0].clone(), clean[1].clone()
+        if what in ("B", "dt"):
+            heads = slice(None) if what == "B" else slice(1, 2)
+            want[at:150, heads] = float("nan")
+            keep[0, heads] = float("nan")
+        else:
+            want[at, slice(None) if what == "C" else slice(1, 2)] = float("nan")
+        assert torch.equal(torch.isnan(y), torch.isnan(want)) and torch.equal(torch.isnan(state), torch.isnan(keep))
+        assert torch.equal(torch.nan_to_num(y), torch.nan_to_num(want)) and torch.equal(torch.nan_to_num(state), torch.nan_to_num(keep))
+
+
+def mscan_ssd(c, lens, softplus):
+    state = torch.zeros(len(lens), c["x"].shape[1], c["x"].shape[2], c["B"].shape[2], device=DEV)
+    n = len(lens)
+    y = mscan.ssd_fwd_varlen(dev(c["x"]), dev(c["dt"]), dev(c["A_log"]), dev(c["B"]), dev(c["C"]), dev(i64(packed(lens))), D=dev(c["D"]),
+                             z=dev(c["z"]), dt_bias=dev(c["dt_bias"]), state=state, slots=dev(i64(list(range(n)))),
+                             positions=dev(i64([0] * n)), dt_softplus=softplus, max_seqlen=max(lens))
+    torch.cuda.synchronize()
+    return y, state
