@@ -1,5 +1,5 @@
-// packed.h -- device-side lookup of packed sequences and request slots, shared
-// by the SSD layer's kernels.
+// packed.h -- device-side lookup of packed sequences and request slots, and the
+// limits of the heads' decay rates, shared by the SSD layer's kernels.
 //
 // Offsets, slots and positions are the caller's device memory, which the host
 // cannot check: offsets are clamped to [0, total], a slot outside [0, nslots)
@@ -88,5 +88,13 @@ __device__ __forceinline__ int64_t seq_position(const Packed& p, int64_t s) {
   const int64_t v = p.positions[s];
   return v < 0 ? 0 : min(v, (int64_t)1 << 62);   // room for the call's tokens
 }
+
+// A = -exp(A_log) in products with Delta is held at this, where exp(Delta A) is 0 for any Delta that is not: an
+// infinite A would make Delta = 0 a NaN
+constexpr float kFastest = -0x1p126f;
+
+// (exp(Delta A) - 1) / A is Delta where |Delta A| is below this, to 2^-26 of it; it is not divided
+// there, since A may be too small a number to divide by
+constexpr float kTinyStep = 0x1p-25f;
 
 }  // namespace mscan

@@ -25,6 +25,7 @@
 // rounding error shrinks with Delta |A|.
 #include "internal.h"
 #include "io.h"
+#include "packed.h"
 
 #include <algorithm>
 
@@ -109,11 +110,11 @@ __global__ __launch_bounds__(256) void ssd_step_kernel(StArgs a) {
     else ux[i - 2 * N] = acc;
     if (i >= 2 * N || hs == g * (a.H / a.G) * a.nslice) ring[now * a.width + c] = raw;
   }
-  const float A = -expf(a.A_log[h]);
+  const float rate = -expf(a.A_log[h]), A = fmaxf(rate, kFastest);
   const float dr = Io<IoT>::load1(static_cast<const IoT*>(a.dt) + row * a.dt_stride + h) + (a.dt_bias ? a.dt_bias[h] : 0.0f);
   const float delta = a.softplus ? softplus_log2e(dr) * 0.6931471805599453f : dr;
   const float m = expm1f(delta * A);
-  const float wt = a.euler ? delta : A != 0.0f ? m / A : delta;
+  const float wt = a.euler || fabsf(delta * A) < kTinyStep ? delta : m / rate;
   __syncthreads();
 
   const float4 b = *reinterpret_cast<const float4*>(ub + n4), cc = *reinterpret_cast<const float4*>(uc + n4);

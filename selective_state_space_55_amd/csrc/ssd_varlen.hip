@@ -168,8 +168,8 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
   const bool live = ug < upg;                               // the group's last workgroup may have fewer
   const int u = g * upg + (live ? ug : 0);
   const int h = u / tiles, p0 = (u % tiles) * 32;
-  const float Ah = -expf(a.A_log[h]);
-  const float A2 = Ah * 1.4426950408889634f, iA = 1.0f / Ah;   // iA is not used where Ah = 0
+  const float rate = -expf(a.A_log[h]), Ah = fmaxf(rate, kFastest);
+  const float A2 = Ah * 1.4426950408889634f, iA = 1.0f / rate;
   const float Dh = a.D ? a.D[h] : 0.0f;
   const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
   const Packed& q = a.seq;
@@ -260,7 +260,7 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
     delta = t0 + lane < t_end ? delta : 0.0f;
     // 2^kLeast takes any fp32 state to nothing; a larger decay would only cost the sums behind it their last bits
     const float la2 = fmaxf(delta * A2, kLeast);
-    const float wj = a.euler || Ah == 0.0f ? delta : expm1_small(delta * Ah) * iA;
+    const float wj = a.euler || fabsf(delta * Ah) < kTinyStep ? delta : expm1_small(delta * Ah) * iA;
     const float cum = wave_prefix_sum(la2);
     const float rev = wave_prefix_sum(__shfl(la2, 63 - lane));   // from the chunk's end
     const float from = __shfl(rev, 63 - lane);                   // token lane .. the last

@@ -119,3 +119,38 @@ def mscan_ssd(c, lens, softplus):
                              positions=dev(i64([0] * n)), dt_softplus=softplus, max_seqlen=max(lens))
     torch.cuda.synchronize()
     return y, state
+
+
+# ---------------------------------------------------------------- decays at the ends of A's range
+
+
+A_LOG = [-200.0, -100.0, -95.0, -88.0, -60.0, 60.0, 87.0, 92.0]
+
+
+@pytest.mark.parametrize("euler", [False, True])
+def test_ssd_decay_rates_of_any_size(euler):
+    """exp(A_log) under the smallest normal number or over the largest one: (exp(Delta A) - 1) / A is Delta there, or 0."""
+    lens = [100, 3]
+    r = Rng(29)
+    c = ssd_case(r, lens, 8, 32, 64, 1)
+    c["A_log"] = torch.tensor(A_LOG)
+    c["dt"][4::9] = -150.0   # a step of 0
+    y, sd, ref = run_ssd(c, lens, r(2, 8, 32, 64), i64([1, 0]), i64([9, 0]), True, True, euler)
+    close("y", y, ref[0], 2.0 ** -8 * ref[0].abs() + (2.0 ** -8 + 2.0 ** -14) * ref[2] + 2.0 ** -126)
+    close("state", sd, ref[1], (2.0 ** -16 + 2 * 2.0 ** -21) * ref[3] + 2.0 ** -126)
+
+
+@pytest.mark.parametrize("euler", [False, True])
+def test_step_decay_rates_of_any_size(euler):
+    r = Rng(30)
+    c = step_case(r, 3, 8, 32, 64, 1, 4, torch.float32)
+    c["A_log"] = torch.tensor(A_LOG)
+    c["dt"][1] = -150.0
+    ring, state, pos = r(3, 4, c["xbc"].shape[1]), r(3, 8, 32, 64), i64([4, 9, 0])
+    args = [c[k] for k in ("xbc", "dt", "A_log", "conv_weight")]
+    y64, _, st64, ya, sa = layer.ssd_step(*args, ring, state, pos, None, c["D"], c["z"], c["dt_bias"], c["conv_bias"], True, euler)
+    rd, sd = dev(ring.clone(), state.clone())
+    y = mscan.ssd_step(*dev(*args), rd, sd, dev(pos), D=dev(c["D"]), z=dev(c["z"]), dt_bias=dev(c["dt_bias"]), conv_bias=dev(c["conv_bias"]),
+                       discretization="euler" if euler else "zoh")
+    close("y", y, y64, 2.0 ** -24 * y64.abs() + 2.0 ** -15 * (ya + 1))
+    close("state", sd, st64, 2.0 ** -17 * (sa + 1))
