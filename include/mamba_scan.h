@@ -485,7 +485,8 @@ int mamba_ssd_step(const void* xbc, const void* dt, const float* A_log, const fl
  *                             that keeps the block's magnitudes within 448; 1 where all values are 0
  *   rstd         (rows)       f32             OUT, NULL: not written
  * Sizes: rows >= 0, dim >= 1, eps >= 0 (else MAMBA_SCAN_ERR_UNSUPPORTED); the launch's work-items (at most rows * 1024) below 2^32.  A row with a NaN or an
- * Inf has NaNs in y.
+ * Inf has NaNs in y.  The squares of a finite row may leave fp32's range (then they are summed scaled by a power of two); an rstd that
+ * does is stored as Inf.
  */
 int mamba_rms_norm_fwd(const void* x, const void* residual, const float* weight, float eps, void* residual_out,
                        void* y, void* scales, float* rstd, int64_t rows, int64_t dim, int io_dtype,

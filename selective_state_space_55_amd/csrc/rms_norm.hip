@@ -156,9 +156,20 @@ __device__ __forceinline__ int block_exp(float top) {
   return max(-127, min(127, k));
 }
 
+// A row whose mean square is outside of this range may have squares that fp32 does not hold (below it, squares that
+// have lost bits matter): it is summed again, scaled by the power of two that row_exp gives.
+__device__ __forceinline__ bool mean_square_ok(float ms) { return ms >= 0x1p-100f && ms < INFINITY; }
+
+// k, so that the row's largest magnitude and sqrt(eps) are below 1 after a scaling by 2^-k and one of them is at least
+// 1/2; 0 where there is nothing to scale (all 0, or an Inf, whose row is NaN)
+__device__ __forceinline__ int row_exp(float top, float eps) {
+  const float m = fmaxf(top, sqrtf(eps));
+  return m > 0.0f && m < INFINITY ? __builtin_amdgcn_frexp_expf(m) : 0;
+}
+
 template <typename IoT, int W, int T, int V>
 __global__ __launch_bounds__(threads_of(T)) void rms_norm_fwd_kernel(NArgs a) {
-  __shared__ float red[2][16];
+  __shared__ float red[4][16];
   const int64_t row = (int64_t)blockIdx.x * (threads_of(T) / T) + threadIdx.x / T;
   const int t = threadIdx.x % T;
   if (row >= a.rows) return;   // whole waves (T = 64) or no workgroup at all
@@ -207,9 +218,26 @@ __global__ __launch_bounds__(threads_of(T)) void rms_norm_fwd_kernel(NArgs a) {
 #pragma unroll
     for (int j = 0; j < W; ++j) ss = fmaf(r[v][j], r[v][j], ss);
   ss = row_reduce<T, false>(ss, red[0]);
-  const float rstd = 1.0f / sqrtf(ss / (float)a.dim + a.eps);
-  if (a.rstd && t == 0) a.rstd[row] = rstd;
-  float top = 0.0f;
+  float ms = ss / (float)a.dim + a.eps, top = 0.0f;
+  int k = 0;   // r stands for r 2^-k, rstd for rstd 2^k
+  if (!mean_square_ok(ms)) {   // all of the row's lanes
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int j = 0; j < W; ++j) top = fmaxf(top, fabsf(r[v][j]));
+    k = row_exp(row_reduce<T, true>(top, red[2]), a.eps);
+    top = ss = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        r[v][j] = ldexpf(r[v][j], -k);
+        ss = fmaf(r[v][j], r[v][j], ss);
+      }
+    ms = row_reduce<T, false>(ss, red[3]) / (float)a.dim + ldexpf(a.eps, -2 * k);
+  }
+  const float rstd = 1.0f / sqrtf(ms);
+  if (a.rstd && t == 0) a.rstd[row] = ldexpf(rstd, -k);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int vec = v * T + t;
@@ -227,13 +255,13 @@ __global__ __launch_bounds__(threads_of(T)) void rms_norm_fwd_kernel(NArgs a) {
       float m = 0.0f;
 #pragma unroll
       for (int j = 0; j < W; ++j) m = fmaxf(m, fabsf(r[v][j]));
-      const int k = block_exp(block_max<W>(m));
+      const int b = block_exp(block_max<W>(m));
       if (vec < nvec) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) r[v][j] = ldexpf(r[v][j], -k);
+        for (int j = 0; j < W; ++j) r[v][j] = ldexpf(r[v][j], -b);
         store_fp8<W>(a.y, base + (int64_t)vec * W, r[v]);
         if (vec % (32 / W) == 0)
-          static_cast<uint8_t*>(a.scales)[row * ((a.dim + 31) / 32) + vec / (32 / W)] = (uint8_t)(k + 127);
+          static_cast<uint8_t*>(a.scales)[row * ((a.dim + 31) / 32) + vec / (32 / W)] = (uint8_t)(b + 127);
       }
     }
   }
@@ -254,12 +282,12 @@ __global__ __launch_bounds__(threads_of(T)) void rms_norm_fwd_kernel(NArgs a) {
   }
 }
 
-// Rows of any length, one workgroup each, read once for the sum of squares, once for the
-// largest value (row scale) and once for the output.  x and the residual are read
+// Rows of any length, one workgroup each, read once for the sum of squares (twice more where it has to be scaled), once for
+// the largest value (row scale) and once for the output.  x and the residual are read
 // for the last time by the thread that then writes r there, so res_out may be res.
 template <typename IoT>
 __global__ __launch_bounds__(kThreads) void rms_norm_fwd_long_kernel(NArgs a) {
-  __shared__ float red[8];
+  __shared__ float red[4][4];
   const int64_t row = blockIdx.x, base = row * a.dim;
   const int t = threadIdx.x;
   auto value = [&](int64_t c) {
@@ -273,14 +301,27 @@ __global__ __launch_bounds__(kThreads) void rms_norm_fwd_long_kernel(NArgs a) {
     const float v = value(c);
     ss = fmaf(v, v, ss);
   }
-  ss = row_reduce<kThreads, false>(ss, red);
-  const float rstd = 1.0f / sqrtf(ss / (float)a.dim + a.eps);
-  if (a.rstd && t == 0) a.rstd[row] = rstd;
+  ss = row_reduce<kThreads, false>(ss, red[0]);
+  float ms = ss / (float)a.dim + a.eps;
+  int k = 0;
+  if (!mean_square_ok(ms)) {
+    float top = 0.0f;
+    for (int64_t c = t; c < a.dim; c += kThreads) top = fmaxf(top, fabsf(value(c)));
+    k = row_exp(row_reduce<kThreads, true>(top, red[2]), a.eps);
+    ss = 0.0f;
+    for (int64_t c = t; c < a.dim; c += kThreads) {
+      const float v = ldexpf(value(c), -k);
+      ss = fmaf(v, v, ss);
+    }
+    ms = row_reduce<kThreads, false>(ss, red[3]) / (float)a.dim + ldexpf(a.eps, -2 * k);
+  }
+  const float rstd = 1.0f / sqrtf(ms);
+  if (a.rstd && t == 0) a.rstd[row] = ldexpf(rstd, -k);
   float s = 1.0f;
   if (a.out == kNormRow8) {
     float top = 0.0f;
-    for (int64_t c = t; c < a.dim; c += kThreads) top = fmaxf(top, fabsf(value(c) * rstd * a.w[c]));
-    s = row_scale(row_reduce<kThreads, true>(top, red + 4));
+    for (int64_t c = t; c < a.dim; c += kThreads) top = fmaxf(top, fabsf(ldexpf(value(c), -k) * rstd * a.w[c]));
+    s = row_scale(row_reduce<kThreads, true>(top, red[1]));
     if (t == 0) static_cast<float*>(a.scales)[row] = s;
   }
   // whole waves run the same trips: a 32-column block is spread over 32 lanes
@@ -288,11 +329,11 @@ __global__ __launch_bounds__(kThreads) void rms_norm_fwd_long_kernel(NArgs a) {
     const int64_t c = c0 + t;
     const bool in = c < a.dim;
     const float r = in ? value(c) : 0.0f;
-    float y = in ? r * rstd * a.w[c] : 0.0f;
+    float y = in ? ldexpf(r, -k) * rstd * a.w[c] : 0.0f;
     if (a.out == kNormMx8) {
-      const int k = block_exp(block_max<1>(fabsf(y)));
-      y = ldexpf(y, -k);
-      if (in && (c & 31) == 0) static_cast<uint8_t*>(a.scales)[row * ((a.dim + 31) / 32) + (c >> 5)] = (uint8_t)(k + 127);
+      const int b = block_exp(block_max<1>(fabsf(y)));
+      y = ldexpf(y, -b);
+      if (in && (c & 31) == 0) static_cast<uint8_t*>(a.scales)[row * ((a.dim + 31) / 32) + (c >> 5)] = (uint8_t)(b + 127);
     }
     if (!in) continue;
     if (a.res) {

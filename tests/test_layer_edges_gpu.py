@@ -154,3 +154,48 @@ def test_step_decay_rates_of_any_size(euler):
                        discretization="euler" if euler else "zoh")
     close("y", y, y64, 2.0 ** -24 * y64.abs() + 2.0 ** -15 * (ya + 1))
     close("state", sd, st64, 2.0 ** -17 * (sa + 1))
+
+
+# ---------------------------------------------------------------- norm: squares out of fp32's range
+
+
+@pytest.mark.parametrize("dim", [96, 100, 768, 4096, 5001, 16400])
+@pytest.mark.parametrize("io", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("eps", [1e-5, 0.0, 1e-40])
+def test_norm_of_rows_whose_squares_leave_the_range(dim, io, eps):
+    """The mean of the squares overflows fp32 or falls under it, the norm does not."""
+    r = Rng(dim)
+    x, w = r(9, dim), 1 + r(dim, scale=0.1)
+    for i, size in enumerate([3e18, 1e19, 1e30, 1e38, 1e-19, 1e-25, 1e-37, 1e-41]):
+        x[i] = x[i].clamp(-3, 3) * size
+    x[8], x[8, 5] = 0, 3e38
+    x = x.to(io)
+    y64, _, rstd64 = layer.rms_norm(x, w, None, eps)
+    seen = rstd64 < 3e38   # past that rstd is infinite in fp32; y is not
+    say(f"norm of extreme rows, dim {dim} {io} eps {eps}")
+    for quant in (None, "row", "mx"):
+        got = mscan.rms_norm_fwd(*dev(x, w), eps=eps, quant=quant, return_rstd=True)
+        torch.cuda.synchronize()
+        got = list(got)
+        y = got.pop(0)
+        if quant is None:
+            close("y", y, y64, (HALF[io] + F32) * y64.abs() + 2.0 ** -133)   # half the smallest bf16
+        else:
+            scale = got.pop(0).float().cpu().double()
+            each = scale[:, None] if quant == "row" else scale.repeat_interleave(32, 1)[:, :dim]
+            close("q", y.cpu().float().double() * each, y64, (2.0 ** -4 + F32) * y64.abs() + 2.0 ** -10 * each)
+        close("rstd", got.pop(0)[seen.to(DEV)], rstd64[seen], F32 * rstd64[seen])
+
+
+def test_norm_with_a_residual_of_rows_whose_squares_leave_the_range():
+    r = Rng(3)
+    for dim in (512, 77, 16400):
+        x, res, w = r(4, dim), r(4, dim), 1 + r(dim, scale=0.1)
+        x[0], res[0], x[1], res[1] = x[0] * 1e37, res[0] * 2e37, x[1] * 1e-30, res[1] * 1e-28
+        for rt in (torch.float32, torch.bfloat16):
+            xb, rb = x.bfloat16(), res.to(rt)
+            y64, r64, rstd64 = layer.rms_norm(xb, w, rb, 0.0)
+            y, ro, rstd = mscan.rms_norm_fwd(*dev(xb, w, rb), eps=0.0, return_rstd=True)
+            close("y", y, y64, (2.0 ** -8 + F32) * y64.abs())
+            close("r", ro, r64, (HALF[rt] + 2.0 ** -24) * r64.abs())
+            close("rstd", rstd, rstd64, F32 * rstd64)
