@@ -199,3 +199,84 @@ def test_norm_with_a_residual_of_rows_whose_squares_leave_the_range():
             close("y", y, y64, (2.0 ** -8 + F32) * y64.abs())
             close("r", ro, r64, (HALF[rt] + 2.0 ** -24) * r64.abs())
             close("rstd", rstd, rstd64, F32 * rstd64)
+
+
+# ---------------------------------------------------------------- packed SSM: pieces of several chunks
+
+
+def ssd_on_gpu(c, lens, state, slots, pos, softplus, euler=False):
+    """layer.ssd_varlen's recurrence in fp64 on the device, for prompts of many tokens."""
+    g = {k: None if v is None else v.to(DEV).double() for k, v in c.items()}
+    a, w = (v.to(DEV) for v in layer._decay(c["dt"], c["A_log"], c["dt_bias"], softplus, euler))
+    H, G = c["x"].shape[1], c["B"].shape[1]
+    y, ya = torch.zeros_like(g["x"]), torch.zeros_like(g["x"])
+    st = state.to(DEV).double()
+    sa = st.abs()
+    cu = packed(lens)
+    for s in range(len(lens)):
+        if cu[s] == cu[s + 1]:
+            continue
+        h = st[slots[s]] * (1.0 if pos[s] > 0 else 0.0)
+        ha = h.abs()
+        for t in range(cu[s], cu[s + 1]):
+            B, C = (g[k][t].repeat_interleave(H // G, 0)[:, None, :] for k in ("B", "C"))
+            wx, at = (w[t][:, None] * g["x"][t])[:, :, None], a[t][:, None, None]
+            h = torch.addcmul(at * h, wx, B)
+            ha = torch.addcmul(at * ha, wx.abs(), B.abs())
+            y[t] = (h * C).sum(2)
+            ya[t] = (ha * C.abs()).sum(2)
+        st[slots[s]], sa[slots[s]] = h, ha
+    Dx = g["D"][:, None] * g["x"]
+    gate = g["z"] / (1 + torch.exp(-g["z"]))
+    return ((y + Dx) * gate).cpu(), st.cpu(), ((ya + Dx.abs()) * gate.abs()).cpu(), sa.cpu()
+
+
+def steps_of(kind, r, H):
+    """Delta: heads that keep everything over a piece, that forget within a chunk or two, or both in turn."""
+    slow, fast = r.uniform(1e-5, 1e-4, H), r.uniform(0.08, 0.3, H)
+    return torch.where(torch.arange(H) % 2 == 0, slow, fast) if kind == "both" else slow if kind == "slow" else fast
+
+
+PIECES = [  # piece, H, P, N, G, lens
+    (128, 32, 32, 64, 32, [4100]),
+    (128, 32, 32, 64, 32, [127, 128, 129, 255, 256, 257, 0, 1, 383, 384, 385, 1795]),
+    (256, 32, 32, 64, 32, [255, 256, 257, 511, 512, 513, 5896]),
+    (128, 32, 32, 64, 8, [16400]),              # four heads in a workgroup
+    (512, 64, 32, 128, 32, [511, 513, 1025, 14351]),
+    (256, 24, 64, 64, 24, [12000]),             # two units of a head in a workgroup
+]
+
+
+@pytest.mark.parametrize("kind", ["slow", "fast", "both", "signed"])
+@pytest.mark.parametrize("case", PIECES, ids=[f"piece{c[0]}G{c[4]}N{c[3]}x{len(c[5])}" for c in PIECES])
+def test_ssd_pieces_of_several_chunks(case, kind):
+    """The first pass over more than one chunk, with and without its early end; the fold over what it leaves out; a main
+    pass that walks several chunks from a state of the workspace."""
+    piece, H, P, N, G, lens = case
+    total, n = sum(lens), len(lens)
+    # the workspace holds a state per part, so its size tells the pieces' length
+    full = total // piece
+    parts = full + min(n, full)
+    got = mscan.ssd_fwd_varlen_workspace_size(n, total, H, P, N, G)
+    want = -(-parts * H * P * N * 4 // 256) * 256 + -(-parts * H * 4 // 256) * 256
+    assert got == want, (got / want, piece)
+    r = Rng(total + len(kind))
+    c = ssd_case(r, lens, H, P, N, G, dt_std=0.3)
+    c["A_log"] = torch.log(r.uniform(8, 16, H))
+    c["dt_bias"] = torch.log(torch.expm1(steps_of(kind if kind != "signed" else "slow", r, H)))
+    if kind == "signed":
+        c["dt"], c["dt_bias"] = (c["dt"].float() * 0.003).bfloat16(), torch.full((H,), 2e-4)
+    state, slots = r(n, H, P, N), r.slots(n, n)
+    pos = i64([[5, 0][i % 2] for i in range(n)])
+    say(f"ssd pieces of {piece}, {kind}, {lens}")
+    ref = ssd_on_gpu(c, lens, state, slots.tolist(), pos.tolist(), kind != "signed")
+    d = {k: v.to(DEV) for k, v in c.items()}
+    got = []
+    for _ in range(2):
+        sd = dev(state.clone())
+        y = mscan.ssd_fwd_varlen(d["x"], d["dt"], d["A_log"], d["B"], d["C"], dev(i64(packed(lens))), D=d["D"], z=d["z"], dt_bias=d["dt_bias"],
+                                 state=sd, slots=dev(slots), positions=dev(pos), dt_softplus=kind != "signed")
+        torch.cuda.synchronize()
+        got.append((y, sd))
+    check_ssd(lens, *got[0], ref)
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
