@@ -247,6 +247,7 @@ hipError_t launch_ssd_step(const SsdStepArgs& a, hipStream_t stream);
 // Multi-head SSM over packed sequences with a state per slot (ssd_varlen.hip), bf16 io.
 struct SsdVarlenPlan {
   int shift;           // pieces of 2^shift tokens, at least 64
+  int whole;           // a sequence of at most 2^whole tokens is one piece; whole >= shift
   bool cut;            // a sequence may have more than one piece: two more passes and a workspace
   int64_t pieces;      // piece numbers (some of them name no piece)
   int64_t quads;       // workgroups per piece

@@ -73,6 +73,7 @@ struct VArgs {
   uint16_t* y;
   int x_stride, dt_stride, b_stride, c_stride, z_stride;
   int shift;          // pieces of 2^shift tokens
+  int whole;          // sequences of at most 2^whole tokens are not cut
   float* ws_state;    // (parts, H, P, N): a piece's own state, then the state that enters it
   float* ws_decay;    // (parts, H): sum of log a over a piece
   int H, HP, G;       // heads, head dim, groups
@@ -175,8 +176,11 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
   const Packed& q = a.seq;
   const Run run = find_run<kAgg>(q, number, a.shift);
   if (run.s < 0) return;   // no such piece; a sequence without tokens leaves its slot as it is
+  const bool cut = run.stop - run.start > (int64_t)1 << a.whole;
+  if (!cut && (kAgg || run.k > 0)) return;   // the main pass's first workgroups walk the whole sequence
   const int64_t s = run.s, t_first = run.start + (run.k << a.shift);
-  const int64_t t_end = min(run.stop, t_first + ((int64_t)1 << a.shift));   // (no overflow: shift <= 62, t_first 0 .. total)
+  // (no overflow: shift <= 62, t_first 0 .. total)
+  const int64_t t_end = cut ? min(run.stop, t_first + ((int64_t)1 << a.shift)) : run.stop;
   const bool last = t_end == run.stop, alone = last && run.k == 0;
   const int64_t v = part_of(run.start >> a.shift, s) + run.k;   // the piece's part of the workspace
   const int64_t nchunk = (t_end - t_first + kQ - 1) / kQ;
@@ -559,15 +563,15 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
 }
 
 // The fold over a sequence's pieces: entry k of its part of ws_state, piece k's own state, becomes the
-// state that enters piece k.  A thread per cut sequence and four states; a cut sequence is found by its
-// first piece's number among the full pieces, so that the grid does not grow with the uncut ones.
+// state that enters piece k.  A thread per cut sequence and four states; a cut sequence is found by the number
+// of its first run of 2^whole tokens among the full ones, so that the grid does not grow with the uncut ones.
 __global__ __launch_bounds__(256) void ssd_fold_kernel(VArgs a, int N) {
   const Packed& q = a.seq;
   const uint32_t row_state = (uint32_t)a.H * a.HP * N;   // at most 2^24 channels x 128 states
   const uint32_t e = (blockIdx.x * 256 + threadIdx.x) * 4;
   const bool in = e < row_state;   // (whole waves look for the sequence)
   const int h = (int)(e / (uint32_t)(a.HP * N));
-  const Run run = find_run<true>(q, blockIdx.y, a.shift);
+  const Run run = find_run<true>(q, blockIdx.y, a.whole);
   if (run.s < 0 || run.k != 0) return;
   const int64_t s = run.s, v0 = part_of(run.start >> a.shift, s), slot = seq_slot(q, s);
   const int64_t n = (run.stop - run.start + ((int64_t)1 << a.shift) - 1) >> a.shift;
@@ -615,7 +619,7 @@ hipError_t run(const VArgs& a, const SsdVarlenPlan& p, hipStream_t s) {
     hipError_t e = launch<N, kAggregate, true>(a, dim3((unsigned)(full * p.quads)), s);
     if (e != hipSuccess) return e;
     const int64_t blocks = ((int64_t)a.H * a.HP * N / 4 + 255) / 256;
-    hipLaunchKernelGGL(ssd_fold_kernel, dim3((unsigned)blocks, full), dim3(256), 0, s, a, N);
+    hipLaunchKernelGGL(ssd_fold_kernel, dim3((unsigned)blocks, (unsigned)(a.seq.total >> a.whole)), dim3(256), 0, s, a, N);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -631,21 +635,25 @@ int64_t quads_of(int64_t nheads, int64_t headdim, int64_t ngroups) { return (nhe
 // Pieces: as many tokens as share them out over two rounds of two workgroups per CU, a power of two
 // (so that a piece number needs no division).  32768 tokens of 28 sequences, 32 workgroups a piece: 435 us in
 // pieces of 1024, 467 in 512, 508 in 2048; 20000 tokens of one sequence, 32 a piece: 225 us in 512, 251 in 256,
-// 238 in 1024; 509 tokens, 12 workgroups a piece: 29 us in 64, 32 in 128, 44 in 256.  Where the sequences fill the GPU by themselves and are
-// that short on average, or are known to be, they are not cut: 16 sequences of 256 tokens, 32 workgroups
-// each, 57 us whole and 104 in pieces of 128.
+// 238 in 1024; 509 tokens, 12 workgroups a piece: 29 us in 64, 32 in 128, 44 in 256.
+// Where the sequences fill the GPU by themselves, those of up to four pieces are better left whole if they are all like
+// that: the host knows it from the hint and launches the main pass alone (16 sequences of 256 tokens, 32 workgroups
+// each: 54 us whole, 104 in pieces of 128).  Without a hint a mean of two pieces or more says so, but bounds no
+// sequence: the launches for the cut ones are there and the device cuts those over four pieces (the 16 of 256: 72
+// us; 28 sequences with one of 50000 tokens among 60000 805 us, left whole 4445).  With shorter means a sequence of four
+// pieces would outlast all others: every sequence over one piece is cut (32768 tokens of 28 sequences of 120 to 3600: 490 us,
+// with those of up to four pieces whole 571).
 SsdVarlenPlan make_ssd_varlen_plan(int64_t nseq, int64_t total, int64_t nheads, int64_t headdim, int64_t dstate,
                                    int64_t ngroups, int64_t longest) {
   SsdVarlenPlan p{};
   p.quads = quads_of(nheads, headdim, ngroups) * ngroups;
   p.shift = 6;
   while ((int64_t)2 << p.shift <= total / 1024 * p.quads + total % 1024 * p.quads / 1024) ++p.shift;
-  const int64_t piece = (int64_t)1 << p.shift;
   const bool fills = nseq >= (512 + p.quads - 1) / p.quads;
-  if (fills && longest <= 0 && piece <= total / nseq / 2) longest = total / nseq;
   if (longest <= 0 || longest > total) longest = total;
-  p.cut = longest > (fills ? 4 * piece : piece);
-  if (!p.cut) p.shift = 62;   // every sequence is one piece, however long it is
+  p.cut = longest > (int64_t)1 << (fills ? p.shift + 2 : p.shift);
+  p.whole = fills && (int64_t)2 << p.shift <= total / nseq ? p.shift + 2 : p.shift;
+  if (!p.cut) p.shift = p.whole = 62;   // every sequence is one piece, however long it is
   p.pieces = (total >> p.shift) + nseq;   // piece numbers end below that
   if (p.cut) {
     const size_t parts = (size_t)((total >> p.shift) + std::min(nseq, total >> p.shift));
@@ -667,6 +675,7 @@ hipError_t launch_ssd_varlen(const SsdVarlenArgs& p, const SsdVarlenPlan& plan, 
   a.H = (int)p.nheads; a.HP = (int)p.headdim; a.G = (int)p.ngroups; a.softplus = p.softplus; a.euler = p.euler;
   a.nquad = (int)(plan.quads / p.ngroups);
   a.shift = plan.shift;
+  a.whole = plan.whole;
   if (plan.cut) {
     a.ws_state = static_cast<float*>(p.workspace);
     a.ws_decay = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + plan.off_decay);

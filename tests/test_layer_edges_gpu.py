@@ -280,3 +280,41 @@ def test_ssd_pieces_of_several_chunks(case, kind):
         got.append((y, sd))
     check_ssd(lens, *got[0], ref)
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+# ---------------------------------------------------------------- packed SSM: unequal lengths
+
+
+UNEQUAL = {  # 16 sequences, 32 workgroups a piece of 256: the mean is two pieces, those of up to four stay whole
+    "one_long": [1, 700, 7000, 3, 64, 0, 65, 30, 2, 63, 128, 1, 50, 20, 5, 70],
+    "around_four_pieces": [1024, 1025, 1, 0, 1023, 256, 257, 255, 1280, 512, 513, 2, 1026, 3, 64, 959],
+    "equal": [513] * 16,
+}
+
+
+@pytest.mark.parametrize("kind", ["slow", "both", "signed"])
+@pytest.mark.parametrize("name", UNEQUAL)
+def test_ssd_whole_and_cut_sequences_in_one_call(name, kind):
+    lens, H, P, N, G = UNEQUAL[name], 32, 32, 64, 32
+    total, n = sum(lens), len(lens)
+    assert 8192 <= total < 16384 and total // n >= 512
+    hint = max(lens)
+    assert mscan.ssd_fwd_varlen_workspace_size(n, total, H, P, N, G) > 0
+    assert (mscan.ssd_fwd_varlen_workspace_size(n, total, H, P, N, G, hint) > 0) == (hint > 1024)
+    r = Rng(total + len(kind))
+    c = ssd_case(r, lens, H, P, N, G, dt_std=0.3)
+    c["A_log"] = torch.log(r.uniform(8, 16, H))
+    c["dt_bias"] = torch.log(torch.expm1(steps_of(kind if kind != "signed" else "slow", r, H)))
+    if kind == "signed":
+        c["dt"], c["dt_bias"] = (c["dt"].float() * 0.003).bfloat16(), torch.full((H,), 2e-4)
+    state, slots = r(n, H, P, N), r.slots(n, n)
+    pos = i64([[5, 0][i % 2] for i in range(n)])
+    say(f"ssd {name}, {kind}, {lens}")
+    ref = ssd_on_gpu(c, lens, state, slots.tolist(), pos.tolist(), kind != "signed")
+    d = {k: v.to(DEV) for k, v in c.items()}
+    for longest in (0, hint):
+        sd = dev(state.clone())
+        y = mscan.ssd_fwd_varlen(d["x"], d["dt"], d["A_log"], d["B"], d["C"], dev(i64(packed(lens))), D=d["D"], z=d["z"], dt_bias=d["dt_bias"],
+                                 state=sd, slots=dev(slots), positions=dev(pos), dt_softplus=kind != "signed", max_seqlen=longest)
+        torch.cuda.synchronize()
+        check_ssd(lens, y, sd, ref)
