@@ -896,12 +896,13 @@ def rms_norm_bwd_workspace_size(rows: int, dim: int) -> int:
 
 @_entry
 def rms_norm_bwd(dy: torch.Tensor, r: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
-                 d_residual: Optional[torch.Tensor] = None, *, workspace: Optional[torch.Tensor] = None,
-                 stream=None) -> dict:
+                 d_residual: Optional[torch.Tensor] = None, return_dresidual: bool = False, *,
+                 workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
     """Gradient of rms_norm_fwd.  dy (..., dim) in the io dtype; r, what was normed (residual_out, or x where there
     was no residual), in the io dtype or float32; rstd float32 from the forward; d_residual, the gradient that
     reaches r from the residual stream, in r's dtype.  Returns a dict: dx in the io dtype, dweight float32, and
-    with d_residual also dresidual in r's dtype (dx itself where that is the io dtype)."""
+    with d_residual or return_dresidual also dresidual, the gradient of r, in r's dtype (dx itself where that is the io
+    dtype; for a float32 residual of a bfloat16 layer dx alone is the gradient cut to 8 bits)."""
     lib = load_library()
     if dy.dim() < 1 or dy.shape[-1] < 1:
         raise ValueError("dy must be (..., dim)")
@@ -915,8 +916,9 @@ def rms_norm_bwd(dy: torch.Tensor, r: torch.Tensor, weight: torch.Tensor, rstd: 
         raise ValueError("r must have dy's dtype or float32")
     f32, rt = torch.float32, r.dtype
     dx = torch.empty_like(dy)
-    apart = d_residual is not None and rio != io
-    dres = torch.empty_like(d_residual) if apart else None
+    return_dresidual = return_dresidual or d_residual is not None
+    apart = return_dresidual and rio != io
+    dres = torch.empty_like(r) if apart else None
     dw = torch.empty_like(weight)
     ws, ws_ptr, ws_bytes = _scratch(rms_norm_bwd_workspace_size(rows, dim), workspace, dev)
     rc = lib.mamba_rms_norm_bwd(
@@ -925,6 +927,6 @@ def rms_norm_bwd(dy: torch.Tensor, r: torch.Tensor, weight: torch.Tensor, rstd: 
         None if dres is None else dres.data_ptr(), dw.data_ptr(), rows, dim, io, rio, ws_ptr, ws_bytes, _handle(dev, stream))
     _check("mamba_rms_norm_bwd", rc)
     g = {"dx": dx, "dweight": dw}
-    if d_residual is not None:
+    if return_dresidual:
         g["dresidual"] = dres if apart else dx
     return g

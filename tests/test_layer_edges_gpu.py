@@ -318,3 +318,24 @@ def test_ssd_whole_and_cut_sequences_in_one_call(name, kind):
                                  state=sd, slots=dev(slots), positions=dev(pos), dt_softplus=kind != "signed", max_seqlen=longest)
         torch.cuda.synchronize()
         check_ssd(lens, y, sd, ref)
+
+
+# ---------------------------------------------------------------- norm: the gradient of the residual
+
+
+@pytest.mark.parametrize("dim", [96, 100, 2560, 16400])
+def test_norm_gradient_of_a_residual_that_goes_nowhere_else(dim):
+    """The last norm of a bf16 layer with an fp32 residual: the residual's gradient is dr in fp32, not dx."""
+    g = Rng(dim)
+    r, w, dy = g(5, dim, scale=2.0), 1 + g(dim, scale=0.1), g(5, dim, dtype=torch.bfloat16)
+    rstd = (1 / torch.sqrt(r.double().square().mean(1) + 1e-5)).float()
+    dr64, dw64, dra, dwa = layer.rms_norm_bwd(dy, r, w, rstd, None)
+    out = mscan.rms_norm_bwd(*dev(dy, r, w, rstd), return_dresidual=True)
+    assert out["dresidual"].dtype == torch.float32
+    close("dresidual", out["dresidual"], dr64, F32 * dra)
+    close("dx", out["dx"], dr64, 2.0 ** -8 * dr64.abs() + F32 * dra)
+    close("dweight", out["dweight"], dw64, (F32 + 2.0 ** -24 * 21) * dwa)
+    plain = mscan.rms_norm_bwd(*dev(dy, r, w, rstd))
+    assert set(plain) == {"dx", "dweight"} and all(torch.equal(plain[k], out[k]) for k in plain)
+    same = mscan.rms_norm_bwd(*dev(dy, r.bfloat16(), w, rstd), return_dresidual=True)   # one dtype: dx is that gradient
+    assert same["dresidual"] is same["dx"]
