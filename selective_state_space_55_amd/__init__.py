@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import os
 from typing import Optional, Tuple
 
@@ -602,13 +603,14 @@ def ssd_fwd(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, B: torch.Ten
 
 
 def _entry(fn):
-    """Runs fn with the device of its first argument current (the library launches on the current device) and
-    with its `stream` argument, if any, made the current stream, as _on_stream does."""
+    """Runs fn with the device of its first parameter, passed by place or by name, current (the library launches on
+    the current device) and with its `stream` argument, if any, made the current stream, as _on_stream does."""
     on_stream = _on_stream(fn)
+    first = next(iter(inspect.signature(fn).parameters))
 
     @functools.wraps(fn)
     def run(*args, **kwargs):
-        t0 = args[0] if args else next(iter(kwargs.values()), None)
+        t0 = args[0] if args else kwargs.get(first)
         dev = t0.get_device() if isinstance(t0, torch.Tensor) and t0.is_cuda else -1
         if dev < 0 or dev == torch.cuda.current_device():
             return fn(*args, **kwargs) if kwargs.get("stream") is None else on_stream(*args, **kwargs)
