@@ -666,6 +666,10 @@ def _scratch(need: int, workspace: Optional[torch.Tensor], device):
         if need == 0:
             return None, None, 0
         ws = torch.empty(need + 256, dtype=torch.uint8, device=device)
+    elif ws.device != device:
+        raise ValueError(f"workspace is on {ws.device}, expected {device}")
+    elif not ws.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     base = ws.data_ptr()
     off = (-base) % 256
     return ws, base + off, max(0, ws.numel() * ws.element_size() - off)

@@ -51,3 +51,14 @@ def test_entry_points_launch_on_the_device_of_their_first_parameter(monkeypatch)
         assert run() == [1] and entered == [1, -1]
     entered.clear()
     assert call(host, x) == []
+
+
+def test_a_workspace_of_another_device_is_refused():
+    cuda = torch.device("cuda", 0)
+    with pytest.raises(ValueError):
+        mscan._scratch(100, torch.empty(1000, dtype=torch.uint8), cuda)   # host memory
+    with pytest.raises(ValueError):
+        mscan._scratch(100, torch.empty(2000, dtype=torch.uint8)[::2], torch.device("cpu"))
+    ws = torch.empty(1000, dtype=torch.uint8)
+    kept, at, size = mscan._scratch(100, ws, torch.device("cpu"))
+    assert kept is ws and at % 256 == 0 and at + size == ws.data_ptr() + 1000
