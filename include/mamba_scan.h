@@ -384,6 +384,10 @@ int mamba_conv1d_fwd(const void* x, const float* weight, const float* bias, cons
  * The *_stride arguments are the elements between two tokens of an array whose tokens are
  * otherwise contiguous (at least the token's elements), so that the pieces of one projection's
  * output need not be copied apart.
+ *
+ * An output overlaps no other argument of its call, with these exceptions: y of mamba_ssd_fwd_varlen may be x or z
+ * itself (the same address, tokens without gaps), y of mamba_ssd_step may be z itself, y and residual_out of
+ * mamba_rms_norm_fwd may each be x or residual itself where the element type is the same.
  */
 
 /*

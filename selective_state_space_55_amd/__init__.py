@@ -644,6 +644,11 @@ def _token_stride(name: str, t: torch.Tensor, shape, dtype, device) -> int:
     return -(-width // 8) * 8
 
 
+def _overlap(a: int, a_bytes: int, b: int, b_bytes: int) -> bool:
+    """Whether two ranges of memory share a byte."""
+    return a < b + b_bytes and b < a + a_bytes and a_bytes > 0 and b_bytes > 0
+
+
 def _current_handle(index: int) -> int:
     return torch.cuda.current_stream(index).cuda_stream
 
@@ -706,9 +711,13 @@ def ssd_conv_fwd_varlen(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: torch
         nslots = conv_state.shape[0] if conv_state.dim() == 3 else -1
         if slots is None or positions is None:
             raise ValueError("conv_state needs slots and positions")
-    if out is not None and total and out.data_ptr() < x.data_ptr() + ((total - 1) * xs + width) * x.element_size() and \
-            x.data_ptr() < out.data_ptr() + total * width * out.element_size():
-        raise ValueError("out must not overlap x, whose earlier tokens later ones read")
+    if out is not None and total:
+        e = x.element_size()
+        at, end = out.data_ptr(), total * width * e
+        if _overlap(at, end, x.data_ptr(), ((total - 1) * xs + width) * e):
+            raise ValueError("out must not overlap x, whose earlier tokens later ones read")
+        if conv_state is not None and _overlap(at, end, conv_state.data_ptr(), conv_state.numel() * e):
+            raise ValueError("out must not overlap conv_state")
     u = out if out is not None else torch.empty((total, width), dtype=iot, device=dev)
     rc = lib.mamba_ssd_conv_fwd_varlen(
         x.data_ptr(), _need("weight", weight, (width, K), f32, dev), _need("bias", bias, (width,), f32, dev),
@@ -740,7 +749,7 @@ def ssd_fwd_varlen(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, B: to
     z 16-byte aligned.  cu_seqlens (nseq + 1,) int64 on the device.  state (nslots, H, P, N) float32 is
     updated IN PLACE by slot, as conv_state in ssd_conv_fwd_varlen.  max_seqlen, the longest sequence's length where
     the host knows it, only serves the choice of launches.  Returns y (total, H, P); rows outside every
-    sequence are not written."""
+    sequence are not written.  out may be x or z itself (contiguous), and overlap no other argument."""
     lib = load_library()
     if x.dim() != 3:
         raise ValueError("x must be (total, H, P)")
@@ -767,6 +776,16 @@ def ssd_fwd_varlen(x: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, B: to
         nslots = state.shape[0] if state.dim() == 4 else -1
         if slots is None or positions is None:
             raise ValueError("state needs slots and positions")
+    if out is not None and total:
+        at, end = out.data_ptr(), total * H * P * 2
+        px, pz, far = x.data_ptr(), 0 if z is None else z.data_ptr(), total - 1
+        if (at != px or xs != H * P) and _overlap(at, end, px, (far * xs + H * P) * 2) or \
+                z is not None and (at != pz or zs != H * P) and _overlap(at, end, pz, (far * zs + H * P) * 2) or \
+                _overlap(at, end, dt.data_ptr(), (far * ds + H) * 2) or \
+                _overlap(at, end, B.data_ptr(), (far * bs + G * N) * 2) or \
+                _overlap(at, end, C.data_ptr(), (far * cs + G * N) * 2) or \
+                state is not None and _overlap(at, end, state.data_ptr(), state.numel() * 4):
+            raise ValueError("out overlaps an argument that other workgroups read (x or z itself may be out)")
     y = out if out is not None else torch.empty((total, H, P), dtype=iot, device=dev)
     ws, ws_ptr, ws_bytes = _scratch(ssd_fwd_varlen_workspace_size(nseq, total, H, P, N, G, max_seqlen), workspace, dev)
     rc = lib.mamba_ssd_fwd_varlen(
@@ -793,7 +812,8 @@ def ssd_step(xbc: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, conv_weig
     the io dtype (float32 or bfloat16; rows may lie apart).  conv_state (nslots, K, width) in the io dtype and
     state (nslots, H, P, N) float32 are updated IN PLACE at slots[i] (default: i); a row whose slot is
     outside [0, nslots) is padding and its y is not written.  positions (batch,): tokens each request has
-    behind it (0: a new one).  No slot may be named twice.  Returns y (batch, H, P)."""
+    behind it (0: a new one).  No slot may be named twice.  Returns y (batch, H, P); out may be z itself
+    (contiguous), and overlap no other argument."""
     lib = load_library()
     if xbc.dim() != 2 or state.dim() != 4:
         raise ValueError("xbc must be (batch, width) and state (nslots, H, P, N)")
@@ -815,6 +835,14 @@ def ssd_step(xbc: torch.Tensor, dt: torch.Tensor, A_log: torch.Tensor, conv_weig
         raise ValueError(f"{batch} rows without slots, but {nslots} pool entries")
     if positions is None:
         raise ValueError("ssd_step needs positions")
+    if out is not None and batch:
+        e = xbc.element_size()
+        at, end, far, pz = out.data_ptr(), batch * H * P * e, batch - 1, 0 if z is None else z.data_ptr()
+        if _overlap(at, end, xbc.data_ptr(), (far * xs + width) * e) or _overlap(at, end, dt.data_ptr(), (far * ds + H) * e) or \
+                z is not None and (at != pz or far and zs != H * P) and _overlap(at, end, pz, (far * zs + H * P) * e) or \
+                _overlap(at, end, conv_state.data_ptr(), nslots * K * width * e) or \
+                _overlap(at, end, state.data_ptr(), state.numel() * 4):
+            raise ValueError("out overlaps an argument that other workgroups read (z itself may be out)")
     y = out if out is not None else torch.empty((batch, H, P), dtype=iot, device=dev)
     i64 = torch.int64
     rc = lib.mamba_ssd_step(
@@ -840,7 +868,8 @@ def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
     dtype, weight (dim,) float32, residual (..., dim) in the io dtype or float32.  quant None: y in the io
     dtype; "row": y in float8_e4m3fn with one float32 scale per row (shape x.shape[:-1]); "mx": y in
     float8_e4m3fn with one float8_e8m0fnu scale per 32 columns.  Returns y, followed by the scales (quant), r in
-    the residual's dtype (residual given; residual_out may be residual itself) and rstd float32 (return_rstd)."""
+    the residual's dtype (residual given) and rstd float32 (return_rstd).  out and residual_out may each be x or
+    residual itself where the dtype is the same; outputs overlap nothing else."""
     lib = load_library()
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x must be (..., dim)")
@@ -876,6 +905,15 @@ def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
         if scales is None:
             scales = torch.empty(ss, dtype=st, device=dev)
     y = out if out is not None else torch.empty_like(x) if quant is None else torch.empty(shape, dtype=yt, device=dev)
+    if rows and (out is not None or residual_out is not None or scales is not None):
+        ins = [t for t in (x, residual) if t is not None]
+        outs = [t for t in (y, ro, scales) if t is not None]
+        for i, t in enumerate(outs):
+            at, end = t.data_ptr(), t.numel() * t.element_size()
+            if any(_overlap(at, end, o.data_ptr(), o.numel() * o.element_size()) for o in outs[:i] + [weight]) or \
+                    any(_overlap(at, end, o.data_ptr(), o.numel() * o.element_size()) for o in ins
+                        if t is scales or t.dtype != o.dtype or at != o.data_ptr()):
+                raise ValueError("an output overlaps another argument (x or residual itself may be out or residual_out)")
     rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev) if return_rstd else None
     rc = lib.mamba_rms_norm_fwd(
         _need("x", x, shape, iot, dev), _need("residual", residual, shape, rt, dev),

@@ -339,3 +339,84 @@ def test_norm_gradient_of_a_residual_that_goes_nowhere_else(dim):
     assert set(plain) == {"dx", "dweight"} and all(torch.equal(plain[k], out[k]) for k in plain)
     same = mscan.rms_norm_bwd(*dev(dy, r.bfloat16(), w, rstd), return_dresidual=True)   # one dtype: dx is that gradient
     assert same["dresidual"] is same["dx"]
+
+
+# ---------------------------------------------------------------- outputs in place of inputs
+
+
+def test_ssd_out_over_its_inputs():
+    """x or z may be the output; B, C, dt, parts of x and the state, which other workgroups read, may not."""
+    r = Rng(41)
+    lens = [700, 3, 90]   # one sequence is cut
+    c = {k: v.to(DEV) for k, v in ssd_case(r, lens, 4, 64, 64, 2).items()}
+    cu = dev(i64(packed(lens)))
+
+    def call(c, **more):
+        return mscan.ssd_fwd_varlen(c["x"], c["dt"], c["A_log"], c["B"], c["C"], cu, D=c["D"], z=c["z"], dt_bias=c["dt_bias"], **more)
+
+    want = call(c)
+    for k in ("x", "z"):
+        d = dict(c, **{k: c[k].clone()})
+        y = call(d, out=d[k])
+        torch.cuda.synchronize()
+        assert y is d[k] and torch.equal(y, want)
+    total = sum(lens)
+    pool = torch.zeros(3, 4, 64, 64, device=DEV)
+    i = dev(i64([0, 1, 2]))
+    big = torch.zeros(2 * total * 256, dtype=torch.bfloat16, device=DEV)
+    part = lambda at: big[at:at + total * 256].view(total, 4, 64)
+    for d, out in [(dict(c, x=part(0)), part(256)), (dict(c, z=part(256)), part(0)), (dict(c, B=big[:total * 128].view(total, 2, 64)), part(0)),
+                   (dict(c, C=big[:total * 128].view(total, 2, 64)), part(64)), (dict(c, dt=big[8:8 + total * 4].view(total, 4)), part(0)),
+                   (dict(c, x=big.view(total, 512)[:, :256].unflatten(1, (4, 64))), part(0))]:
+        with pytest.raises(ValueError):
+            call(d, out=out)
+    over = torch.zeros(max(pool.numel(), total * 128), device=DEV)
+    with pytest.raises(ValueError):
+        call(c, out=over[:total * 128].view(torch.bfloat16).view(total, 4, 64), state=over[:pool.numel()].view_as(pool), slots=i, positions=i)
+
+
+def test_step_out_over_its_inputs():
+    r = Rng(42)
+    batch, H, P, N = 5, 4, 64, 64
+    c = step_case(r, batch, H, P, N, 1, 4, torch.bfloat16)
+    width = c["xbc"].shape[1]
+    ring, state, pos = r(batch, 4, width, dtype=torch.bfloat16), r(batch, H, P, N), dev(i64([3] * batch))
+
+    def call(out, **other):
+        d = {k: v.to(DEV) for k, v in c.items()} | {"ring": dev(ring.clone()), "state": dev(state.clone())} | other
+        return mscan.ssd_step(d["xbc"], d["dt"], d["A_log"], d["conv_weight"], d["ring"], d["state"], pos, D=d["D"], z=d["z"], out=out)
+
+    want = call(None)
+    z = dev(c["z"].clone())
+    assert torch.equal(call(z, z=z), want)
+    big = torch.zeros(4 * batch * width, dtype=torch.bfloat16, device=DEV)
+    out = big[:batch * H * P].view(batch, H, P)
+    for bad in (dict(xbc=big[:batch * width].view(batch, width)), dict(dt=big[16:16 + batch * H].view(batch, H)),
+                dict(z=big[64:64 + batch * H * P].view(batch, H, P)), dict(ring=big.view(batch, 4, width))):
+        with pytest.raises(ValueError):
+            call(out, **bad)
+    flat = torch.zeros(batch * H * P * N, device=DEV)
+    with pytest.raises(ValueError):
+        call(flat[:batch * H * P // 2].view(torch.bfloat16).view(batch, H, P), state=flat.view(batch, H, P, N))
+
+
+@pytest.mark.parametrize("dim", [256, 255, 16400])
+def test_norm_out_over_its_inputs(dim):
+    g = Rng(dim)
+    x, res, w = dev(g(6, dim), g(6, dim), g(dim))
+    y, r = mscan.rms_norm_fwd(x, w, res)
+    for a, b in (("x", None), ("res", None), (None, "x"), (None, "res"), ("x", "res"), ("res", "x")):
+        t = {"x": x.clone(), "res": res.clone(), None: None}
+        y2, r2 = mscan.rms_norm_fwd(t["x"], w, t["res"], out=t[a], residual_out=t[b])
+        torch.cuda.synchronize()
+        assert torch.equal(y, y2) and torch.equal(r, r2), (a, b)
+    t = x.clone()
+    assert torch.equal(mscan.rms_norm_fwd(t, w, out=t), mscan.rms_norm_fwd(x, w))
+    big = torch.zeros(8, dim, device=DEV)
+    e4 = big.view(-1).view(torch.float8_e4m3fn)[:6 * dim].view(6, dim)
+    for call in (lambda: mscan.rms_norm_fwd(big[:6], w, out=big[1:7]), lambda: mscan.rms_norm_fwd(big[:6], w, res, residual_out=big[2:]),
+                 lambda: mscan.rms_norm_fwd(x, w, big[:6], out=big[1:7]), lambda: mscan.rms_norm_fwd(x, w, res, out=big[:6], residual_out=big[:6]),
+                 lambda: mscan.rms_norm_fwd(big[:6], w, quant="row", out=e4), lambda: mscan.rms_norm_fwd(x, big[7], out=big[2:]),
+                 lambda: mscan.rms_norm_fwd(big[:6], w, quant="row", scales=big.view(-1)[:6])):
+        with pytest.raises(ValueError):
+            call()
