@@ -879,6 +879,7 @@ def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
         raise ValueError("rms_norm_fwd needs device tensors (HIP)")
     if quant not in _NORM_OUT:
         raise ValueError(f"quant must be None, 'row' or 'mx', got {quant!r}")
+    given = out is not None or residual_out is not None or scales is not None
     io, iot = _io_dtype(x), x.dtype
     rio = io
     ro = residual_out
@@ -905,7 +906,7 @@ def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
         if scales is None:
             scales = torch.empty(ss, dtype=st, device=dev)
     y = out if out is not None else torch.empty_like(x) if quant is None else torch.empty(shape, dtype=yt, device=dev)
-    if rows and (out is not None or residual_out is not None or scales is not None):
+    if given and rows:
         ins = [t for t in (x, residual) if t is not None]
         outs = [t for t in (y, ro, scales) if t is not None]
         for i, t in enumerate(outs):
