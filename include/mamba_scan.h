@@ -431,7 +431,8 @@ int mamba_ssd_conv_fwd_varlen(const void* x, const float* weight, const float* b
  * divisor of nheads, strides up to 2^24 (others MAMBA_SCAN_ERR_UNSUPPORTED); x, B, C, z, y and state
  * 16-byte aligned, the strides of x, B, C and z multiples of 8.  Products of bf16 operands with fp32
  * accumulation; the state's own update carries fp32's accuracy (the scaled x in three bf16 parts), and y is
- * rounded once.  The terms x (C.B) w of 64 tokens may add up to 2^95 in magnitude.
+ * rounded once.  The terms x (C.B) w of 64 tokens may add up to 2^95 in magnitude, and negative steps (without
+ * softplus) may grow a state up to 2^127 over 64 tokens.
  * Where long sequences are cut, an input whose weight has decayed below 2^-96 by the end of its piece
  * need not reach the pieces after it.
  */

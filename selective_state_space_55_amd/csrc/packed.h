@@ -90,8 +90,8 @@ __device__ __forceinline__ int64_t seq_position(const Packed& p, int64_t s) {
 }
 
 // A = -exp(A_log) in products with Delta is held at this, where exp(Delta A) is 0 for any Delta that is not: an
-// infinite A would make Delta = 0 a NaN
-constexpr float kFastest = -0x1p126f;
+// infinite A would make Delta = 0 a NaN (a NaN stays one)
+__device__ __forceinline__ float ssd_held(float rate) { return rate < -0x1p126f ? -0x1p126f : rate; }
 
 // (exp(Delta A) - 1) / A is Delta where |Delta A| is below this, to 2^-26 of it; it is not divided
 // there, since A may be too small a number to divide by

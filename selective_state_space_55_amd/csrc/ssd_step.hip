@@ -110,7 +110,7 @@ __global__ __launch_bounds__(256) void ssd_step_kernel(StArgs a) {
     else ux[i - 2 * N] = acc;
     if (i >= 2 * N || hs == g * (a.H / a.G) * a.nslice) ring[now * a.width + c] = raw;
   }
-  const float rate = -expf(a.A_log[h]), A = fmaxf(rate, kFastest);
+  const float rate = -expf(a.A_log[h]), A = ssd_held(rate);
   const float dr = Io<IoT>::load1(static_cast<const IoT*>(a.dt) + row * a.dt_stride + h) + (a.dt_bias ? a.dt_bias[h] : 0.0f);
   const float delta = a.softplus ? softplus_log2e(dr) * 0.6931471805599453f : dr;
   const float m = expm1f(delta * A);

@@ -169,7 +169,7 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
   const bool live = ug < upg;                               // the group's last workgroup may have fewer
   const int u = g * upg + (live ? ug : 0);
   const int h = u / tiles, p0 = (u % tiles) * 32;
-  const float rate = -expf(a.A_log[h]), Ah = fmaxf(rate, kFastest);
+  const float rate = -expf(a.A_log[h]), Ah = ssd_held(rate);
   const float A2 = Ah * 1.4426950408889634f, iA = 1.0f / rate;
   const float Dh = a.D ? a.D[h] : 0.0f;
   const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
@@ -263,7 +263,7 @@ __global__ __launch_bounds__(256, kMode == kAggregate ? 3 : 2) void ssd_varlen_k
     float delta = a.softplus ? softplus_log2e(r) * 0.6931471805599453f : r;
     delta = t0 + lane < t_end ? delta : 0.0f;
     // 2^kLeast takes any fp32 state to nothing; a larger decay would only cost the sums behind it their last bits
-    const float la2 = fmaxf(delta * A2, kLeast);
+    const float la = delta * A2, la2 = la < kLeast ? kLeast : la;   // (a NaN stays one)
     const float wj = a.euler || fabsf(delta * Ah) < kTinyStep ? delta : expm1_small(delta * Ah) * iA;
     const float cum = wave_prefix_sum(la2);
     const float rev = wave_prefix_sum(__shfl(la2, 63 - lane));   // from the chunk's end

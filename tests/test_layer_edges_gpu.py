@@ -420,3 +420,37 @@ def test_norm_out_over_its_inputs(dim):
                  lambda: mscan.rms_norm_fwd(big[:6], w, quant="row", scales=big.view(-1)[:6])):
         with pytest.raises(ValueError):
             call()
+
+
+# ---------------------------------------------------------------- heads without a rate
+
+
+@pytest.mark.parametrize("euler", [False, True])
+def test_a_rate_that_is_no_number_reaches_its_head(euler):
+    """A_log of NaN: all of its head is NaN, in whole and in cut sequences and for single tokens; the other heads are as they were."""
+    r = Rng(51)
+    rule = "euler" if euler else "zoh"
+    for lens in ([100, 5], [700]):
+        c = ssd_case(r, lens, 3, 64, 64, 1)
+        n = len(lens)
+        got = []
+        for bad in (False, True):
+            A = c["A_log"].clone()
+            if bad:
+                A[1] = float("nan")
+            state = torch.ones(n, 3, 64, 64, device=DEV)
+            y = mscan.ssd_fwd_varlen(*dev(c["x"], c["dt"], A, c["B"], c["C"], i64(packed(lens))), state=state, slots=dev(i64(list(range(n)))),
+                                     positions=dev(i64([1] * n)), discretization=rule)
+            got.append((y, state))
+        for a, b in zip(*got):
+            assert torch.isnan(b[:, 1]).all() and torch.equal(a[:, [0, 2]], b[:, [0, 2]])
+    s = step_case(r, 2, 3, 64, 64, 1, 4, torch.bfloat16)
+    got = []
+    for bad in (False, True):
+        A = s["A_log"].clone()
+        if bad:
+            A[1] = float("nan")
+        state, ring = torch.ones(2, 3, 64, 64, device=DEV), torch.zeros(2, 4, s["xbc"].shape[1], dtype=torch.bfloat16, device=DEV)
+        got.append((mscan.ssd_step(*dev(s["xbc"], s["dt"], A, s["conv_weight"]), ring, state, dev(i64([1, 1])), discretization=rule), state))
+    for a, b in zip(*got):
+        assert torch.isnan(b[:, 1]).all() and torch.equal(a[:, [0, 2]], b[:, [0, 2]])
