@@ -454,3 +454,36 @@ def test_a_rate_that_is_no_number_reaches_its_head(euler):
         got.append((mscan.ssd_step(*dev(s["xbc"], s["dt"], A, s["conv_weight"]), ring, state, dev(i64([1, 1])), discretization=rule), state))
     for a, b in zip(*got):
         assert torch.isnan(b[:, 1]).all() and torch.equal(a[:, [0, 2]], b[:, [0, 2]])
+
+
+# ---------------------------------------------------------------- norm in a graph
+
+
+@pytest.mark.parametrize("dim", [768, 2560, 77, 16400])
+def test_norm_graph_replays_equal_eager(dim):
+    """A norm with an 8-bit output and its gradient captured together and replayed on new data, with eager calls in between."""
+    r = Rng(dim)
+    x, res, dy, w = dev(r(40, dim, dtype=torch.bfloat16), r(40, dim), r(40, dim, dtype=torch.bfloat16), r(dim))
+
+    def both():
+        y, scale, rr, rstd = mscan.rms_norm_fwd(x, w, res, quant="mx", return_rstd=True)
+        g = mscan.rms_norm_bwd(dy, rr, w, rstd, return_dresidual=True)
+        return [y.view(torch.uint8), scale.view(torch.uint8), rr, rstd, g["dx"], g["dresidual"], g["dweight"]]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = both()
+    for rep in range(4):
+        for t in (x, res, dy):
+            t.copy_(r(40, dim).to(t.dtype))
+        want = both()
+        graph.replay()
+        torch.cuda.synchronize()
+        say(f"norm of {dim}, replay {rep}")
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
