@@ -17,8 +17,8 @@
 // sum of squares and its use.  W elements per access (8, or 1 for rows that are
 // not 16-byte aligned), T lanes per row (a wave, so that the sum needs no LDS,
 // or a 256-thread workgroup for long rows) and V accesses per lane.  32768 rows of 2560, bf16 to e4m3 with a
-// scale per row: 117 us, 5.0 TB/s; the gradient of 32768 rows of 2048, bf16 with an fp32 residual: 198 us + 5
-// for dweight, 5.3 TB/s (a copy of 1 GiB: 4.8); 16 rows: 5 us.
+// scale per row: 123 us, 4.8 TB/s; the gradient of 32768 rows of 2048, bf16 with an fp32 residual: 198 us + 5
+// for dweight, 5.3 TB/s (a copy of 1 GiB: 4.8 - 5.2); 16 rows: 5 us.
 #include "internal.h"
 #include "io.h"
 #include "mfma.h"
@@ -115,8 +115,9 @@ __device__ __forceinline__ void store_w(void* p, int64_t i, const float (&f)[W])
     Io<T>::store1(q, f[0]);
 }
 
-// load_w for data that the kernel reads once and no one soon after: 32768 rows of 2560 take 117 us with
-// these loads and 127 with plain ones (the gradient, whose stores are larger, 210 against 202)
+// load_w for data that the kernel reads once and no one soon after: 32768 rows of 2560 with e4m3 output take 123 us
+// with these loads and 126 with plain ones, with bf16 output 129 and 135; of 2048 with an fp32 residual 155 and 147 (the
+// gradient, whose stores are larger, 210 against 202)
 template <typename T, int W>
 __device__ __forceinline__ void load_once(const void* p, int64_t i, float (&f)[W]) {
   if constexpr (W == 8) {
@@ -503,9 +504,10 @@ __global__ __launch_bounds__(1024) void dweight_kernel(const float* part, float*
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // The shapes a row is run in.  Aligned rows: a wave per row while it holds the row in a few registers, then a
-// workgroup (forward, 16384 rows of 4096: 159 us against 171 with a wave of 8 accesses; gradient, which holds
-// three rows' worth: 200 against 242, and at 2560 130 against 159 with 5 accesses).  Rows off 16-byte alignment go
-// element by element, at most 8 per lane (8192 rows of 5001, forward: 149 us; with up to 32 per lane 323).
+// workgroup (bf16 with an fp32 residual; forward, 16384 rows of 4096: 155 us against 171 with a wave of 8 accesses;
+// gradient, which holds three rows' worth: 203 against 242, and at 2560 130 against 159 with 5 accesses).  Rows off 16-byte
+// alignment go element by element, at most 8 per lane (8192 rows of 5001, forward: 150 us, with up to 32 per lane 323; of
+// 5000, aligned, 97).
 enum { kLong, kWave1, kWave2, kWave3, kWave4, kWave5, kGroup2, kGroup4, kGroup8, kOddWave, kOddGroup, kOddGroup2, kOddGroup4 };
 
 int row_shape(int64_t dim, bool vec, bool backward) {

@@ -37,16 +37,17 @@
 // into the state that enters each piece (the associative (a, b) operator), and the main pass
 // starts from it.
 //
-// What bounds it: instruction issue.  A chunk of a unit (N = 128, gated) is 1100 vector instructions (a
-// quarter of them the splits of S and of the scaled x, 300 the gate and the epilogue, 64 exponentials and
-// reciprocals at a quarter of the rate), 92 MFMAs of 32 cycles and 126 LDS accesses.  Two waves on a SIMD take
-// 17,000 cycles for a chunk each, of which 10,300 issue vector instructions and 5,900 run MFMAs; the clock
-// falls from 2.3 to 1.8 GHz under it (64 heads, 8 sequences of 1024 tokens, a wave per SIMD: 97 us; 16, two waves
-// per SIMD: 168).  A third wave per SIMD would need 168 registers (S
-// alone is 64) and 53 KB of LDS.  28 sequences, 32768 tokens, 64 heads of 64, N = 128, gated: 435 us, of them
-// the main pass 350 (1.13 GB, 3.2 TB/s; B and C are read again by each XCD), the pieces' own states 70, the
-// fold 22; one prompt of 20000 tokens, 32 heads of 128, N = 64: 225 us; one of 509, 24 heads of 64: 29 us,
-// three short launches.
+// What bounds it: instruction issue, and waiting for it.  A chunk of a unit (N = 128, gated) is 1280 vector
+// instructions (a third of them the splits of S, M and the scaled x; the gate and the epilogue, with 64 exponentials and
+// reciprocals at a quarter of the rate, 300), 98 MFMAs of 32 cycles and 126 LDS accesses.  Two waves on a SIMD take
+// 18,100 cycles for a chunk each, of which 11,800 issue vector instructions and 6,300 run MFMAs.  Those of two waves
+// overlap (two MFMAs beside another wave's 16 multiplies: 91 cycles, apart 64 and 76; 128 for four MFMAs), so neither
+// fills the SIMD: 29% of the waves' cycles are waits (B C^T at its barrier, LDS, the chunk's loads).  64 heads, 8 sequences
+// of 1024 tokens, a wave per SIMD: 113 us; 16, two waves per SIMD: 179.  A third wave per SIMD would need 168 registers
+// (S alone is 64) and 53 KB of LDS.  28 sequences, 32768 tokens, 64 heads of 64, N = 128, gated: 435 - 481 us (boxes
+// differ), of them the main pass 356 (1.13 GB, 3.2 TB/s; B and C are read again by each XCD), the pieces' own states
+// 70, the fold 22; one prompt of 20000 tokens, 32 heads of 128, N = 64: 219 - 241 us; one of 509, 24 heads of 64: 29
+// us, three short launches.
 #include "internal.h"
 #include "io.h"
 #include "mfma.h"
@@ -633,14 +634,14 @@ int64_t quads_of(int64_t nheads, int64_t headdim, int64_t ngroups) { return (nhe
 }  // namespace
 
 // Pieces: as many tokens as share them out over two rounds of two workgroups per CU, a power of two
-// (so that a piece number needs no division).  32768 tokens of 28 sequences, 32 workgroups a piece: 435 us in
-// pieces of 1024, 467 in 512, 508 in 2048; 20000 tokens of one sequence, 32 a piece: 225 us in 512, 251 in 256,
-// 238 in 1024; 509 tokens, 12 workgroups a piece: 29 us in 64, 32 in 128, 44 in 256.
+// (so that a piece number needs no division).  32768 tokens of 28 sequences, 32 workgroups a piece: 479 us in
+// pieces of 1024, 471 in 512, 536 in 2048; 20000 tokens of one sequence, 32 a piece: 240 us in 512, 268 in 256,
+// 255 in 1024; 509 tokens, 12 workgroups a piece: 29 us in 64, 32 in 128, 45 in 256.
 // Where the sequences fill the GPU by themselves, those of up to four pieces are better left whole if they are all like
 // that: the host knows it from the hint and launches the main pass alone (16 sequences of 256 tokens, 32 workgroups
-// each: 54 us whole, 104 in pieces of 128).  Without a hint a mean of two pieces or more says so, but bounds no
-// sequence: the launches for the cut ones are there and the device cuts those over four pieces (the 16 of 256: 72
-// us; 28 sequences with one of 50000 tokens among 60000 805 us, left whole 4445).  With shorter means a sequence of four
+// each: 55 us whole, 105 in pieces of 128).  Without a hint a mean of two pieces or more says so, but bounds no
+// sequence: the launches for the cut ones are there and the device cuts those over four pieces (the 16 of 256: 68
+// us; 28 sequences with one of 50000 tokens among 60000 770 us, left whole 4448).  With shorter means a sequence of four
 // pieces would outlast all others: every sequence over one piece is cut (32768 tokens of 28 sequences of 120 to 3600: 490 us,
 // with those of up to four pieces whole 571).
 SsdVarlenPlan make_ssd_varlen_plan(int64_t nseq, int64_t total, int64_t nheads, int64_t headdim, int64_t dstate,
