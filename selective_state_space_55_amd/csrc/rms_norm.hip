@@ -17,7 +17,7 @@
 // sum of squares and its use.  W elements per access (8, or 1 for rows that are
 // not 16-byte aligned), T lanes per row (a wave, so that the sum needs no LDS,
 // or a 256-thread workgroup for long rows) and V accesses per lane.  32768 rows of 2560, bf16 to e4m3 with a
-// scale per row: 123 us, 4.8 TB/s; the gradient of 32768 rows of 2048, bf16 with an fp32 residual: 198 us + 5
+// scale per row: 119 - 126 us, 4.9 - 4.7 TB/s; the gradient of 32768 rows of 2048, bf16 with an fp32 residual: 198 us + 5
 // for dweight, 5.3 TB/s (a copy of 1 GiB: 4.8 - 5.2); 16 rows: 5 us.
 #include "internal.h"
 #include "io.h"

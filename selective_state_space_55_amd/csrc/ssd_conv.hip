@@ -17,9 +17,9 @@
 // sequence s has number cu[s] / kRun + s + k; see packed.h), so only a
 // sequence's first run looks at the ring: it reads the rows behind it and then
 // writes the new ones, and no other wave has to be waited for.  28 sequences of 32768 tokens, 4352 channels in
-// bf16: 128 us, 4.5 TB/s (a copy of 1 GiB: 4.8 - 5.2); with tokens 4353
-// elements apart, which take 2-byte accesses, 144 against 119 on the same box; in fp32 224 us, 5.1 TB/s; 333 tokens of 5 sequences, 1792 channels: 9.5 us, the latency
-// of its chain (offsets, slot, ring, taps).
+// bf16: 119 - 137 us, 4.8 - 4.2 TB/s (a copy of 1 GiB: 5.2 - 4.8); with tokens 4353 elements apart, which take 2-byte
+// accesses, 144 against 119 on the same card; in fp32 224 us, 5.1 TB/s.  333 tokens of 5 sequences, 1792 channels:
+// 9.5 us, the latency of its chain (offsets, slot, ring, taps).
 #include "internal.h"
 #include "io.h"
 #include "packed.h"

@@ -44,8 +44,8 @@
 // overlap (two MFMAs beside another wave's 16 multiplies: 91 cycles, apart 64 and 76; 128 for four MFMAs), so neither
 // fills the SIMD: 29% of the waves' cycles are waits (B C^T at its barrier, LDS, the chunk's loads).  64 heads, 8 sequences
 // of 1024 tokens, a wave per SIMD: 113 us; 16, two waves per SIMD: 179.  A third wave per SIMD would need 168 registers
-// (S alone is 64) and 53 KB of LDS.  28 sequences, 32768 tokens, 64 heads of 64, N = 128, gated: 435 - 481 us (boxes
-// differ), of them the main pass 356 (1.13 GB, 3.2 TB/s; B and C are read again by each XCD), the pieces' own states
+// (S alone is 64) and 53 KB of LDS.  28 sequences, 32768 tokens, 64 heads of 64, N = 128, gated: 435 - 481 us (cards
+// differ), of them the main pass 356 - 385 (1.13 GB; B and C are read again by each XCD), the pieces' own states
 // 70, the fold 22; one prompt of 20000 tokens, 32 heads of 128, N = 64: 219 - 241 us; one of 509, 24 heads of 64: 29
 // us, three short launches.
 #include "internal.h"
