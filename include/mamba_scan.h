@@ -518,6 +518,123 @@ int mamba_rms_norm_bwd(const void* dy, const void* r, const float* weight, const
 /* Bytes of workspace mamba_rms_norm_bwd needs (0 only for rows == 0); (size_t)-1 for rejected sizes. */
 size_t mamba_rms_norm_bwd_workspace_size(int64_t rows, int64_t dim);
 
+/* ---- Linear attention with a fixed decay per head ----
+ *
+ * The sibling of the state-space-duality layer whose decay is a constant of the head and whose heads have keys and queries of
+ * their own (State space models and Mamba, §5: the semiseparable form with a_t = const).  Per sequence and head, with
+ * lam = exp(log_decay[h]):
+ *
+ *   S_t = lam S_{t-1} + v_t k_t^T,   o_t = scale S_t q_t        (S: V x K, fp32)
+ *
+ * States have the layout of the SSD layer's pools, (entries, nheads, vdim, kdim).  slots, positions and cu_seqlens are as in
+ * the section on serving above.
+ */
+
+/*
+ * Prompts, or a batch in training:
+ *
+ *   q, k         (total_len, nheads, kdim)   bf16   q_stride, k_stride, v_stride elements between tokens
+ *   v            (total_len, nheads, vdim)   bf16
+ *   log_decay    (nheads)                    f32    at most 0 for a decay; -Inf forgets everything, above 0 grows
+ *   cu_seqlens   (nseq + 1) int64, DEVICE, or NULL: nseq sequences of total_len / nseq tokens each
+ *   initial_state, final_state (entries, nheads, vdim, kdim) f32, each NULL allowed: what a sequence starts from (NULL: zeros),
+ *                and OUT: what it ends with.  Both may be the same array (a pool updated in place)
+ *   slots        (nseq) int64, DEVICE, or NULL.  Given: sequence s works on entry slots[s] of nslots, outside of them it
+ *                starts from zeros and keeps nothing, and without tokens it leaves its slot as it is.  NULL: it works on entry
+ *                s of nseq, and without tokens its final state is what it starts from
+ *   positions    (nseq) int64, DEVICE, or NULL: 0 or less starts from zeros; NULL: every sequence starts from initial_state
+ *   o            (total_len, nheads, vdim)   bf16   OUT, without gaps; tokens outside every sequence are not written
+ *   max_len      with cu_seqlens the longest sequence's length where the host knows it, else 0.  Only speed depends on it
+ *   workspace    at least mamba_linear_attention_fwd_workspace_size(...) bytes, 256-byte aligned; contents on entry ignored
+ * Supported: io_dtype MAMBA_SCAN_BF16, kdim and vdim multiples of 8 up to 256, strides multiples of 8 up to 2^24, scale
+ * finite (others MAMBA_SCAN_ERR_UNSUPPORTED); all pointers but log_decay's 16-byte aligned.  Products of bf16 operands with
+ * fp32 accumulation; the fp32 state and the decayed scores are read as bf16 hi + bf16 (rest), v enters the state in
+ * three bf16 parts (exact), and o is rounded once.
+ */
+int mamba_linear_attention_fwd(const void* q, const void* k, const void* v, const float* log_decay,
+                               const int64_t* cu_seqlens, const float* initial_state, float* final_state,
+                               const int64_t* slots, const int64_t* positions, void* o, int64_t nseq, int64_t total_len,
+                               int64_t nheads, int64_t kdim, int64_t vdim, int64_t max_len, int64_t nslots,
+                               int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale, int io_dtype,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace it needs (may be 0); packed: with cu_seqlens.  (size_t)-1 for rejected sizes. */
+size_t mamba_linear_attention_fwd_workspace_size(int64_t nseq, int64_t total_len, int64_t nheads, int64_t kdim,
+                                                 int64_t vdim, int packed, int64_t max_len);
+
+/*
+ * Gradient of mamba_linear_attention_fwd with respect to q, k, v and the initial state; the decay is a constant.  With
+ * R_t the gradient of S_t:
+ *
+ *   R_t = scale do_t q_t^T + (lam R_{t+1}, for the last token d_final_state),   d_initial_state = lam R_0
+ *   dq_t = scale S_t^T do_t,   dk_t = R_t^T v_t,   dv_t = R_t k_t
+ *
+ *   dout          (total_len, nheads, vdim)  bf16   gradient of o, do_stride elements between tokens
+ *   initial_state, d_final_state (nseq, nheads, vdim, kdim) f32   NULL means zeros
+ *   dq, dk, dv    as q, k, v, without gaps   bf16   OUT
+ *   d_initial_state (nseq, nheads, vdim, kdim) f32  OUT, NULL: not written
+ * The rest as above.  Nothing is summed in an order that changes: repeated calls give identical results.
+ */
+int mamba_linear_attention_bwd(const void* dout, const void* q, const void* k, const void* v, const float* log_decay,
+                               const int64_t* cu_seqlens, const float* initial_state, const float* d_final_state,
+                               void* dq, void* dk, void* dv, float* d_initial_state, int64_t nseq, int64_t total_len,
+                               int64_t nheads, int64_t kdim, int64_t vdim, int64_t max_len, int64_t do_stride,
+                               int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale, int io_dtype,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+size_t mamba_linear_attention_bwd_workspace_size(int64_t nseq, int64_t total_len, int64_t nheads, int64_t kdim,
+                                                 int64_t vdim, int packed, int64_t max_len);
+
+/*
+ * One token per request: S <- lam S + v k^T, o = scale S q.
+ *
+ *   q, k         (batch, nheads, kdim)   io
+ *   v, o         (batch, nheads, vdim)   io    o without a stride of its own
+ *   state        (nslots, nheads, vdim, kdim) f32   IN/OUT, 16-byte aligned
+ *   slots        (batch), NULL: row i has slot i.  Outside [0, nslots): padding, nothing read or written
+ *   positions    (batch): 0 or less starts from zeros
+ * Sizes: batch >= 1, kdim a multiple of 8 up to 256, vdim 1 to 256; the launch's work-items below 2^32 (else
+ * MAMBA_SCAN_ERR_UNSUPPORTED).  o overlaps no other argument.
+ */
+int mamba_linear_attention_step(const void* q, const void* k, const void* v, const float* log_decay, float* state,
+                                const int64_t* slots, const int64_t* positions, void* o, int64_t batch, int64_t nheads,
+                                int64_t kdim, int64_t vdim, int64_t nslots, int64_t q_stride, int64_t k_stride,
+                                int64_t v_stride, float scale, int io_dtype, void* stream);
+
+/*
+ * Norm of groups of a row's channels with an activation, behind a layer's heads.  For each row and each of `groups` groups of
+ * `width` consecutive channels (channels last; a row's statistics are its own, so no token sees another):
+ *
+ *   n = (x - mean) / sqrt(var + eps) weight + bias      center zero: mean = 0, var = mean(x^2)
+ *   y = n SiLU(z) with z,  SiLU(n) where silu is set,  else n
+ *
+ *   x, y     (rows, groups * width)  io    y may be x itself, or z itself where z has no gaps
+ *   z        (rows, groups * width)  io    z_stride elements between rows; NULL means no gate
+ *   weight, bias (groups * width)    f32   each NULL allowed
+ * Sizes: rows >= 0, groups >= 1, 1 <= width <= 8192, eps >= 0, not both z and silu (else MAMBA_SCAN_ERR_UNSUPPORTED); the
+ * launch's work-items (at most 1024 a group) below 2^32.  A group with a NaN or an Inf has NaNs in y.  Groups whose squares
+ * leave fp32's range are summed scaled by a power of two.
+ */
+int mamba_group_norm_fwd(const void* x, const float* weight, const float* bias, const void* z, float eps, void* y,
+                         int64_t rows, int64_t groups, int64_t width, int64_t z_stride, int center, int silu, int io_dtype,
+                         void* stream);
+
+/*
+ * Gradient of mamba_group_norm_fwd; the statistics are formed again from x.
+ *
+ *   dy, dx       (rows, groups * width)  io    dx OUT
+ *   dz           (rows, groups * width)  io    OUT, required iff z is given, without gaps
+ *   dweight, dbias (groups * width)      f32   OUT, summed in a fixed order; NULL: not written
+ *   workspace    at least mamba_group_norm_bwd_workspace_size(...) bytes, 256-byte aligned (NULL where neither is wanted)
+ */
+int mamba_group_norm_bwd(const void* dy, const void* x, const float* weight, const float* bias, const void* z, float eps,
+                         void* dx, void* dz, float* dweight, float* dbias, int64_t rows, int64_t groups, int64_t width,
+                         int64_t z_stride, int center, int silu, int io_dtype, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* Bytes of workspace mamba_group_norm_bwd needs for dweight and dbias; (size_t)-1 for rejected sizes. */
+size_t mamba_group_norm_bwd_workspace_size(int64_t rows, int64_t groups, int64_t width);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char* mamba_scan_status_str(int status);
 

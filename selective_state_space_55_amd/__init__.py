@@ -44,6 +44,11 @@ EXPORTED = (
     "mamba_ssd_fwd_varlen_workspace_size", "mamba_ssd_step",
 )
 EXPORTED_NORM = ("mamba_rms_norm_fwd", "mamba_rms_norm_bwd", "mamba_rms_norm_bwd_workspace_size")
+EXPORTED_LINEAR_ATTENTION = (
+    "mamba_linear_attention_fwd", "mamba_linear_attention_fwd_workspace_size", "mamba_linear_attention_bwd",
+    "mamba_linear_attention_bwd_workspace_size", "mamba_linear_attention_step", "mamba_group_norm_fwd",
+    "mamba_group_norm_bwd", "mamba_group_norm_bwd_workspace_size",
+)
 
 _lib = None
 
@@ -103,6 +108,23 @@ def load_library():
     lib.mamba_rms_norm_bwd.argtypes = [P] * 8 + [I64] * 2 + [I, I, P, SZ, P]
     lib.mamba_rms_norm_bwd_workspace_size.restype = SZ
     lib.mamba_rms_norm_bwd_workspace_size.argtypes = [I64] * 2
+    F = ctypes.c_float
+    lib.mamba_linear_attention_fwd.restype = I
+    lib.mamba_linear_attention_fwd.argtypes = [P] * 10 + [I64] * 10 + [F, I, P, SZ, P]
+    lib.mamba_linear_attention_bwd.restype = I
+    lib.mamba_linear_attention_bwd.argtypes = [P] * 12 + [I64] * 10 + [F, I, P, SZ, P]
+    for name in ("fwd", "bwd"):
+        size = getattr(lib, f"mamba_linear_attention_{name}_workspace_size")
+        size.restype = SZ
+        size.argtypes = [I64] * 5 + [I, I64]
+    lib.mamba_linear_attention_step.restype = I
+    lib.mamba_linear_attention_step.argtypes = [P] * 8 + [I64] * 8 + [F, I, P]
+    lib.mamba_group_norm_fwd.restype = I
+    lib.mamba_group_norm_fwd.argtypes = [P] * 4 + [F, P] + [I64] * 4 + [I, I, I, P]
+    lib.mamba_group_norm_bwd.restype = I
+    lib.mamba_group_norm_bwd.argtypes = [P] * 5 + [F] + [P] * 4 + [I64] * 4 + [I, I, I, P, SZ, P]
+    lib.mamba_group_norm_bwd_workspace_size.restype = SZ
+    lib.mamba_group_norm_bwd_workspace_size.argtypes = [I64] * 3
     lib.mamba_scan_status_str.restype = ctypes.c_char_p
     lib.mamba_scan_status_str.argtypes = [I]
     lib.mamba_scan_abi_version.restype = I
@@ -974,4 +996,319 @@ def rms_norm_bwd(dy: torch.Tensor, r: torch.Tensor, weight: torch.Tensor, rstd: 
     g = {"dx": dx, "dweight": dw}
     if return_dresidual:
         g["dresidual"] = dres if apart else dx
+    return g
+
+
+def _sequences(name: str, t: torch.Tensor) -> torch.Tensor:
+    """(batch, L, H, d) as (batch L, H, d), without a copy."""
+    try:
+        return t.view(t.shape[0] * t.shape[1], *t.shape[2:])
+    except RuntimeError:
+        raise ValueError(f"{name}: the sequences of a batch must follow one another") from None
+
+
+def _span(t: torch.Tensor, stride: int) -> int:
+    """Bytes from the first to behind the last element of a tensor of tokens."""
+    return 0 if t.numel() == 0 else ((t.shape[0] - 1) * stride + t[0].numel()) * t.element_size()
+
+
+def _apart(out: Optional[torch.Tensor], others, same=()) -> None:
+    """Refuses an output given by the caller that shares memory with an argument ((tensor, bytes) pairs), but for
+    being one of `same` itself."""
+    if out is None or out.numel() == 0:
+        return
+    at, end = out.data_ptr(), out.numel() * out.element_size()
+    for t, size in others:
+        if t is not None and not any(t is s and at == s.data_ptr() for s in same) and _overlap(at, end, t.data_ptr(), size):
+            raise ValueError("an output overlaps another argument")
+
+
+def _size_of(t: Optional[torch.Tensor]):
+    return t, 0 if t is None else t.numel() * t.element_size()
+
+
+def linear_attention_workspace_size(nseq: int, total_len: int, nheads: int, kdim: int, vdim: int, *, packed: bool = False,
+                                    max_seqlen: int = 0, backward: bool = False) -> int:
+    lib = load_library()
+    fn = lib.mamba_linear_attention_bwd_workspace_size if backward else lib.mamba_linear_attention_fwd_workspace_size
+    n = fn(nseq, total_len, nheads, kdim, vdim, 1 if packed else 0, max_seqlen)
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("mamba_linear_attention_*_workspace_size: sizes rejected")
+    return int(n)
+
+
+def _linear_attention(q, k, v, log_decay, cu_seqlens, nseq, initial_state, final_state, slots, positions, scale, max_seqlen,
+                      out, workspace, stream):
+    """The forward over tokens (total, H, .); returns o."""
+    lib = load_library()
+    total, H, K = q.shape
+    V = v.shape[-1]
+    dev, io, iot = q.device, _io_dtype(q), q.dtype
+    qs = _token_stride("q", q, (total, H, K), iot, dev)
+    ks = _token_stride("k", k, (total, H, K), iot, dev)
+    vs = _token_stride("v", v, (total, H, V), iot, dev)
+    if out is not None:
+        _apart(out, [(q, _span(q, qs)), (k, _span(k, ks)), (v, _span(v, vs)), _size_of(initial_state), _size_of(final_state)])
+    o = out if out is not None else torch.empty((total, H, V), dtype=iot, device=dev)
+    packed = cu_seqlens is not None
+    need = linear_attention_workspace_size(nseq, total, H, K, V, packed=packed, max_seqlen=max_seqlen)
+    ws, ws_ptr, ws_bytes = _scratch(need, workspace, dev)
+    state = initial_state if initial_state is not None else final_state
+    entries = 0 if state is None else state.shape[0] if slots is not None and state.dim() == 4 else nseq
+    f32, i64 = torch.float32, torch.int64
+    rc = lib.mamba_linear_attention_fwd(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _need("log_decay", log_decay, (H,), f32, dev),
+        _need("cu_seqlens", cu_seqlens, (nseq + 1,), i64, dev), _need("initial_state", initial_state, (entries, H, V, K), f32, dev),
+        _need("final_state", final_state, (entries, H, V, K), f32, dev), _need("slots", slots, (nseq,), i64, dev),
+        _need("positions", positions, (nseq,), i64, dev), _need("out", o, (total, H, V), iot, dev), nseq, total, H, K, V,
+        max_seqlen, entries, qs, ks, vs, K ** -0.5 if scale is None else scale, io, ws_ptr, ws_bytes, _handle(dev, stream))
+    _check("mamba_linear_attention_fwd", rc)
+    return o
+
+
+@_entry
+def linear_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                         initial_state: Optional[torch.Tensor] = None, return_final_state: bool = False, *,
+                         scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                         final_state: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Linear attention with a fixed decay per head over a batch of equal sequences: S_t = exp(log_decay) S_{t-1} + v_t k_t^T,
+    o_t = scale S_t q_t.  q, k (batch, L, H, K), v (batch, L, H, V) in bfloat16, K and V multiples of 8 up to 256; tokens may lie
+    apart (slices of a wider row), each contiguous and 16-byte aligned.  log_decay (H,) float32, at most 0 for a decay;
+    initial_state (batch, H, V, K) float32; scale: K ** -0.5 where None.  Returns o (batch, L, H, V), or (o, final_state) if
+    return_final_state.  final_state may be initial_state itself; outputs overlap nothing else."""
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q must be (batch, L, H, K) and v (batch, L, H, V)")
+    if q.device.type != "cuda":
+        raise ValueError("linear_attention_fwd needs device tensors (HIP)")
+    batch, L, H, K = q.shape
+    V = v.shape[-1]
+    _io_dtype(q)
+    if batch < 1:
+        raise ValueError("linear_attention_fwd needs at least one sequence")
+    for name, t, shape in (("k", k, (batch, L, H, K)), ("v", v, (batch, L, H, V)), ("out", out, (batch, L, H, V))):
+        if t is not None and tuple(t.shape) != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    fs = final_state
+    if fs is None and return_final_state:
+        fs = torch.empty((batch, H, V, K), dtype=torch.float32, device=q.device)
+    q, k, v = _sequences("q", q), _sequences("k", k), _sequences("v", v)
+    if final_state is not None:
+        _apart(fs, [(t, _span(t, t.stride(0))) for t in (q, k, v)] + [_size_of(initial_state)], same=(initial_state,))
+    if out is not None:
+        _need("out", out, (batch, L, H, V), q.dtype, q.device)
+    o = _linear_attention(q, k, v, log_decay, None, batch, initial_state, fs, None, None, scale, 0,
+                          None if out is None else out.view(batch * L, H, V), workspace, stream).view(batch, L, H, V)
+    o = o if out is None else out
+    return (o, fs) if return_final_state else o
+
+
+@_entry
+def linear_attention_fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                                cu_seqlens: torch.Tensor, state: Optional[torch.Tensor] = None,
+                                slots: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None, *,
+                                scale: Optional[float] = None, max_seqlen: int = 0, out: Optional[torch.Tensor] = None,
+                                workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """linear_attention_fwd over packed sequences: q, k (total, H, K), v (total, H, V), cu_seqlens (nseq + 1,) int64 on the
+    device.  state (nslots, H, V, K) float32 is updated IN PLACE: sequence s reads and writes entry slots[s] (outside
+    [0, nslots): starts from zeros, keeps nothing), positions[s] tokens (0: a new request) behind it, both (nseq,) int64.  No
+    slot may be named twice.  max_seqlen, the longest sequence's length where the host knows it, only serves the choice of
+    launches.  Returns o (total, H, V); rows outside every sequence are not written."""
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q must be (total, H, K) and v (total, H, V)")
+    if q.device.type != "cuda":
+        raise ValueError("linear_attention_fwd_varlen needs device tensors (HIP)")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be (nseq + 1,)")
+    if state is not None and (slots is None or positions is None):
+        raise ValueError("state needs slots and positions")
+    if state is None and (slots is not None or positions is not None):
+        raise ValueError("slots and positions need state")
+    return _linear_attention(q, k, v, log_decay, cu_seqlens, cu_seqlens.numel() - 1, state, state, slots, positions, scale,
+                             max_seqlen, out, workspace, stream)
+
+
+@_entry
+def linear_attention_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                         initial_state: Optional[torch.Tensor] = None, d_final_state: Optional[torch.Tensor] = None, *,
+                         cu_seqlens: Optional[torch.Tensor] = None, scale: Optional[float] = None, max_seqlen: int = 0,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradient of linear_attention_fwd, or with cu_seqlens (nseq + 1,) of linear_attention_fwd_varlen.  do, the gradient of o,
+    and q, k, v as there, (batch, L, H, .) or packed (total, H, .); initial_state and d_final_state, the gradient of the final
+    state, (batch or nseq, H, V, K) float32, zeros where None.  Returns a dict of dq, dk, dv in bfloat16 and, with
+    initial_state, d_initial_state float32; rows outside every sequence are not written.  The decay is a constant: it has
+    no gradient."""
+    lib = load_library()
+    if do.device.type != "cuda":
+        raise ValueError("linear_attention_bwd needs device tensors (HIP)")
+    packed = cu_seqlens is not None
+    dims = 3 if packed else 4
+    if q.dim() != dims or v.dim() != dims:
+        raise ValueError("q must be (batch, L, H, K), or (total, H, K) with cu_seqlens")
+    qshape, vshape = tuple(q.shape), tuple(v.shape)
+    if packed:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be (nseq + 1,)")
+        nseq = cu_seqlens.numel() - 1
+    else:
+        nseq = qshape[0]
+        if nseq < 1:
+            raise ValueError("linear_attention_bwd needs at least one sequence")
+        for name, t, shape in (("k", k, qshape), ("v", v, qshape[:3] + vshape[3:]), ("do", do, vshape)):
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+        do, q, k, v = _sequences("do", do), _sequences("q", q), _sequences("k", k), _sequences("v", v)
+    total, H, K = q.shape
+    V = v.shape[-1]
+    dev, io, iot = do.device, _io_dtype(do), do.dtype
+    gs = _token_stride("do", do, (total, H, V), iot, dev)
+    qs = _token_stride("q", q, (total, H, K), iot, dev)
+    ks = _token_stride("k", k, (total, H, K), iot, dev)
+    vs = _token_stride("v", v, (total, H, V), iot, dev)
+    dq, dk = (torch.empty(qshape, dtype=iot, device=dev) for _ in range(2))
+    dv = torch.empty(vshape, dtype=iot, device=dev)
+    dh = None if initial_state is None else torch.empty((nseq, H, V, K), dtype=torch.float32, device=dev)
+    need = linear_attention_workspace_size(nseq, total, H, K, V, packed=packed, max_seqlen=max_seqlen, backward=True)
+    ws, ws_ptr, ws_bytes = _scratch(need, workspace, dev)
+    f32 = torch.float32
+    rc = lib.mamba_linear_attention_bwd(
+        do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), _need("log_decay", log_decay, (H,), f32, dev),
+        _need("cu_seqlens", cu_seqlens, (nseq + 1,), torch.int64, dev),
+        _need("initial_state", initial_state, (nseq, H, V, K), f32, dev),
+        _need("d_final_state", d_final_state, (nseq, H, V, K), f32, dev), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+        None if dh is None else dh.data_ptr(), nseq, total, H, K, V, max_seqlen, gs, qs, ks, vs,
+        K ** -0.5 if scale is None else scale, io, ws_ptr, ws_bytes, _handle(dev, stream))
+    _check("mamba_linear_attention_bwd", rc)
+    g = {"dq": dq, "dk": dk, "dv": dv}
+    if dh is not None:
+        g["d_initial_state"] = dh
+    return g
+
+
+@_entry
+def linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, state: torch.Tensor,
+                          positions: torch.Tensor, slots: Optional[torch.Tensor] = None, *, scale: Optional[float] = None,
+                          out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """One token per request: S = exp(log_decay) S + v k^T, o = scale S q.  q, k (batch, H, K), v (batch, H, V) in the io dtype
+    (float32 or bfloat16; rows may lie apart), K a multiple of 8 up to 256, V up to 256.  state (nslots, H, V, K) float32 is
+    updated IN PLACE at slots[i] (default: i); a row whose slot is outside [0, nslots) is padding and its o is not written.
+    positions (batch,): tokens each request has behind it (0: a new one).  No slot may be named twice.  scale: K ** -0.5
+    where None.  Returns o (batch, H, V); out overlaps no other argument."""
+    lib = load_library()
+    if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
+        raise ValueError("q must be (batch, H, K), v (batch, H, V) and state (nslots, H, V, K)")
+    batch, H, K = q.shape
+    V, nslots = v.shape[-1], state.shape[0]
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("linear_attention_step needs device tensors (HIP)")
+    io, iot = _io_dtype(q), q.dtype
+    qs = _token_stride("q", q, (batch, H, K), iot, dev)
+    ks = _token_stride("k", k, (batch, H, K), iot, dev)
+    vs = _token_stride("v", v, (batch, H, V), iot, dev)
+    if slots is None and batch > nslots:
+        raise ValueError(f"{batch} rows without slots, but {nslots} pool entries")
+    if positions is None:
+        raise ValueError("linear_attention_step needs positions")
+    if out is not None:
+        _apart(out, [(q, _span(q, qs)), (k, _span(k, ks)), (v, _span(v, vs)), _size_of(state)])
+    o = out if out is not None else torch.empty((batch, H, V), dtype=iot, device=dev)
+    f32, i64 = torch.float32, torch.int64
+    rc = lib.mamba_linear_attention_step(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _need("log_decay", log_decay, (H,), f32, dev),
+        _need("state", state, (nslots, H, V, K), f32, dev), _need("slots", slots, (batch,), i64, dev),
+        _need("positions", positions, (batch,), i64, dev), _need("out", o, (batch, H, V), iot, dev), batch, H, K, V, nslots,
+        qs, ks, vs, K ** -0.5 if scale is None else scale, io, _handle(dev, stream))
+    _check("mamba_linear_attention_step", rc)
+    return o
+
+
+def _rows_of(name: str, t: torch.Tensor, shape, dtype, device) -> int:
+    """Checks a tensor (..., dim) whose rows are contiguous but may lie apart; returns the elements between them."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        _req(name, t, shape, dtype, device)
+    if t.is_contiguous():
+        return shape[-1]
+    try:
+        t = t.view(-1, shape[-1])
+    except RuntimeError:
+        raise ValueError(f"{name}: rows must follow one another") from None
+    if t.stride(1) != 1 and shape[-1] > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else shape[-1]
+
+
+def _group_shape(x: torch.Tensor, groups: int):
+    if x.dim() < 1 or groups < 1 or x.shape[-1] < 1 or x.shape[-1] % groups:
+        raise ValueError("x must be (..., dim) with groups a divisor of dim")
+    return x.numel() // x.shape[-1], x.shape[-1], x.shape[-1] // groups
+
+
+@_entry
+def group_norm_fwd(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                   z: Optional[torch.Tensor] = None, *, eps: float = 1e-5, center: bool = True, silu: bool = False,
+                   out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Norm of each of `groups` groups of a row's channels (channels last, statistics of each row alone): n = (x - mean) /
+    sqrt(var + eps) weight + bias, without the mean where center is False; returns n SiLU(z) where z is given, SiLU(n) where
+    silu is set (not both), else n.  x (..., dim) in the io dtype (float32 or bfloat16), z as x (its rows may lie apart, as a
+    slice of a projection's output), weight, bias (dim,) float32.  dim / groups at most 8192.  out may be x, or z itself
+    (contiguous), and overlap nothing else."""
+    lib = load_library()
+    rows, dim, width = _group_shape(x, groups)
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("group_norm_fwd needs device tensors (HIP)")
+    io, iot, shape = _io_dtype(x), x.dtype, x.shape
+    zs = dim if z is None else _rows_of("z", z, shape, iot, dev)
+    if out is not None:
+        _apart(out, [_size_of(x), (z, 0 if z is None or not rows else ((rows - 1) * zs + dim) * z.element_size()), _size_of(weight),
+                     _size_of(bias)], same=(x, z) if zs == dim else (x,))
+    y = out if out is not None else torch.empty(shape, dtype=iot, device=dev)
+    f32 = torch.float32
+    rc = lib.mamba_group_norm_fwd(
+        _need("x", x, shape, iot, dev), _need("weight", weight, (dim,), f32, dev), _need("bias", bias, (dim,), f32, dev),
+        None if z is None else z.data_ptr(), eps, _need("out", y, shape, iot, dev), rows, groups, width, zs,
+        1 if center else 0, 1 if silu else 0, io, _handle(dev, stream))
+    _check("mamba_group_norm_fwd", rc)
+    return y
+
+
+def group_norm_bwd_workspace_size(rows: int, groups: int, width: int) -> int:
+    n = load_library().mamba_group_norm_bwd_workspace_size(rows, groups, width)
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("mamba_group_norm_bwd_workspace_size: sizes rejected")
+    return int(n)
+
+
+@_entry
+def group_norm_bwd(dy: torch.Tensor, x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = None,
+                   bias: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None, *, eps: float = 1e-5,
+                   center: bool = True, silu: bool = False, workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradient of group_norm_fwd, given what it was given and dy (..., dim) in the io dtype.  Returns a dict: dx, with z also
+    dz, both in the io dtype, and with weight and bias dweight and dbias float32, summed in a fixed order."""
+    lib = load_library()
+    rows, dim, width = _group_shape(x, groups)
+    dev = dy.device
+    if dev.type != "cuda":
+        raise ValueError("group_norm_bwd needs device tensors (HIP)")
+    io, iot, shape = _io_dtype(dy), dy.dtype, x.shape
+    zs = dim if z is None else _rows_of("z", z, shape, iot, dev)
+    f32 = torch.float32
+    g = {"dx": torch.empty(shape, dtype=iot, device=dev)}
+    if z is not None:
+        g["dz"] = torch.empty(shape, dtype=iot, device=dev)
+    if weight is not None:
+        g["dweight"] = torch.empty((dim,), dtype=f32, device=dev)
+    if bias is not None:
+        g["dbias"] = torch.empty((dim,), dtype=f32, device=dev)
+    need = 0 if weight is None and bias is None else group_norm_bwd_workspace_size(rows, groups, width)
+    ws, ws_ptr, ws_bytes = _scratch(need, workspace, dev)
+    p = {name: None if t is None else t.data_ptr() for name, t in g.items()}
+    rc = lib.mamba_group_norm_bwd(
+        _need("dy", dy, shape, iot, dev), _need("x", x, shape, iot, dev), _need("weight", weight, (dim,), f32, dev),
+        _need("bias", bias, (dim,), f32, dev), None if z is None else z.data_ptr(), eps, p["dx"], p.get("dz"),
+        p.get("dweight"), p.get("dbias"), rows, groups, width, zs, 1 if center else 0, 1 if silu else 0, io, ws_ptr, ws_bytes,
+        _handle(dev, stream))
+    _check("mamba_group_norm_bwd", rc)
     return g

@@ -14,7 +14,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libmamba_scan.so")
 SOURCES = ["api.hip", "scan_fwd.hip", "scan_fwd_varlen.hip", "scan_step.hip", "scan_bwd.hip", "conv1d.hip", "ssd_fwd.hip",
-           "ssd_conv.hip", "ssd_varlen.hip", "ssd_step.hip", "rms_norm.hip"]
+           "ssd_conv.hip", "ssd_varlen.hip", "ssd_step.hip", "rms_norm.hip", "linear_attention.hip", "linear_attention_step.hip",
+           "group_norm.hip"]
 ARCH = "gfx950"
 
 

@@ -3,6 +3,7 @@
 // Every entry point validates its arguments on the host before touching the
 // HIP runtime; a rejected call launches nothing and returns a status code.
 #include <limits.h>
+#include <math.h>
 
 #include <algorithm>
 #include <atomic>
@@ -676,6 +677,213 @@ int mamba_rms_norm_bwd(const void* dy, const void* r, const float* weight, const
   a.residual_out = dresidual; a.dweight = dweight; a.rows = rows; a.dim = dim;
   a.io_bf16 = io_dtype == MAMBA_SCAN_BF16; a.res_f32 = residual_dtype == MAMBA_SCAN_F32; a.workspace = workspace;
   hipError_t e = mscan::launch_norm_bwd(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MAMBA_SCAN_OK : MAMBA_SCAN_ERR_HIP;
+}
+
+// ---- linear attention with a fixed decay per head ----
+
+static int check_linear_attention(int64_t nseq, int64_t total_len, int64_t nheads, int64_t kdim, int64_t vdim, bool packed,
+                                  int64_t max_len, bool backward, mscan::LinearAttentionPlan* plan) {
+  if (nseq < 1 || total_len < 0 || max_len < 0 || nheads < 1 || kdim < 1 || vdim < 1) return MAMBA_SCAN_ERR_SHAPE;
+  if (!packed && total_len % nseq != 0) return MAMBA_SCAN_ERR_SHAPE;
+  if (kdim % 8 != 0 || vdim % 8 != 0 || kdim > 256 || vdim > 256) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  if (nheads > (1 << 24) / std::max(kdim, vdim)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  int64_t t;
+  if (nseq > INT32_MAX || !mul_ok(total_len, nheads * std::max(kdim, vdim), &t) || !mul_ok(t, 4, &t) ||
+      t > ((int64_t)1 << 61) || !mul_ok(nseq, nheads * kdim, &t) || !mul_ok(t, vdim * 4, &t))
+    return MAMBA_SCAN_ERR_SHAPE;
+  *plan = mscan::make_linear_attention_plan(nseq, total_len, nheads, kdim, vdim, packed, max_len, backward);
+  // grid: a piece's workgroups, heads rounded up to eight at a time, 256 work-items each
+  if (!mul_ok(plan->pieces + 8, plan->wgs, &t) || !launch_ok(t, 256)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  return MAMBA_SCAN_OK;
+}
+
+// tokens of an array whose rows take 32-bit offsets and 16-byte accesses
+static int check_tokens(const void* p, int64_t total_len, int64_t width, int64_t stride) {
+  int st = check_rows(total_len, width, stride);
+  if (st != MAMBA_SCAN_OK) return st;
+  if (stride > (1 << 24)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  if (stride % 8 != 0 || !aligned(p, 16)) return MAMBA_SCAN_ERR_ALIGN;
+  return total_len > 0 && !p ? MAMBA_SCAN_ERR_NULL : MAMBA_SCAN_OK;
+}
+
+static size_t linear_attention_workspace(int64_t nseq, int64_t total_len, int64_t nheads, int64_t kdim, int64_t vdim,
+                                         int packed, int64_t max_len, bool backward) {
+  mscan::LinearAttentionPlan plan;
+  if (check_linear_attention(nseq, total_len, nheads, kdim, vdim, packed != 0, max_len, backward, &plan) != MAMBA_SCAN_OK)
+    return (size_t)-1;
+  return plan.ws_total;
+}
+
+size_t mamba_linear_attention_fwd_workspace_size(int64_t nseq, int64_t total_len, int64_t nheads, int64_t kdim,
+                                                 int64_t vdim, int packed, int64_t max_len) {
+  return linear_attention_workspace(nseq, total_len, nheads, kdim, vdim, packed, max_len, false);
+}
+
+size_t mamba_linear_attention_bwd_workspace_size(int64_t nseq, int64_t total_len, int64_t nheads, int64_t kdim,
+                                                 int64_t vdim, int packed, int64_t max_len) {
+  return linear_attention_workspace(nseq, total_len, nheads, kdim, vdim, packed, max_len, true);
+}
+
+int mamba_linear_attention_fwd(const void* q, const void* k, const void* v, const float* log_decay,
+                               const int64_t* cu_seqlens, const float* initial_state, float* final_state,
+                               const int64_t* slots, const int64_t* positions, void* o, int64_t nseq, int64_t total_len,
+                               int64_t nheads, int64_t kdim, int64_t vdim, int64_t max_len, int64_t nslots,
+                               int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale, int io_dtype,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  if (io_dtype != MAMBA_SCAN_F32 && io_dtype != MAMBA_SCAN_BF16) return MAMBA_SCAN_ERR_DTYPE;
+  if (io_dtype != MAMBA_SCAN_BF16) return MAMBA_SCAN_ERR_UNSUPPORTED;   // bf16 operands only
+  mscan::LinearAttentionPlan plan;
+  int st = check_linear_attention(nseq, total_len, nheads, kdim, vdim, cu_seqlens != nullptr, max_len, false, &plan);
+  if (st != MAMBA_SCAN_OK) return st;
+  if (!(fabsf(scale) < INFINITY)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  int64_t t;
+  if (nslots < 0 || !mul_ok(nslots, nheads * kdim, &t) || !mul_ok(t, vdim * 4, &t)) return MAMBA_SCAN_ERR_SHAPE;
+  if (!log_decay || (slots && !initial_state && !final_state)) return MAMBA_SCAN_ERR_NULL;
+  if (st = check_tokens(q, total_len, nheads * kdim, q_stride); st != MAMBA_SCAN_OK) return st;
+  if (st = check_tokens(k, total_len, nheads * kdim, k_stride); st != MAMBA_SCAN_OK) return st;
+  if (st = check_tokens(v, total_len, nheads * vdim, v_stride); st != MAMBA_SCAN_OK) return st;
+  if (st = check_tokens(o, total_len, nheads * vdim, nheads * vdim); st != MAMBA_SCAN_OK) return st;
+  if (!aligned(log_decay, 4) || !aligned(initial_state, 16) || !aligned(final_state, 16) || !aligned(cu_seqlens, 8) ||
+      !aligned(slots, 8) || !aligned(positions, 8))
+    return MAMBA_SCAN_ERR_ALIGN;
+  if (plan.ws_total > 0 && (!workspace || workspace_bytes < plan.ws_total || !aligned(workspace, 256)))
+    return MAMBA_SCAN_ERR_WORKSPACE;
+  if (total_len == 0 && (slots || !final_state)) return MAMBA_SCAN_OK;
+  mscan::LinearAttentionArgs a{};
+  a.q = q; a.k = k; a.v = v; a.log_decay = log_decay; a.cu = cu_seqlens; a.initial_state = initial_state;
+  a.final_state = final_state; a.slots = slots; a.positions = positions; a.o = o; a.nseq = nseq; a.total = total_len;
+  a.nslots = nslots; a.nheads = nheads; a.kdim = kdim; a.vdim = vdim; a.q_stride = q_stride; a.k_stride = k_stride;
+  a.v_stride = v_stride; a.scale = scale; a.workspace = workspace;
+  hipError_t e = mscan::launch_linear_attention(a, plan, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MAMBA_SCAN_OK : MAMBA_SCAN_ERR_HIP;
+}
+
+int mamba_linear_attention_bwd(const void* dout, const void* q, const void* k, const void* v, const float* log_decay,
+                               const int64_t* cu_seqlens, const float* initial_state, const float* d_final_state,
+                               void* dq, void* dk, void* dv, float* d_initial_state, int64_t nseq, int64_t total_len,
+                               int64_t nheads, int64_t kdim, int64_t vdim, int64_t max_len, int64_t do_stride,
+                               int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale, int io_dtype,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  if (io_dtype != MAMBA_SCAN_F32 && io_dtype != MAMBA_SCAN_BF16) return MAMBA_SCAN_ERR_DTYPE;
+  if (io_dtype != MAMBA_SCAN_BF16) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  mscan::LinearAttentionPlan plan;
+  int st = check_linear_attention(nseq, total_len, nheads, kdim, vdim, cu_seqlens != nullptr, max_len, true, &plan);
+  if (st != MAMBA_SCAN_OK) return st;
+  if (!(fabsf(scale) < INFINITY)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  if (!log_decay) return MAMBA_SCAN_ERR_NULL;
+  const int64_t inner_k = nheads * kdim, inner_v = nheads * vdim;
+  if (st = check_tokens(dout, total_len, inner_v, do_stride); st != MAMBA_SCAN_OK) return st;
+  if (st = check_tokens(q, total_len, inner_k, q_stride); st != MAMBA_SCAN_OK) return st;
+  if (st = check_tokens(k, total_len, inner_k, k_stride); st != MAMBA_SCAN_OK) return st;
+  if (st = check_tokens(v, total_len, inner_v, v_stride); st != MAMBA_SCAN_OK) return st;
+  if (st = check_tokens(dq, total_len, inner_k, inner_k); st != MAMBA_SCAN_OK) return st;
+  if (st = check_tokens(dk, total_len, inner_k, inner_k); st != MAMBA_SCAN_OK) return st;
+  if (st = check_tokens(dv, total_len, inner_v, inner_v); st != MAMBA_SCAN_OK) return st;
+  if (!aligned(log_decay, 4) || !aligned(initial_state, 16) || !aligned(d_final_state, 16) ||
+      !aligned(d_initial_state, 16) || !aligned(cu_seqlens, 8))
+    return MAMBA_SCAN_ERR_ALIGN;
+  if (plan.ws_total > 0 && (!workspace || workspace_bytes < plan.ws_total || !aligned(workspace, 256)))
+    return MAMBA_SCAN_ERR_WORKSPACE;
+  if (total_len == 0 && !d_initial_state) return MAMBA_SCAN_OK;
+  mscan::LinearAttentionArgs a{};
+  a.dout = dout; a.q = q; a.k = k; a.v = v; a.log_decay = log_decay; a.cu = cu_seqlens; a.initial_state = initial_state;
+  a.d_final_state = d_final_state; a.dq = dq; a.dk = dk; a.dv = dv; a.d_initial_state = d_initial_state; a.nseq = nseq;
+  a.total = total_len; a.nheads = nheads; a.kdim = kdim; a.vdim = vdim; a.dout_stride = do_stride; a.q_stride = q_stride;
+  a.k_stride = k_stride; a.v_stride = v_stride; a.scale = scale; a.workspace = workspace; a.backward = true;
+  hipError_t e = mscan::launch_linear_attention(a, plan, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MAMBA_SCAN_OK : MAMBA_SCAN_ERR_HIP;
+}
+
+int mamba_linear_attention_step(const void* q, const void* k, const void* v, const float* log_decay, float* state,
+                                const int64_t* slots, const int64_t* positions, void* o, int64_t batch, int64_t nheads,
+                                int64_t kdim, int64_t vdim, int64_t nslots, int64_t q_stride, int64_t k_stride,
+                                int64_t v_stride, float scale, int io_dtype, void* stream) {
+  if (io_dtype != MAMBA_SCAN_F32 && io_dtype != MAMBA_SCAN_BF16) return MAMBA_SCAN_ERR_DTYPE;
+  if (batch < 1 || nslots < 0 || nheads < 1 || kdim < 1 || vdim < 1) return MAMBA_SCAN_ERR_SHAPE;
+  if (kdim % 8 != 0 || kdim > 256 || vdim > 256 || nheads > (1 << 24) / std::max(kdim, vdim)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  if (!(fabsf(scale) < INFINITY)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  int64_t t;
+  const int64_t slice = mscan::linear_attention_step_slice(batch, nheads, kdim, vdim);
+  if (!mul_ok(batch, nheads * ((vdim + slice - 1) / slice), &t) || !launch_ok(t, 256)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  if (!mul_ok(nslots, nheads * kdim, &t) || !mul_ok(t, vdim * 4, &t)) return MAMBA_SCAN_ERR_SHAPE;
+  int st = check_rows(batch, nheads * kdim, q_stride);
+  if (st == MAMBA_SCAN_OK) st = check_rows(batch, nheads * kdim, k_stride);
+  if (st == MAMBA_SCAN_OK) st = check_rows(batch, nheads * vdim, v_stride);
+  if (st != MAMBA_SCAN_OK) return st;
+  if (!q || !k || !v || !log_decay || !state || !positions || !o) return MAMBA_SCAN_ERR_NULL;
+  const size_t esz = io_dtype == MAMBA_SCAN_BF16 ? 2 : 4;
+  if (!aligned(q, esz) || !aligned(k, esz) || !aligned(v, esz) || !aligned(o, esz) || !aligned(log_decay, 4) ||
+      !aligned(state, 16) || !aligned(slots, 8) || !aligned(positions, 8))
+    return MAMBA_SCAN_ERR_ALIGN;
+  mscan::LinearAttentionStepArgs a{};
+  a.q = q; a.k = k; a.v = v; a.log_decay = log_decay; a.state = state; a.slots = slots; a.positions = positions; a.o = o;
+  a.batch = batch; a.nslots = nslots; a.nheads = nheads; a.kdim = kdim; a.vdim = vdim; a.q_stride = q_stride;
+  a.k_stride = k_stride; a.v_stride = v_stride; a.scale = scale; a.io_bf16 = io_dtype == MAMBA_SCAN_BF16;
+  hipError_t e = mscan::launch_linear_attention_step(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MAMBA_SCAN_OK : MAMBA_SCAN_ERR_HIP;
+}
+
+// ---- norm of groups with an activation ----
+
+static int check_group_norm(int64_t rows, int64_t groups, int64_t width, int io_dtype) {
+  if (io_dtype != MAMBA_SCAN_F32 && io_dtype != MAMBA_SCAN_BF16) return MAMBA_SCAN_ERR_DTYPE;
+  if (rows < 0 || groups < 1 || width < 1) return MAMBA_SCAN_ERR_SHAPE;
+  if (width > 8192 || groups > (1 << 24) / width) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  int64_t t;
+  // at most a workgroup of 1024 per group, 64 work-items a column
+  if (!mul_ok(rows + 2048, groups, &t) || !launch_ok(t, width > 2048 ? 1024 : 256)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  return MAMBA_SCAN_OK;
+}
+
+static int check_group_norm_args(int64_t rows, int64_t groups, int64_t width, int64_t z_stride, const void* x, const void* z,
+                                 const void* y, const float* weight, const float* bias, float eps, int silu, int io_dtype) {
+  int st = check_group_norm(rows, groups, width, io_dtype);
+  if (st != MAMBA_SCAN_OK) return st;
+  if (!(eps >= 0.0f) || (z && silu)) return MAMBA_SCAN_ERR_UNSUPPORTED;
+  st = check_rows(rows, groups * width, z ? z_stride : groups * width);
+  if (st != MAMBA_SCAN_OK) return st;
+  if (rows > 0 && (!x || !y)) return MAMBA_SCAN_ERR_NULL;
+  const size_t esz = io_dtype == MAMBA_SCAN_BF16 ? 2 : 4;
+  if (!aligned(x, esz) || !aligned(z, esz) || !aligned(y, esz) || !aligned(weight, 4) || !aligned(bias, 4))
+    return MAMBA_SCAN_ERR_ALIGN;
+  return MAMBA_SCAN_OK;
+}
+
+int mamba_group_norm_fwd(const void* x, const float* weight, const float* bias, const void* z, float eps, void* y,
+                         int64_t rows, int64_t groups, int64_t width, int64_t z_stride, int center, int silu, int io_dtype,
+                         void* stream) {
+  int st = check_group_norm_args(rows, groups, width, z_stride, x, z, y, weight, bias, eps, silu, io_dtype);
+  if (st != MAMBA_SCAN_OK) return st;
+  if (rows == 0) return MAMBA_SCAN_OK;
+  mscan::GroupNormArgs a{};
+  a.x = x; a.z = z; a.weight = weight; a.bias = bias; a.y = y; a.rows = rows; a.groups = groups; a.width = width;
+  a.z_stride = z_stride; a.eps = eps; a.center = center != 0; a.silu = silu != 0; a.io_bf16 = io_dtype == MAMBA_SCAN_BF16;
+  hipError_t e = mscan::launch_group_norm_fwd(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MAMBA_SCAN_OK : MAMBA_SCAN_ERR_HIP;
+}
+
+size_t mamba_group_norm_bwd_workspace_size(int64_t rows, int64_t groups, int64_t width) {
+  if (check_group_norm(rows, groups, width, MAMBA_SCAN_F32) != MAMBA_SCAN_OK) return (size_t)-1;
+  return rows == 0 ? 0 : (size_t)(mscan::group_norm_bwd_parts(rows, groups, width) * groups * width) * 8;
+}
+
+int mamba_group_norm_bwd(const void* dy, const void* x, const float* weight, const float* bias, const void* z, float eps,
+                         void* dx, void* dz, float* dweight, float* dbias, int64_t rows, int64_t groups, int64_t width,
+                         int64_t z_stride, int center, int silu, int io_dtype, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  int st = check_group_norm_args(rows, groups, width, z_stride, x, z, dx, weight, bias, eps, silu, io_dtype);
+  if (st != MAMBA_SCAN_OK) return st;
+  if (rows > 0 && (!dy || (z == nullptr) != (dz == nullptr))) return MAMBA_SCAN_ERR_NULL;
+  const size_t esz = io_dtype == MAMBA_SCAN_BF16 ? 2 : 4;
+  if (!aligned(dy, esz) || !aligned(dz, esz) || !aligned(dweight, 4) || !aligned(dbias, 4)) return MAMBA_SCAN_ERR_ALIGN;
+  const size_t need = dweight || dbias ? mamba_group_norm_bwd_workspace_size(rows, groups, width) : 0;
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return MAMBA_SCAN_ERR_WORKSPACE;
+  mscan::GroupNormArgs a{};
+  a.dy = dy; a.x = x; a.z = z; a.weight = weight; a.bias = bias; a.y = dx; a.dz = dz; a.dweight = dweight; a.dbias = dbias;
+  a.rows = rows; a.groups = groups; a.width = width; a.z_stride = z_stride; a.eps = eps; a.center = center != 0;
+  a.silu = silu != 0; a.io_bf16 = io_dtype == MAMBA_SCAN_BF16; a.workspace = workspace;
+  hipError_t e = mscan::launch_group_norm_bwd(a, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? MAMBA_SCAN_OK : MAMBA_SCAN_ERR_HIP;
 }
 

@@ -279,4 +279,87 @@ struct SsdVarlenArgs {
 };
 hipError_t launch_ssd_varlen(const SsdVarlenArgs& a, const SsdVarlenPlan& p, hipStream_t stream);
 
+// Linear attention with a fixed decay per head over packed or equal sequences, and its gradient
+// (linear_attention.hip), bf16 io.
+struct LinearAttentionPlan {
+  int shift;           // pieces of 2^shift tokens, at least 64
+  int whole;           // packed: a sequence of at most 2^whole tokens is one piece
+  bool cut;            // a sequence may have more than one piece: two more passes and a workspace
+  int64_t np;          // equal sequences: pieces of each
+  int64_t pieces;      // piece numbers (of packed sequences some name no piece)
+  int64_t full;        // numbers of pieces that another one of the sequence follows
+  int64_t folds;       // numbers of cut sequences
+  int64_t parts;       // states in the workspace
+  int64_t wgs;         // workgroups per piece
+  size_t off_later;    // workspace: (parts, H, V, K) fp32; for the gradient once more, of the state's gradient
+  size_t ws_total;
+};
+// longest: a bound of packed sequences' lengths, 0: unknown
+LinearAttentionPlan make_linear_attention_plan(int64_t nseq, int64_t total, int64_t nheads, int64_t kdim, int64_t vdim,
+                                               bool packed, int64_t longest, bool backward);
+
+struct LinearAttentionArgs {
+  const void* q;          // (total, H, K)
+  const void* k;          // (total, H, K)
+  const void* v;          // (total, H, V)
+  const void* dout;       // (total, H, V): gradient of o
+  const float* log_decay; // (H)
+  const int64_t* cu;      // (nseq + 1), or NULL: equal sequences
+  const float* initial_state;     // (entries, H, V, K) or NULL
+  float* final_state;             // forward OUT or NULL
+  const float* d_final_state;
+  float* d_initial_state;
+  const int64_t* slots;   // (nseq) or NULL: sequence s has entry s
+  const int64_t* positions;   // (nseq) or NULL: every sequence continues its entry
+  void* o;                // (total, H, V), contiguous
+  void* dq;               // (total, H, K)
+  void* dk;
+  void* dv;               // (total, H, V)
+  int64_t nseq, total, nslots, nheads, kdim, vdim;
+  int64_t q_stride, k_stride, v_stride, dout_stride;   // elements between tokens
+  float scale;
+  bool backward;
+  void* workspace;
+};
+hipError_t launch_linear_attention(const LinearAttentionArgs& a, const LinearAttentionPlan& p, hipStream_t stream);
+
+// One token per row through it (linear_attention_step.hip).
+struct LinearAttentionStepArgs {
+  const void* q;          // (batch, H, K) io
+  const void* k;
+  const void* v;          // (batch, H, V) io
+  const float* log_decay; // (H)
+  float* state;           // (nslots, H, V, K)
+  const int64_t* slots;   // (batch) or NULL: row i has slot i
+  const int64_t* positions;   // (batch)
+  void* o;                // (batch, H, V) io
+  int64_t batch, nslots, nheads, kdim, vdim, q_stride, k_stride, v_stride;
+  float scale;
+  int io_bf16;
+};
+
+int linear_attention_step_slice(int64_t batch, int64_t nheads, int64_t kdim, int64_t vdim);   // values per workgroup
+hipError_t launch_linear_attention_step(const LinearAttentionStepArgs& a, hipStream_t stream);
+
+// Norm of groups of channels with an activation, and its gradient (group_norm.hip).
+struct GroupNormArgs {
+  const void* dy;         // (rows, groups, width) io; gradient only
+  const void* x;          // (rows, groups, width) io
+  const void* z;          // the gate, z_stride elements between rows, or NULL
+  const float* weight;    // (groups, width) or NULL
+  const float* bias;
+  void* y;                // forward: y; gradient: dx
+  void* dz;               // gradient, iff z
+  float* dweight;         // gradient, or NULL
+  float* dbias;
+  int64_t rows, groups, width, z_stride;
+  float eps;
+  int center, silu, io_bf16;
+  void* workspace;        // gradient: (parts, 2, groups, width) fp32
+};
+
+int64_t group_norm_bwd_parts(int64_t rows, int64_t groups, int64_t width);   // at most
+hipError_t launch_group_norm_fwd(const GroupNormArgs& a, hipStream_t stream);
+hipError_t launch_group_norm_bwd(const GroupNormArgs& a, hipStream_t stream);
+
 }  // namespace mscan

@@ -48,9 +48,10 @@ struct Run {
   int64_t k;            // the run's number in it
 };
 
-// The run of a uniform number; whole waves.  Looks at 64 offsets at a time.
+// The run that a uniform number would be if its sequence had it (run 0 of a sequence without tokens among them);
+// whole waves.  Looks at 64 offsets at a time.
 template <bool kFull>
-__device__ __forceinline__ Run find_run(const Packed& p, int64_t number, int shift) {
+__device__ __forceinline__ Run locate_run(const Packed& p, int64_t number, int shift) {
   const int lane = threadIdx.x & 63;
   int64_t lo = 0, n = p.nseq;
   while (n > 63) {
@@ -70,8 +71,15 @@ __device__ __forceinline__ Run find_run(const Packed& p, int64_t number, int shi
   r.start = lane64(v, c - 1);
   r.stop = lane64(v, c);
   r.k = number - ((r.start >> shift) + (kFull ? 0 : r.s));
-  // (k < 0 only where offsets fall)
-  if (r.k < 0 || r.start + ((r.k + (kFull ? 1 : 0)) << shift) >= r.stop) r.s = -1;
+  if (r.k < 0) r.s = -1;   // only where offsets fall
+  return r;
+}
+
+// The run of a uniform number; whole waves.
+template <bool kFull>
+__device__ __forceinline__ Run find_run(const Packed& p, int64_t number, int shift) {
+  Run r = locate_run<kFull>(p, number, shift);
+  if (r.start + ((r.k + (kFull ? 1 : 0)) << shift) >= r.stop) r.s = -1;
   return r;
 }
 
