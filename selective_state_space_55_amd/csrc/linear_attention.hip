@@ -21,11 +21,14 @@
 #include "packed.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace mscan {
 namespace {
 
 constexpr int kQ = 64;   // tokens per chunk
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int kOut = 0x7ffffff0;   // a buffer offset past any descriptor's end
 
 struct Role {
@@ -55,6 +58,7 @@ struct LaArgs {
   int np;              // equal sequences: pieces of each
   int shift, whole;    // pieces of 2^shift tokens; packed sequences of at most 2^whole are not cut
   int H, KV;
+  int exact;           // a state leaves the call, or may: v goes into it in three parts, else in two
   float scale;
 };
 
@@ -63,27 +67,48 @@ __device__ __forceinline__ uint32_t hi16x2(float lo, float hi) {
 }
 __device__ __forceinline__ float trunc16(float v) { return __uint_as_float(__float_as_uint(v) & 0xffff0000u); }
 
+__device__ __forceinline__ f32x4 product(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 product(bf16x8 a, bf16x8 b, f32x16 c) { return mfma(a, b, c); }
+
 // index m of 32 with bits 2 and 3 exchanged: where operand row m takes row turn(m) of its array, an accumulator's
 // registers 8 s .. 8 s + 7 hold the array's rows 16 s + 8 h .. + 7 (h the lane's half), which is an operand's k order
 __device__ __forceinline__ int turn(int m) { return (m & 19) | ((m & 4) << 1) | ((m & 8) >> 1); }
 
-// Operand of a 32x32x16 MFMA whose k index runs along the rows of a row-major tile: lane l gets rows k0 + 8 (l / 32) ..
-// + 7 of column n0 + turn(l % 32).  (lds_opnd_tr of mfma.h with the columns' blocks of four exchanged.)
-__device__ __forceinline__ bf16x8 opnd_tr(const uint16_t* base, int pitch, int k0, int n0, int lane) {
+// Operands of an MFMA whose k index runs along the rows of a row-major tile, by two transposing reads of 4 rows each; in a
+// 16-lane group the lane a + 4 kk addresses row kk and the four columns of a.
+// 32x32x16: lane l gets rows k0 + 8 (l / 32) .. + 7 of column n0 + turn(l % 32)
+__device__ __forceinline__ bf16x8 opnd32(const uint16_t* base, int pitch, int k0, int n0, int lane) {
   const int g = lane >> 4, m = lane & 15, a = m & 3;
   const uint16_t* p = base + (k0 + 8 * (g >> 1) + (m >> 2)) * pitch + n0 + 16 * (g & 1) + 4 * ((a >> 1) | ((a & 1) << 1));
   const uint2 lo = lds_tr16(p);
   const uint2 hi = lds_tr16(p + 4 * pitch);
   return __builtin_bit_cast(bf16x8, make_uint4(lo.x, lo.y, hi.x, hi.y));
 }
+// 16x16x32: lane l gets rows k0 + 8 (l / 16) .. + 7 of column n0 + step (l % 16 / 4) + l % 4
+__device__ __forceinline__ bf16x8 opnd16(const uint16_t* base, int pitch, int k0, int n0, int step, int lane) {
+  const uint16_t* p = base + (k0 + 8 * (lane >> 4) + ((lane >> 2) & 3)) * pitch + n0 + step * (lane & 3);
+  const uint2 lo = lds_tr16(p);
+  const uint2 hi = lds_tr16(p + 4 * pitch);
+  return __builtin_bit_cast(bf16x8, make_uint4(lo.x, lo.y, hi.x, hi.y));
+}
+
+__device__ __forceinline__ bf16x8 words(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_bit_cast(bf16x8, make_uint4(a, b, c, d));
+}
 
 __device__ __forceinline__ float power(float l2, float x) { return x == 0.0f ? 1.0f : __builtin_amdgcn_exp2f(x * l2); }
 
-template <int A, int NW, bool kAgg>
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
+
+// A: width of q and k, rounded up; CW: columns of a wave
+template <int A, int CW, bool kAgg>
 struct Lds {
-  static constexpr int kRowQ = A + 8, kRowK = A + 16, kRowV = NW * 32 + 16;
-  static constexpr int kQs = kAgg ? 0 : kQ * kRowQ, kKs = kQ * kRowK, kVs = kQ * kRowV;
-  static constexpr size_t bytes() { return 2 * (size_t)(kQs + kKs + kVs) + 4 * 2 * kQ; }
+  // pitches that spread the rows of one read over the banks
+  static constexpr int kRowQ = CW == 32 ? A + 8 : A + 16, kRowK = A + 16, kRowV = kWaves * CW + 16, kRowP = kQ + 8;
+  static constexpr int kQs = kAgg ? 0 : kQ * kRowQ, kKs = kQ * kRowK, kVs = kQ * kRowV, kPs = kAgg ? 0 : 2 * kQ * kRowP;
+  static constexpr size_t bytes() { return 2 * (size_t)(kQs + kKs + kVs + kPs) + 4 * (2 * kQ + (kAgg ? 0 : 256)); }
 };
 
 __device__ __forceinline__ int64_t part_of(int64_t b, int64_t s) { return b + min(b, s); }
@@ -94,19 +119,24 @@ struct Piece {
   int64_t k, n;   // number, and pieces of the sequence
 };
 
+// Workgroups that the tiles leave room for on a CU (160 KB of LDS), which is waves on a SIMD
+constexpr int per_cu(int A, int CW) { return A == 256 ? 1 : A == 64 && CW == 16 ? 3 : 2; }
+
 // kAgg: only the state that a piece would end with from zero
-template <int A, int NW, bool kAgg>
-__global__ __launch_bounds__(64 * NW, A == 256 ? 1 : 2) void linear_attention_kernel(LaArgs a) {
-  using L = Lds<A, NW, kAgg>;
-  constexpr int NT = A / 32, NS = A / 16, kThreads = 64 * NW;
+template <int A, int CW, bool kAgg, int kParts>
+__global__ __launch_bounds__(kThreads, per_cu(A, CW)) void linear_attention_kernel(LaArgs a) {
+  using L = Lds<A, CW, kAgg>;
+  constexpr int NB = A / 32;
   extern __shared__ __align__(16) uint16_t sm[];
-  const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h32 = lane >> 5;
+  const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   uint16_t* Qs = sm;
   uint16_t* Ks = Qs + L::kQs;
   uint16_t* Vs = Ks + L::kKs;
-  float* into = reinterpret_cast<float*>(Vs + L::kVs);   // lam^(what follows in the chunk), by token
-  float* half = into + kQ;                               // lam^(32 - j) for the first 32 tokens
+  uint16_t* Ps = Vs + L::kVs;                            // the decayed scores, token i's row: bf16 hi, and kQ rows on the rest
+  float* into = reinterpret_cast<float*>(Ps + L::kPs);   // lam^(what follows in the chunk), by token
+  float* back = into + kQ;                               // scale lam^(48 - y) by y
+  float* diag = back + kQ;                               // scale lam^(i - j) by 16 i + j
   lds_poison(sm, (int)L::bytes());
 
   // eight units at a time, each unit's workgroups on one XCD
@@ -142,62 +172,55 @@ __global__ __launch_bounds__(64 * NW, A == 256 ? 1 : 2) void linear_attention_ke
   const int64_t t_first = np == 1 ? start : start + (k << a.shift);
   const int64_t t_end = np == 1 ? stop : min(stop, t_first + ((int64_t)1 << a.shift));
   const int64_t part = (a.seq.cu ? part_of(start >> a.shift, s) : s * np) + k;
-  const int64_t nchunk = (t_end - t_first + kQ - 1) / kQ;
+  const int nchunk = (int)((t_end - t_first + kQ - 1) / kQ);   // (an array of 2^31 chunks fits no memory)
+  const int rest = (int)((t_end - t_first - 1) % kQ) + 1;     // tokens of the last one
   const int A_ = R.A, cols = min(R.slab, R.B - b0);
-  const bool live = w * 32 < cols;
+  const bool live = w * CW < cols;
 
   const float ld = a.log_decay[h], l2 = ld * 1.4426950408889634f;
   const float e = later ? 0.0f : 1.0f;   // decays between a token's entry and the state that it reads
 
-  const uint16_t* qb = kAgg ? nullptr : R.q + (int64_t)h * A_;
-  const uint16_t* kb = R.k + (int64_t)h * A_;
-  const uint16_t* vb = R.v + (int64_t)h * R.B + b0;
-
-  auto tokens = [&](int64_t c, int64_t& t0) -> int {   // of chunk c, in the order they are taken
-    if (later) {
-      const int64_t hi = t_end - c * kQ;
-      t0 = max(t_first, hi - kQ);
-      return (int)(hi - t0);
-    }
-    t0 = t_first + c * kQ;
-    return (int)min(t_end - t0, (int64_t)kQ);
-  };
   auto ld16 = [&](__amdgpu_buffer_rsrc_t r, int off) -> uint4 {
     return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
   };
+  // a value that the compiler takes as new each time: what is added to it is formed where it is used, not
+  // kept in a register over the loop
+  auto anew = [](int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+  };
 
+  // Chunks are taken from the first token on, or `later` from the last one back; token i of a chunk in the order they are
+  // taken is row i of a tile.  A chunk's descriptor ends with its last token, so that rows past its n tokens, which lie
+  // behind the end, or in front of the start at an unsigned offset past it, load as 0.
   constexpr int kCpr = A / 8, kRpp = kThreads / kCpr, kR = kQ / kRpp;   // q, k: 16-byte pieces per row, rows per pass
-  constexpr int kVpr = NW * 4, kVr = kQ * kVpr / kThreads;              // v: 16 rows per pass
+  constexpr int kVpr = kWaves * CW / 8, kVr = kQ * kVpr / kThreads;     // v
+  // The next chunk's loads go out at a chunk's start where they fit the registers beside the rest, else behind the state's update
+  constexpr bool kLate = !kAgg && 2 * kR + kVr > 12;
   const int kr = tid / kCpr, kc = (tid % kCpr) * 8;
   const int vr = tid / kVpr, vc = (tid % kVpr) * 8;
-  const bool k_in = kc < A_, v_in = vc < cols;
+  const int out_of = later ? -16 : kOut;   // stays past the end (2^31 - 32 bytes at most) with a chunk's rows added
+  const int64_t t_start = later ? t_end - (nchunk == 1 ? rest : kQ) : t_first;
+  const uint16_t* kp = R.k + t_start * R.k_stride + (int64_t)h * A_;
+  const uint16_t* vp = R.v + t_start * R.v_stride + (int64_t)h * R.B + b0;
+  const uint16_t* qp = kAgg ? nullptr : R.q + t_start * R.q_stride + (int64_t)h * A_;
+  const int o_stride = a.H * R.B;
+  uint16_t* op = kAgg ? nullptr : R.o + t_start * o_stride + (int64_t)h * R.B + b0;
   uint4 qq[kAgg ? 1 : kR], kq[kR], vq[kVr];
-  auto load = [&](int64_t c) {
-    int64_t t0;
-    const int n = tokens(c, t0);
-    const auto rk = make_rsrc(kb + t0 * R.k_stride, ((n - 1) * R.k_stride + A_) * 2);
-    const auto rv = make_rsrc(vb + t0 * R.v_stride, ((n - 1) * R.v_stride + cols) * 2);
+  auto load_rows = [&](const uint16_t* base, int stride, int width, int n, int row, int col, int rows, auto& to) {
+    const auto r = make_rsrc(base, ((n - 1) * stride + width) * 2);
+    const uint32_t step = (later ? -rows : rows) * stride * 2;
+    uint32_t off = anew(col < width ? ((later ? n - 1 - row : row) * stride + col) * 2 : out_of);
 #pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      const int i = kr + r * kRpp, row = later ? n - 1 - i : i;
-      const bool in = k_in && i < n;
-      kq[r] = ld16(rk, in ? (row * R.k_stride + kc) * 2 : kOut);
+    for (int i = 0; i < (int)(sizeof(to) / 16); ++i) {
+      to[i] = ld16(r, (int)off);
+      off += step;
     }
-    if constexpr (!kAgg) {
-      const auto rq = make_rsrc(qb + t0 * R.q_stride, ((n - 1) * R.q_stride + A_) * 2);
-#pragma unroll
-      for (int r = 0; r < kR; ++r) {
-        const int i = kr + r * kRpp, row = later ? n - 1 - i : i;
-        const bool in = k_in && i < n;
-        qq[r] = ld16(rq, in ? (row * R.q_stride + kc) * 2 : kOut);
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < kVr; ++r) {
-      const int i = vr + r * 16, row = later ? n - 1 - i : i;
-      const bool in = v_in && i < n;
-      vq[r] = ld16(rv, in ? (row * R.v_stride + vc) * 2 : kOut);
-    }
+  };
+  auto load = [&](int n) {
+    load_rows(kp, R.k_stride, A_, n, kr, kc, kRpp, kq);
+    if constexpr (!kAgg) load_rows(qp, R.q_stride, A_, n, kr, kc, kRpp, qq);
+    load_rows(vp, R.v_stride, cols, n, vr, vc, kQ / kVr, vq);
   };
   auto store_tiles = [&]() {
 #pragma unroll
@@ -206,212 +229,244 @@ __global__ __launch_bounds__(64 * NW, A == 256 ? 1 : 2) void linear_attention_ke
       if constexpr (!kAgg) *reinterpret_cast<uint4*>(Qs + (kr + r * kRpp) * L::kRowQ + kc) = qq[r];
     }
 #pragma unroll
-    for (int r = 0; r < kVr; ++r) *reinterpret_cast<uint4*>(Vs + (vr + r * 16) * L::kRowV + vc) = vq[r];
+    for (int r = 0; r < kVr; ++r) *reinterpret_cast<uint4*>(Vs + (vr + r * (kQ / kVr)) * L::kRowV + vc) = vq[r];
   };
 
-  if (nchunk > 0) load(0);
+  if (nchunk > 0) load(nchunk == 1 ? rest : kQ);
 
-  // the lane's column of the state, and the entry it comes from
-  const int64_t bcol = b0 + w * 32 + turn(l32);
-  const bool has_col = live && w * 32 + turn(l32) < cols;
+  // The state: f32x16 tiles of 32 rows x 32 columns, registers 8 s + r row 16 s + 8 (lane / 32) + r of column turn(lane % 32);
+  // or pairs of f32x4 tiles of 32 rows x 16 columns, register 4 t + r row 8 (lane / 16) + 4 t + r of column lane % 16.
+  // Either way a lane holds eight rows in a row, `step` of these to the next.
+  constexpr int kOct = CW == 32 ? 2 * NB : NB, kStep = CW == 32 ? 16 : 32;
+  const int wcol = w * CW + (CW == 32 ? turn(lane & 31) : lane & 15);
+  const int row8 = 8 * (CW == 32 ? lane >> 5 : lane >> 4);
+  const bool has_col = wcol < cols;
   const int64_t entry = a.seq.slots ? seq_slot(a.seq, s) : s;
   const bool started = entry >= 0 && (!a.seq.positions || a.seq.positions[s] > 0);
   const int64_t at_head = (int64_t)h * a.KV, row_state = (int64_t)a.H * a.KV;
   const float* from = kAgg ? nullptr : np > 1 ? R.ws + part * row_state + at_head
                     : R.from && started ? R.from + entry * row_state + at_head : nullptr;
-  f32x16 S[NT];
+  typedef typename std::conditional<CW == 32, f32x16, f32x4>::type Tile;
+  Tile S[CW == 32 ? NB : 2 * NB];
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int o = 0; o < kOct; ++o) {
+    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const int ra = o * kStep + row8;
+    if (from && has_col && ra < A_) {
+      const float* p = from + (int64_t)ra * R.sa + (int64_t)(b0 + wcol) * R.sb;
+      if (R.sa == 1) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(p), z = *reinterpret_cast<const f32x4*>(p + 4);
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const int64_t ra = n * 32 + g * 16 + h32 * 8;
-      const bool in = from && has_col && ra < A_;
-      float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (in) {
-        const float* p = from + ra * R.sa + bcol * R.sb;
-        if (R.sa == 1) {
-          const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
-          f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w; f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
-        } else {
+        for (int j = 0; j < 8; ++j) f[j] = j < 4 ? x[j % 4] : z[j % 4];
+      } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = p[(int64_t)j * R.sa];
-        }
+        for (int j = 0; j < 8; ++j) f[j] = p[(int64_t)j * R.sa];
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) S[n][8 * g + j] = f[j];
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (CW == 32) S[o / 2][8 * (o & 1) + j] = f[j];
+      else S[2 * o + j / 4][j % 4] = f[j];
+    }
+  }
+  auto row_of = [&](int o, int j) -> float {
+    if constexpr (CW == 32) return S[o / 2][8 * (o & 1) + j];
+    else return S[2 * o + j / 4][j % 4];
+  };
 
-  // lam^(i - j) of a diagonal tile of P^T: lane = token i, register 8 s + r = token j = 16 s + 8 h + r; and which are causal
-  float diag[kAgg ? 1 : 16];
-  uint32_t causal[kAgg ? 1 : 8];
-  float li = 0.0f, out0 = 0.0f, out1 = 0.0f;
+  float li = 0.0f, out[64 / CW];
   if constexpr (!kAgg) {
+    for (int x = tid; x < 256; x += kThreads) diag[x] = a.scale * power(l2, (float)max((x >> 4) - (x & 15), 0));
+    li = power(l2, (float)(lane & 15));
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int j = 16 * (r / 8) + 8 * h32 + r % 8;
-      diag[r] = j <= l32 ? a.scale * power(l2, (float)(l32 - j)) : 0.0f;
-      if (r % 2 == 0) causal[r / 2] = (j <= l32 ? 0xffffu : 0u) | (j + 1 <= l32 ? 0xffff0000u : 0u);
-    }
-    li = power(l2, (float)l32);
-    out0 = R.c_out * power(l2, (float)l32 + e);
-    out1 = R.c_out * power(l2, (float)(l32 + 32) + e);
-    if (tid < 32) half[tid] = a.scale * power(l2, (float)(32 - tid));
+    for (int i = 0; i < 64 / CW; ++i) out[i] = R.c_out * power(l2, (float)(CW * i + lane % CW) + e);
+    if (tid < kQ) back[tid] = a.scale * power(l2, (float)max(48 - tid, 0));
   }
 
-  for (int64_t c = 0; c < nchunk; ++c) {
-    int64_t t0;
-    const int n = tokens(c, t0);
+  // The state's decay over a chunk, as a factor whose rounding error goes into the next chunk's, so that a head that forgets
+  // slowly does not add it up
+  const double whole = exp((double)kQ * (double)ld), part_chunk = exp((double)rest * (double)ld);
+  const bool carry = whole > 0x1p-100 && whole < 0x1p100;   // (else the factor has few bits or none)
+  const double per_whole = 1.0 / whole;
+  double off = 0.0;
+
+  for (int c = 0; c < nchunk; ++c) {
+    const int n = c + 1 == nchunk ? rest : kQ;
     if (c) lds_barrier();   // every wave has read the previous chunk
     store_tiles();
     if (tid < kQ && (c == 0 || n < kQ)) into[tid] = tid < n ? R.c_in * power(l2, (float)(n - tid) - e) : 0.0f;
     lds_barrier();
-    if (c + 1 < nchunk) load(c + 1);
-    if (!live) continue;
-
-    f32x16 y[2] = {};
+    const int next = c + 2 >= nchunk ? rest : kQ;   // tokens of the next chunk, and how far it is
+    const int64_t ahead = later ? -next : kQ;
+    auto load_next = [&]() {
+      if (c + 1 == nchunk) return;
+      kp += ahead * R.k_stride;
+      vp += ahead * R.v_stride;
+      if constexpr (!kAgg) qp += ahead * R.q_stride;
+      load(next);
+    };
+    if constexpr (!kLate) load_next();
     if constexpr (!kAgg) {
+      // P^T in 16 x 16 tiles (token blocks i, j <= i), three to a wave: ten, and the two behind their tokens that the
+      // products below meet, which come out as zeros
+      const int l16 = anew(lane & 15), h16 = anew(lane >> 4);
 #pragma unroll
-      for (int ks = 0; ks < NS; ++ks) {
-        uint32_t hi[4], lo[4];
+      for (int u = 0; u < 3; ++u) {
+        const int x = u * kWaves + w;
+        const int i = (int)(0x203333222110ull >> (4 * x)) & 15, j = (int)(0x313210210100ull >> (4 * x)) & 15;
+        f32x4 m = {};
+#pragma unroll
+        for (int ks = 0; ks < NB; ++ks)
+          m = product(lds_b8(Ks + (16 * j + l16) * L::kRowK + 32 * ks + 8 * h16),
+                      lds_b8(Qs + (16 * i + l16) * L::kRowQ + 32 * ks + 8 * h16), m);
+        // (no branch here: what a branch skips must not count as the wait for the products)
+        const float4 wt = *reinterpret_cast<const float4*>(i <= j ? diag + 16 * l16 + 4 * h16 : back + 48 - 16 * (i - j) + 4 * h16);
+        const float wa[4] = {wt.x, wt.y, wt.z, wt.w}, of = i == j ? 1.0f : li;
+        const int last = l16 - 4 * h16 + 16 * (i - j);   // the last register that is not behind the token
+        float f[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) f[r] = r <= last ? m[r] * (wa[r] * of) : 0.0f;
+        uint16_t* p = Ps + (16 * i + l16) * L::kRowP + 16 * j + 4 * h16;
+        *reinterpret_cast<uint2*>(p) = make_uint2(hi16x2(f[0], f[1]), hi16x2(f[2], f[3]));
+        *reinterpret_cast<uint2*>(p + kQ * L::kRowP) = make_uint2(pack_bf16x2(f[0] - trunc16(f[0]), f[1] - trunc16(f[1])),
+                                                                  pack_bf16x2(f[2] - trunc16(f[2]), f[3] - trunc16(f[3])));
+      }
+    }
+
+    const double exactly = (n == kQ ? whole : part_chunk) * (1.0 + off);
+    const float fade = (float)exactly;
+    off = carry ? (exactly - (double)fade) * per_whole : 0.0;
+    Tile y[64 / CW];
+    bf16x8 xf[CW == 32 ? 4 : 2];
+    if (live) {
+      const int lc = anew(lane % CW), k8 = anew(8 * (lane / CW));   // an operand's row or column, and its first k
+      if constexpr (!kAgg) {
+#pragma unroll
+        for (int o = 0; o < kOct; ++o) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float v0 = row_of(o, 2 * j), v1 = row_of(o, 2 * j + 1);
+            hi[j] = hi16x2(v0, v1);
+            lo[j] = pack_bf16x2(v0 - trunc16(v0), v1 - trunc16(v1));
+          }
+          const bf16x8 sh = words(hi[0], hi[1], hi[2], hi[3]), sl = words(lo[0], lo[1], lo[2], lo[3]);
+          bf16x8 q[64 / CW];
+#pragma unroll
+          for (int i = 0; i < 64 / CW; ++i) q[i] = lds_b8(Qs + (CW * i + lc) * L::kRowQ + kStep * o + k8);
+#pragma unroll
+          for (int i = 0; i < 64 / CW; ++i) y[i] = product(sl, q[i], o ? y[i] : Tile{});
+#pragma unroll
+          for (int i = 0; i < 64 / CW; ++i) y[i] = product(sh, q[i], y[i]);
+        }
+      }
+#pragma unroll
+      for (auto& tile : S)
+#pragma unroll
+        for (int r = 0; r < (CW == 32 ? 16 : 4); ++r) tile[r] *= fade;
+#pragma unroll
+      for (int ks = 0; ks < kQ / kStep; ++ks) {
+        if constexpr (CW == 32) xf[ks] = opnd32(Vs, L::kRowV, 16 * ks, w * 32, lane);
+        else xf[ks] = opnd16(Vs, L::kRowV, 32 * ks, w * 16, 4, lane);
+        const float4 w0 = *reinterpret_cast<const float4*>(into + kStep * ks + k8);
+        const float4 w1 = *reinterpret_cast<const float4*>(into + kStep * ks + k8 + 4);
+        const uint4 xv = __builtin_bit_cast(uint4, xf[ks]);
+        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+        const float wt[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+        uint32_t part3[3][4];   // hi, mid and lo bits of the weighted v
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float v0 = S[ks / 2][8 * (ks & 1) + 2 * j], v1 = S[ks / 2][8 * (ks & 1) + 2 * j + 1];
-          hi[j] = hi16x2(v0, v1);
-          lo[j] = pack_bf16x2(v0 - trunc16(v0), v1 - trunc16(v1));
+          const float v0 = bf16_lo(xw[j]) * wt[2 * j], v1 = bf16_hi(xw[j]) * wt[2 * j + 1];
+          const float r0 = v0 - trunc16(v0), r1 = v1 - trunc16(v1);
+          part3[0][j] = hi16x2(v0, v1);
+          part3[1][j] = kParts == 3 ? hi16x2(r0, r1) : pack_bf16x2(r0, r1);
+          if constexpr (kParts == 3) part3[2][j] = hi16x2(r0 - trunc16(r0), r1 - trunc16(r1));
         }
-        const bf16x8 sh = __builtin_bit_cast(bf16x8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-        const bf16x8 sl = __builtin_bit_cast(bf16x8, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-        const bf16x8 q0 = lds_b8(Qs + l32 * L::kRowQ + 16 * ks + 8 * h32);
-        const bf16x8 q1 = lds_b8(Qs + (32 + l32) * L::kRowQ + 16 * ks + 8 * h32);
-        y[0] = mfma(sl, q0, y[0]);
-        y[1] = mfma(sl, q1, y[1]);
-        y[0] = mfma(sh, q0, y[0]);
-        y[1] = mfma(sh, q1, y[1]);
+        constexpr int kTiles = sizeof(S) / sizeof(Tile);
+        bf16x8 key[2];
+#pragma unroll
+        for (int b = 0; b < kTiles; b += 2) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if constexpr (CW == 32) key[u] = opnd32(Ks, L::kRowK, 16 * ks, 32 * (b + u), lane);
+            else key[u] = opnd16(Ks, L::kRowK, 32 * ks, 16 * b + 4 * u, 8, lane);
+          }
+#pragma unroll
+          for (int x = kParts - 1; x >= 0; --x)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) S[b + u] = product(key[u], words(part3[x][0], part3[x][1], part3[x][2], part3[x][3]), S[b + u]);
+        }
       }
     }
-    __builtin_amdgcn_sched_barrier(0);   // the phases' registers do not fit side by side
-    const float gone = expm1f((float)n * ld);
-    if (gone > -0.5f) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) S[t][r] = fmaf(S[t][r], gone, S[t][r]);
-    } else {
-      const float at = power(l2, (float)n);
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) S[t][r] *= at;
-    }
-    bf16x8 xf[4];
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) xf[ks] = opnd_tr(Vs, L::kRowV, 16 * ks, w * 32, lane);
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      const float4 w0 = *reinterpret_cast<const float4*>(into + 16 * ks + 8 * h32);
-      const float4 w1 = *reinterpret_cast<const float4*>(into + 16 * ks + 8 * h32 + 4);
-      const uint4 xv = __builtin_bit_cast(uint4, xf[ks]);
-      const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
-      const float wt[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-      uint32_t hi[4], mid[4], lo[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float v0 = bf16_lo(xw[j]) * wt[2 * j], v1 = bf16_hi(xw[j]) * wt[2 * j + 1];
-        const float r0 = v0 - trunc16(v0), r1 = v1 - trunc16(v1);
-        hi[j] = hi16x2(v0, v1);
-        mid[j] = hi16x2(r0, r1);
-        lo[j] = hi16x2(r0 - trunc16(r0), r1 - trunc16(r1));
-      }
-      const bf16x8 xh = __builtin_bit_cast(bf16x8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-      const bf16x8 xm = __builtin_bit_cast(bf16x8, make_uint4(mid[0], mid[1], mid[2], mid[3]));
-      const bf16x8 xl = __builtin_bit_cast(bf16x8, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const bf16x8 kt = opnd_tr(Ks, L::kRowK, 16 * ks, t * 32, lane);
-        S[t] = mfma(kt, xl, S[t]);
-        S[t] = mfma(kt, xm, S[t]);
-        S[t] = mfma(kt, xh, S[t]);
-      }
-    }
+    if constexpr (kLate) load_next();
     if constexpr (!kAgg) {
-      __builtin_amdgcn_sched_barrier(0);
+      lds_barrier();   // P
+      if (!live) continue;   // (and store nothing)
+      const int lc = anew(lane % CW), k8 = anew(8 * (lane / CW));
       // A NaN or infinity in a token's v makes all of its column's state non-finite, so one state per column tells of
       // it.  It would meet P's zeros in front of the token: it is taken out of V and put back below.
       const bool bad = __ballot(!(fabsf(S[0][0]) < INFINITY)) != 0;
       if (bad) {
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          uint4 v = __builtin_bit_cast(uint4, xf[ks]);
+        for (auto& f : xf) {
+          const uint4 v = __builtin_bit_cast(uint4, f);
           uint32_t xw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             if ((xw[j] & 0x7f80u) == 0x7f80u) xw[j] &= 0xffff0000u;
             if ((xw[j] & 0x7f800000u) == 0x7f800000u) xw[j] &= 0xffffu;
           }
-          xf[ks] = __builtin_bit_cast(bf16x8, make_uint4(xw[0], xw[1], xw[2], xw[3]));
+          f = words(xw[0], xw[1], xw[2], xw[3]);
         }
       }
-      const int o_stride = a.H * R.B;
-      const auto ro = make_rsrc(R.o + t0 * o_stride + (int64_t)h * R.B + b0, ((n - 1) * o_stride + cols) * 2);
+      const auto ro = make_rsrc(op, ((n - 1) * o_stride + cols) * 2);
+      op += ahead * o_stride;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 64 / CW; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) y[i][r] *= i ? out1 : out0;
+        for (int r = 0; r < (CW == 32 ? 16 : 4); ++r) y[i][r] *= out[i];
+      // + V^T P^T over the tokens up to each tile's last
 #pragma unroll
-        for (int jt = 0; jt <= i; ++jt) {
-          __builtin_amdgcn_sched_barrier(0);
-          f32x16 m = {};
+      for (int ks = 0; ks < kQ / kStep; ++ks)
 #pragma unroll
-          for (int ks = 0; ks < NS; ++ks)
-            m = mfma(lds_b8(Ks + (jt * 32 + turn(l32)) * L::kRowK + 16 * ks + 8 * h32),
-                     lds_b8(Qs + (i * 32 + l32) * L::kRowQ + 16 * ks + 8 * h32), m);
+        for (int x = 1; x >= 0; --x)
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            float f[8];
-            if (jt == i) {
+          for (int i = 0; i < 64 / CW; ++i) {
+            if (CW * (i + 1) <= kStep * ks) continue;
+            y[i] = product(xf[ks], lds_b8(Ps + (x * kQ + CW * i + lc) * L::kRowP + kStep * ks + k8), y[i]);
+          }
+      if (bad) {   // NaN from a non-finite token on
+        for (int j = 0; j < kQ; ++j) {
+          const uint16_t* v = Vs + j * L::kRowV + w * CW;
 #pragma unroll
-              for (int r = 0; r < 8; ++r) f[r] = m[8 * g + r] * diag[8 * g + r];
-            } else {
-              const float4 w0 = *reinterpret_cast<const float4*>(half + 16 * g + 8 * h32);
-              const float4 w1 = *reinterpret_cast<const float4*>(half + 16 * g + 8 * h32 + 4);
-              const float wt[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+          for (int r = 0; r < (CW == 32 ? 16 : 4); ++r) {
+            const float x = __uint_as_float((uint32_t)v[CW == 32 ? 16 * (r / 8) + k8 + r % 8 : k8 / 2 + r] << 16);
 #pragma unroll
-              for (int r = 0; r < 8; ++r) f[r] = m[8 * g + r] * wt[r] * li;
-            }
-            uint32_t ph[4], pl[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t mask = jt == i ? causal[4 * g + j] : ~0u;
-              ph[j] = hi16x2(f[2 * j], f[2 * j + 1]) & mask;
-              pl[j] = pack_bf16x2(f[2 * j] - trunc16(f[2 * j]), f[2 * j + 1] - trunc16(f[2 * j + 1])) & mask;
-            }
-            y[i] = mfma(xf[2 * jt + g], __builtin_bit_cast(bf16x8, make_uint4(pl[0], pl[1], pl[2], pl[3])), y[i]);
-            y[i] = mfma(xf[2 * jt + g], __builtin_bit_cast(bf16x8, make_uint4(ph[0], ph[1], ph[2], ph[3])), y[i]);
+            for (int i = 0; i < 64 / CW; ++i) y[i][r] = fmaf(j <= CW * i + lc ? x : 0.0f, 0.0f, y[i][r]);
           }
         }
-        const int tok = i * 32 + l32;
-        if (bad) {   // NaN from a non-finite token on
-          for (int j = 0; j < 32 * i + 32; ++j) {
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              const uint4 xv = *reinterpret_cast<const uint4*>(Vs + j * L::kRowV + w * 32 + 16 * g + 8 * h32);
-              const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
-#pragma unroll
-              for (int r = 0; r < 8; ++r) {
-                const float x = r & 1 ? bf16_hi(xw[r / 2]) : bf16_lo(xw[r / 2]);
-                y[i][8 * g + r] = fmaf(j <= tok ? x : 0.0f, 0.0f, y[i][8 * g + r]);
-              }
-            }
-          }
-        }
+      }
+      typedef __attribute__((ext_vector_type(4))) unsigned u32x4;
+      auto store = [&](int tok, int ch, u32x4 v) {
         const int row = later ? n - 1 - tok : tok;
+        __builtin_amdgcn_raw_buffer_store_b128(v, ro, ch < cols && tok < n ? (row * o_stride + ch) * 2 : kOut, 0, 0);
+      };
+      if constexpr (CW == 32) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const int ch = w * 32 + 16 * g + 8 * h32;
-          typedef __attribute__((ext_vector_type(4))) unsigned u32x4;
-          const u32x4 v = {pack_bf16x2(y[i][8 * g], y[i][8 * g + 1]), pack_bf16x2(y[i][8 * g + 2], y[i][8 * g + 3]),
-                           pack_bf16x2(y[i][8 * g + 4], y[i][8 * g + 5]), pack_bf16x2(y[i][8 * g + 6], y[i][8 * g + 7])};
-          __builtin_amdgcn_raw_buffer_store_b128(v, ro, ch < cols && tok < n ? (row * o_stride + ch) * 2 : kOut, 0, 0);
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+            store(32 * i + lc, w * 32 + 16 * g + k8,
+                  u32x4{pack_bf16x2(y[i][8 * g], y[i][8 * g + 1]), pack_bf16x2(y[i][8 * g + 2], y[i][8 * g + 3]),
+                        pack_bf16x2(y[i][8 * g + 4], y[i][8 * g + 5]), pack_bf16x2(y[i][8 * g + 6], y[i][8 * g + 7])});
+      } else {
+        // a lane holds channels 4 g .. + 3 (g = lane / 16) of token 16 i + lane % 16; groups 2 p and 2 p + 1 trade, so that
+        // the first has channels 8 p .. + 7 of tile i and the second those of tile i + 1
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const auto x = __builtin_amdgcn_permlane16_swap(pack_bf16x2(y[i][0], y[i][1]), pack_bf16x2(y[i + 1][0], y[i + 1][1]), false, false);
+          const auto z = __builtin_amdgcn_permlane16_swap(pack_bf16x2(y[i][2], y[i][3]), pack_bf16x2(y[i + 1][2], y[i + 1][3]), false, false);
+          store(16 * i + 2 * (k8 & 8) + lc, w * 16 + 4 * (k8 >> 3 & 2), u32x4{x[0], z[0], x[1], z[1]});
         }
       }
     }
@@ -421,21 +476,21 @@ __global__ __launch_bounds__(64 * NW, A == 256 ? 1 : 2) void linear_attention_ke
             : R.to && entry >= 0 && k == (later ? 0 : np - 1) && (nchunk > 0 || !a.seq.slots) ? R.to + entry * row_state + at_head
             : nullptr;
   if (!to || !has_col) return;
+  const int r8 = anew(row8);
+  to += (int64_t)(b0 + anew(wcol)) * R.sb;
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int o = 0; o < kOct; ++o) {
+    const int ra = o * kStep + r8;
+    if (ra >= A_) continue;
+    float* p = to + (int64_t)ra * R.sa;
+    if (R.sa == 1) {
+      *reinterpret_cast<f32x4*>(p) = f32x4{row_of(o, 0), row_of(o, 1), row_of(o, 2), row_of(o, 3)};
+      *reinterpret_cast<f32x4*>(p + 4) = f32x4{row_of(o, 4), row_of(o, 5), row_of(o, 6), row_of(o, 7)};
+    } else {
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const int64_t ra = n * 32 + g * 16 + h32 * 8;
-      if (ra >= A_) continue;
-      float* p = to + ra * R.sa + bcol * R.sb;
-      if (R.sa == 1) {
-        *reinterpret_cast<float4*>(p) = make_float4(S[n][8 * g], S[n][8 * g + 1], S[n][8 * g + 2], S[n][8 * g + 3]);
-        *reinterpret_cast<float4*>(p + 4) = make_float4(S[n][8 * g + 4], S[n][8 * g + 5], S[n][8 * g + 6], S[n][8 * g + 7]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) p[(int64_t)j * R.sa] = S[n][8 * g + j];
-      }
+      for (int j = 0; j < 8; ++j) p[(int64_t)j * R.sa] = row_of(o, j);
     }
+  }
 }
 
 // The fold over a cut sequence's pieces: a piece's own state in the workspace becomes the state that enters it.  A
@@ -473,9 +528,8 @@ __global__ __launch_bounds__(256) void linear_attention_fold_kernel(LaArgs a) {
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (i0 + i >= n) break;
       const int64_t k = later ? n - 1 - (i0 + i) : i0 + i;
-      ws[k * step] = f;
+      if (i0 + i < n) ws[k * step] = f;
       const float at = power(l2, (float)(k == n - 1 ? last : len));
       f.x = fmaf(at, f.x, own[i].x);
       f.y = fmaf(at, f.y, own[i].y);
@@ -486,24 +540,30 @@ __global__ __launch_bounds__(256) void linear_attention_fold_kernel(LaArgs a) {
 }
 
 int pad_of(int64_t width) { return width <= 64 ? 64 : width <= 128 ? 128 : 256; }
-int waves_of(int64_t width) { return width <= 64 ? 2 : 4; }
+int columns_of(int64_t width) { return width <= 64 ? 16 : 32; }   // of a wave
 int slabs_of(int64_t width) { return (int)((width + 127) / 128); }
 
-template <int A, int NW, bool kAgg>
+template <int A, int CW, bool kAgg, int kParts>
 hipError_t launch(const LaArgs& a, hipStream_t s) {
-  constexpr size_t lds = Lds<A, NW, kAgg>::bytes();
-  hipError_t e = hipFuncSetAttribute((const void*)linear_attention_kernel<A, NW, kAgg>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)lds);
+  constexpr size_t lds = Lds<A, CW, kAgg>::bytes();
+  hipError_t e = hipFuncSetAttribute((const void*)linear_attention_kernel<A, CW, kAgg, kParts>,
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
   const dim3 grid((unsigned)((a.units + 7) / 8 * 8 * a.wgs));
-  hipLaunchKernelGGL((linear_attention_kernel<A, NW, kAgg>), grid, dim3(64 * NW), lds, s, a);
+  hipLaunchKernelGGL((linear_attention_kernel<A, CW, kAgg, kParts>), grid, dim3(kThreads), lds, s, a);
   return hipGetLastError();
 }
 
+template <int CW, bool kAgg, int kParts>
+hipError_t launch_pad(int pad, const LaArgs& a, hipStream_t s) {
+  return pad == 64 ? launch<64, CW, kAgg, kParts>(a, s) : pad == 128 ? launch<128, CW, kAgg, kParts>(a, s)
+                                                                     : launch<256, CW, kAgg, kParts>(a, s);
+}
+
 template <bool kAgg>
-hipError_t launch_for(int pad, int waves, const LaArgs& a, hipStream_t s) {
-  if (waves == 2) return pad == 64 ? launch<64, 2, kAgg>(a, s) : pad == 128 ? launch<128, 2, kAgg>(a, s) : launch<256, 2, kAgg>(a, s);
-  return pad == 64 ? launch<64, 4, kAgg>(a, s) : pad == 128 ? launch<128, 4, kAgg>(a, s) : launch<256, 4, kAgg>(a, s);
+hipError_t launch_for(int pad, int columns, const LaArgs& a, hipStream_t s) {
+  if (columns == 16) return a.exact ? launch_pad<16, kAgg, 3>(pad, a, s) : launch_pad<16, kAgg, 2>(pad, a, s);
+  return a.exact ? launch_pad<32, kAgg, 3>(pad, a, s) : launch_pad<32, kAgg, 2>(pad, a, s);
 }
 
 // the roles of `of` (a bit each) that one kernel can take, in one launch; returns what is left
@@ -511,19 +571,19 @@ template <bool kAgg>
 unsigned launch_some(const LaArgs& all, unsigned of, hipStream_t s, hipError_t* e) {
   LaArgs a = all;
   a.nroles = a.wgs = 0;
-  int pad = 0, waves = 0;
+  int pad = 0, columns = 0;
   for (int r = 0; r < 3; ++r) {
     if (!(of >> r & 1)) continue;
     const Role& R = all.role[r];
-    if (a.nroles && (pad_of(R.A) != pad || waves_of(R.B) != waves)) continue;
+    if (a.nroles && (pad_of(R.A) != pad || columns_of(R.B) != columns)) continue;
     pad = pad_of(R.A);
-    waves = waves_of(R.B);
+    columns = columns_of(R.B);
     a.first[a.nroles] = a.wgs;
     a.role[a.nroles++] = R;
     a.wgs += R.slabs;
     of &= ~(1u << r);
   }
-  *e = launch_for<kAgg>(pad, waves, a, s);
+  *e = launch_for<kAgg>(pad, columns, a, s);
   return of;
 }
 
@@ -532,7 +592,7 @@ void set_shape(Role& R, int64_t A, int64_t B, bool transposed, int64_t K) {
   R.sa = transposed ? (int)K : 1;   // the state is (V, K)
   R.sb = transposed ? 1 : (int)K;
   R.slabs = slabs_of(B);
-  R.slab = (int)(((B + 31) / 32 + R.slabs - 1) / R.slabs) * 32;
+  R.slab = (int)(((B + 15) / 16 + R.slabs - 1) / R.slabs) * 16;
 }
 
 }  // namespace
@@ -579,6 +639,7 @@ hipError_t launch_linear_attention(const LinearAttentionArgs& p, const LinearAtt
   a.len = p.total / p.nseq;
   a.np = (int)plan.np; a.shift = plan.shift; a.whole = plan.whole;
   a.H = (int)p.nheads; a.KV = (int)(p.kdim * p.vdim); a.scale = p.scale;
+  a.exact = !p.backward || p.d_initial_state;
   const uint16_t *q = static_cast<const uint16_t*>(p.q), *k = static_cast<const uint16_t*>(p.k),
                  *v = static_cast<const uint16_t*>(p.v), *g = static_cast<const uint16_t*>(p.dout);
   const int sq = (int)p.q_stride, sk = (int)p.k_stride, sv = (int)p.v_stride, sg = (int)p.dout_stride;
