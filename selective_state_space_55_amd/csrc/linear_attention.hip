@@ -72,6 +72,9 @@ __device__ __forceinline__ f32x4 product(bf16x8 a, bf16x8 b, f32x4 c) {
 }
 __device__ __forceinline__ f32x16 product(bf16x8 a, bf16x8 b, f32x16 c) { return mfma(a, b, c); }
 
+// makes the compiler wait for a load here
+__device__ __forceinline__ void arrived(uint4& v) { asm volatile("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w)); }
+
 // index m of 32 with bits 2 and 3 exchanged: where operand row m takes row turn(m) of its array, an accumulator's
 // registers 8 s .. 8 s + 7 hold the array's rows 16 s + 8 h .. + 7 (h the lane's half), which is an operand's k order
 __device__ __forceinline__ int turn(int m) { return (m & 19) | ((m & 4) << 1) | ((m & 8) >> 1); }
@@ -175,7 +178,6 @@ __global__ __launch_bounds__(kThreads, per_cu(A, CW)) void linear_attention_kern
   const int nchunk = (int)((t_end - t_first + kQ - 1) / kQ);   // (an array of 2^31 chunks fits no memory)
   const int rest = (int)((t_end - t_first - 1) % kQ) + 1;     // tokens of the last one
   const int A_ = R.A, cols = min(R.slab, R.B - b0);
-  const bool live = w * CW < cols;
 
   const float ld = a.log_decay[h], l2 = ld * 1.4426950408889634f;
   const float e = later ? 0.0f : 1.0f;   // decays between a token's entry and the state that it reads
@@ -290,6 +292,20 @@ __global__ __launch_bounds__(kThreads, per_cu(A, CW)) void linear_attention_kern
   const double per_whole = 1.0 / whole;
   double off = 0.0;
 
+  // The loads of the state and of the first chunk end here.  Left in flight into the loop, the state's would make each turn
+  // wait at its first use of it, for the next chunk's loads too, and the first chunk's would make the wait for a
+  // chunk's loads one for the stores behind them.
+#pragma unroll
+  for (auto& tile : S) asm volatile("" : "+v"(tile));
+#pragma unroll
+  for (auto& x : kq) arrived(x);
+#pragma unroll
+  for (auto& x : vq) arrived(x);
+  if constexpr (!kAgg) {
+#pragma unroll
+    for (auto& x : qq) arrived(x);
+  }
+
   for (int c = 0; c < nchunk; ++c) {
     const int n = c + 1 == nchunk ? rest : kQ;
     if (c) lds_barrier();   // every wave has read the previous chunk
@@ -338,7 +354,7 @@ __global__ __launch_bounds__(kThreads, per_cu(A, CW)) void linear_attention_kern
     off = carry ? (exactly - (double)fade) * per_whole : 0.0;
     Tile y[64 / CW];
     bf16x8 xf[CW == 32 ? 4 : 2];
-    if (live) {
+    {
       const int lc = anew(lane % CW), k8 = anew(8 * (lane / CW));   // an operand's row or column, and its first k
       if constexpr (!kAgg) {
 #pragma unroll
@@ -401,7 +417,6 @@ __global__ __launch_bounds__(kThreads, per_cu(A, CW)) void linear_attention_kern
     if constexpr (kLate) load_next();
     if constexpr (!kAgg) {
       lds_barrier();   // P
-      if (!live) continue;   // (and store nothing)
       const int lc = anew(lane % CW), k8 = anew(8 * (lane / CW));
       // A NaN or infinity in a token's v makes all of its column's state non-finite, so one state per column tells of
       // it.  It would meet P's zeros in front of the token: it is taken out of V and put back below.
