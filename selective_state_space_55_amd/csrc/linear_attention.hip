@@ -109,9 +109,9 @@ constexpr int kWaves = 4, kThreads = 64 * kWaves;
 template <int A, int CW, bool kAgg>
 struct Lds {
   // pitches that spread the rows of one read over the banks
-  static constexpr int kRowQ = CW == 32 ? A + 8 : A + 16, kRowK = A + 16, kRowV = kWaves * CW + 16, kRowP = kQ + 8;
+  static constexpr int kRowQ = CW == 32 ? A + 8 : A + 16, kRowK = A + 16, kRowV = kWaves * CW + 16, kRowP = kQ + 8, kRowD = CW + 4;
   static constexpr int kQs = kAgg ? 0 : kQ * kRowQ, kKs = kQ * kRowK, kVs = kQ * kRowV, kPs = kAgg ? 0 : 2 * kQ * kRowP;
-  static constexpr size_t bytes() { return 2 * (size_t)(kQs + kKs + kVs + kPs) + 4 * (2 * kQ + (kAgg ? 0 : 256)); }
+  static constexpr size_t bytes() { return 2 * (size_t)(kQs + kKs + kVs + kPs) + 4 * (2 * kQ + (kAgg ? 0 : CW * kRowD)); }
 };
 
 __device__ __forceinline__ int64_t part_of(int64_t b, int64_t s) { return b + min(b, s); }
@@ -139,7 +139,7 @@ __global__ __launch_bounds__(kThreads, per_cu(A, CW)) void linear_attention_kern
   uint16_t* Ps = Vs + L::kVs;                            // the decayed scores, token i's row: bf16 hi, and kQ rows on the rest
   float* into = reinterpret_cast<float*>(Ps + L::kPs);   // lam^(what follows in the chunk), by token
   float* back = into + kQ;                               // scale lam^(48 - y) by y
-  float* diag = back + kQ;                               // scale lam^(i - j) by 16 i + j
+  float* diag = back + kQ;                               // scale lam^(i - j) of a diagonal tile, row i
   lds_poison(sm, (int)L::bytes());
 
   // eight units at a time, each unit's workgroups on one XCD
@@ -197,8 +197,6 @@ __global__ __launch_bounds__(kThreads, per_cu(A, CW)) void linear_attention_kern
   // behind the end, or in front of the start at an unsigned offset past it, load as 0.
   constexpr int kCpr = A / 8, kRpp = kThreads / kCpr, kR = kQ / kRpp;   // q, k: 16-byte pieces per row, rows per pass
   constexpr int kVpr = kWaves * CW / 8, kVr = kQ * kVpr / kThreads;     // v
-  // The next chunk's loads go out at a chunk's start where they fit the registers beside the rest, else behind the state's update
-  constexpr bool kLate = !kAgg && 2 * kR + kVr > 12;
   const int kr = tid / kCpr, kc = (tid % kCpr) * 8;
   const int vr = tid / kVpr, vc = (tid % kVpr) * 8;
   const int out_of = later ? -16 : kOut;   // stays past the end (2^31 - 32 bytes at most) with a chunk's rows added
@@ -219,9 +217,18 @@ __global__ __launch_bounds__(kThreads, per_cu(A, CW)) void linear_attention_kern
       off += step;
     }
   };
-  auto load = [&](int n) {
+  auto load_k = [&](int n, int64_t ahead) {
+    kp += ahead * R.k_stride;
     load_rows(kp, R.k_stride, A_, n, kr, kc, kRpp, kq);
-    if constexpr (!kAgg) load_rows(qp, R.q_stride, A_, n, kr, kc, kRpp, qq);
+  };
+  auto load_q = [&](int n, int64_t ahead) {
+    if constexpr (!kAgg) {
+      qp += ahead * R.q_stride;
+      load_rows(qp, R.q_stride, A_, n, kr, kc, kRpp, qq);
+    }
+  };
+  auto load_v = [&](int n, int64_t ahead) {
+    vp += ahead * R.v_stride;
     load_rows(vp, R.v_stride, cols, n, vr, vc, kQ / kVr, vq);
   };
   auto store_tiles = [&]() {
@@ -234,7 +241,12 @@ __global__ __launch_bounds__(kThreads, per_cu(A, CW)) void linear_attention_kern
     for (int r = 0; r < kVr; ++r) *reinterpret_cast<uint4*>(Vs + (vr + r * (kQ / kVr)) * L::kRowV + vc) = vq[r];
   };
 
-  if (nchunk > 0) load(nchunk == 1 ? rest : kQ);
+  if (nchunk > 0) {
+    const int n = nchunk == 1 ? rest : kQ;
+    load_k(n, 0);
+    load_q(n, 0);
+    load_v(n, 0);
+  }
 
   // The state: f32x16 tiles of 32 rows x 32 columns, registers 8 s + r row 16 s + 8 (lane / 32) + r of column turn(lane % 32);
   // or pairs of f32x4 tiles of 32 rows x 16 columns, register 4 t + r row 8 (lane / 16) + 4 t + r of column lane % 16.
@@ -278,8 +290,8 @@ __global__ __launch_bounds__(kThreads, per_cu(A, CW)) void linear_attention_kern
 
   float li = 0.0f, out[64 / CW];
   if constexpr (!kAgg) {
-    for (int x = tid; x < 256; x += kThreads) diag[x] = a.scale * power(l2, (float)max((x >> 4) - (x & 15), 0));
-    li = power(l2, (float)(lane & 15));
+    for (int x = tid; x < CW * CW; x += kThreads) diag[x / CW * L::kRowD + x % CW] = a.scale * power(l2, (float)max(x / CW - x % CW, 0));
+    li = power(l2, (float)(lane % CW));
 #pragma unroll
     for (int i = 0; i < 64 / CW; ++i) out[i] = R.c_out * power(l2, (float)(CW * i + lane % CW) + e);
     if (tid < kQ) back[tid] = a.scale * power(l2, (float)max(48 - tid, 0));
@@ -314,41 +326,8 @@ __global__ __launch_bounds__(kThreads, per_cu(A, CW)) void linear_attention_kern
     lds_barrier();
     const int next = c + 2 >= nchunk ? rest : kQ;   // tokens of the next chunk, and how far it is
     const int64_t ahead = later ? -next : kQ;
-    auto load_next = [&]() {
-      if (c + 1 == nchunk) return;
-      kp += ahead * R.k_stride;
-      vp += ahead * R.v_stride;
-      if constexpr (!kAgg) qp += ahead * R.q_stride;
-      load(next);
-    };
-    if constexpr (!kLate) load_next();
-    if constexpr (!kAgg) {
-      // P^T in 16 x 16 tiles (token blocks i, j <= i), three to a wave: ten, and the two behind their tokens that the
-      // products below meet, which come out as zeros
-      const int l16 = anew(lane & 15), h16 = anew(lane >> 4);
-#pragma unroll
-      for (int u = 0; u < 3; ++u) {
-        const int x = u * kWaves + w;
-        const int i = (int)(0x203333222110ull >> (4 * x)) & 15, j = (int)(0x313210210100ull >> (4 * x)) & 15;
-        f32x4 m = {};
-#pragma unroll
-        for (int ks = 0; ks < NB; ++ks)
-          m = product(lds_b8(Ks + (16 * j + l16) * L::kRowK + 32 * ks + 8 * h16),
-                      lds_b8(Qs + (16 * i + l16) * L::kRowQ + 32 * ks + 8 * h16), m);
-        // (no branch here: what a branch skips must not count as the wait for the products)
-        const float4 wt = *reinterpret_cast<const float4*>(i <= j ? diag + 16 * l16 + 4 * h16 : back + 48 - 16 * (i - j) + 4 * h16);
-        const float wa[4] = {wt.x, wt.y, wt.z, wt.w}, of = i == j ? 1.0f : li;
-        const int last = l16 - 4 * h16 + 16 * (i - j);   // the last register that is not behind the token
-        float f[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) f[r] = r <= last ? m[r] * (wa[r] * of) : 0.0f;
-        uint16_t* p = Ps + (16 * i + l16) * L::kRowP + 16 * j + 4 * h16;
-        *reinterpret_cast<uint2*>(p) = make_uint2(hi16x2(f[0], f[1]), hi16x2(f[2], f[3]));
-        *reinterpret_cast<uint2*>(p + kQ * L::kRowP) = make_uint2(pack_bf16x2(f[0] - trunc16(f[0]), f[1] - trunc16(f[1])),
-                                                                  pack_bf16x2(f[2] - trunc16(f[2]), f[3] - trunc16(f[3])));
-      }
-    }
-
+    const bool more = c + 1 < nchunk;
+    if (more) load_k(next, ahead);   // the others follow, so that no wave stands in line for its loads
     const double exactly = (n == kQ ? whole : part_chunk) * (1.0 + off);
     const float fade = (float)exactly;
     off = carry ? (exactly - (double)fade) * per_whole : 0.0;
@@ -357,6 +336,12 @@ __global__ __launch_bounds__(kThreads, per_cu(A, CW)) void linear_attention_kern
     {
       const int lc = anew(lane % CW), k8 = anew(8 * (lane / CW));   // an operand's row or column, and its first k
       if constexpr (!kAgg) {
+        // S^T Q^T, and the scores, which take the same operands of Q.  A wave's scores: the 32 x 32 tile of token half `pi`
+        // by half `pj`, or the 16 x 16 tiles of all tokens by token block w; with the tiles behind their tokens, which
+        // come out as zeros, as many for each wave.
+        const int pi = CW == 32 ? (0x6 >> w) & 1 : 0, pj = CW == 32 ? w >> 1 : w;
+        const uint16_t* const krow = Ks + (CW == 32 ? 32 * pj + turn(lc) : 16 * pj + lc) * L::kRowK + k8;
+        Tile score[CW == 32 ? 1 : 4];
 #pragma unroll
         for (int o = 0; o < kOct; ++o) {
           uint32_t hi[4], lo[4];
@@ -367,14 +352,55 @@ __global__ __launch_bounds__(kThreads, per_cu(A, CW)) void linear_attention_kern
             lo[j] = pack_bf16x2(v0 - trunc16(v0), v1 - trunc16(v1));
           }
           const bf16x8 sh = words(hi[0], hi[1], hi[2], hi[3]), sl = words(lo[0], lo[1], lo[2], lo[3]);
+          const bf16x8 kf = lds_b8(krow + kStep * o);
           bf16x8 q[64 / CW];
 #pragma unroll
           for (int i = 0; i < 64 / CW; ++i) q[i] = lds_b8(Qs + (CW * i + lc) * L::kRowQ + kStep * o + k8);
 #pragma unroll
           for (int i = 0; i < 64 / CW; ++i) y[i] = product(sl, q[i], o ? y[i] : Tile{});
+          if constexpr (CW == 32) {
+            score[0] = product(kf, pi ? q[1] : q[0], o ? score[0] : Tile{});
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) score[i] = product(kf, q[i], o ? score[i] : Tile{});
+          }
 #pragma unroll
           for (int i = 0; i < 64 / CW; ++i) y[i] = product(sh, q[i], y[i]);
         }
+        // decayed, in two bf16 parts.  (No branch here: what a branch skips must not count as the wait for the products.)
+#pragma unroll
+        for (int x = 0; x < (CW == 32 ? 2 : 4); ++x) {
+          const int i = CW == 32 ? pi : x, apart = i - pj, j0 = CW == 32 ? 16 * x + k8 : k8 / 2;   // the lane's first j
+          const int last = lc + CW * apart - j0;   // the last register that is not behind the token
+          const float* const wt = apart <= 0 ? diag + L::kRowD * lc + j0 : back + 48 - CW * apart + j0;
+          const float of = apart <= 0 ? 1.0f : li;
+          float f[CW == 32 ? 8 : 4];
+#pragma unroll
+          for (int r = 0; r < (CW == 32 ? 8 : 4); r += 4) {
+            const float4 w4 = *reinterpret_cast<const float4*>(wt + r);
+            const float wa[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {   // (bits, not a product: what is behind a token may be a NaN)
+              const float m = CW == 32 ? score[0][8 * x + r + u] : score[x][r + u];
+              f[r + u] = __uint_as_float(__float_as_uint(m * (wa[u] * of)) & (uint32_t)((r + u - 1 - last) >> 31));
+            }
+          }
+          uint16_t* const p = Ps + (CW * i + lc) * L::kRowP + CW * pj + j0;
+          uint32_t ph[CW / 8], pl[CW / 8];
+#pragma unroll
+          for (int u = 0; u < CW / 8; ++u) {
+            ph[u] = hi16x2(f[2 * u], f[2 * u + 1]);
+            pl[u] = pack_bf16x2(f[2 * u] - trunc16(f[2 * u]), f[2 * u + 1] - trunc16(f[2 * u + 1]));
+          }
+          if constexpr (CW == 32) {
+            *reinterpret_cast<uint4*>(p) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+            *reinterpret_cast<uint4*>(p + kQ * L::kRowP) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+          } else {
+            *reinterpret_cast<uint2*>(p) = make_uint2(ph[0], ph[1]);
+            *reinterpret_cast<uint2*>(p + kQ * L::kRowP) = make_uint2(pl[0], pl[1]);
+          }
+        }
+        if (more) load_q(next, ahead);
       }
 #pragma unroll
       for (auto& tile : S)
@@ -414,7 +440,12 @@ __global__ __launch_bounds__(kThreads, per_cu(A, CW)) void linear_attention_kern
         }
       }
     }
-    if constexpr (kLate) load_next();
+    // The products' last results are there before any branch: the compiler counts instructions that a branch may skip among
+    // those that it waits with (seen in its output; the assembly is tested for it).
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 15");
+    __builtin_amdgcn_sched_barrier(0);
+    if (more) load_v(next, ahead);
     if constexpr (!kAgg) {
       lds_barrier();   // P
       const int lc = anew(lane % CW), k8 = anew(8 * (lane / CW));
