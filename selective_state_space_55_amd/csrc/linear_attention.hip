@@ -570,7 +570,8 @@ __global__ __launch_bounds__(256) void linear_attention_fold_kernel(LaArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int64_t k = later ? n - 1 - (i0 + i) : i0 + i;
-      own[i] = i0 + i + 1 < n ? ws[k * step] : f;
+      own[i] = make_float4(0.f, 0.f, 0.f, 0.f);   // the last one in this order has none
+      if (i0 + i + 1 < n) own[i] = ws[k * step];
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -643,28 +644,38 @@ void set_shape(Role& R, int64_t A, int64_t B, bool transposed, int64_t K) {
 
 }  // namespace
 
+// A workgroup that has its CU to itself takes 4.0 us for a chunk of 128 x 128, two on a CU 3.8 us each chunk; a first pass
+// over a piece costs about half of its main pass, and a piece's states as much traffic as four chunks.  So sequences
+// are cut only where they leave CUs idle for long enough: 2048 tokens of 32, 64 and 128 workgroups take 129, 127
+// and 132 us whole and 60, 86 and 135 cut; 8192 tokens of 64 (heads of 64) 279 and 98; gradients of 2048 and 8192 tokens of 192
+// workgroups 124 and 272 us whole, 147 and 195 cut; 509 tokens of 12 workgroups 22 and 28.  Pieces are as long as about 512
+// workgroups share out, a power of two (so that a piece number needs no division), and four chunks at least (2048 tokens of 32
+// workgroups in pieces of 256: 58 us, of 128: 66, of 64: 90).
+// Where packed sequences fill the GPU by themselves, only those over four such pieces are cut (28 of 32768 tokens, 32
+// workgroups each: 422 us with those over one piece cut 530).
 LinearAttentionPlan make_linear_attention_plan(int64_t nseq, int64_t total, int64_t nheads, int64_t kdim, int64_t vdim,
                                                bool packed, int64_t longest, bool backward) {
   LinearAttentionPlan p{};
   const int64_t wgs = nheads * (backward ? 2 * slabs_of(kdim) + slabs_of(vdim) : slabs_of(vdim));
   p.wgs = wgs;
-  p.shift = 6;
-  while ((int64_t)2 << p.shift <= total / 1024 * wgs + total % 1024 * wgs / 1024) ++p.shift;
-  const bool fills = nseq >= (512 + wgs - 1) / wgs;
+  p.shift = 8;
+  while ((int64_t)2 << p.shift <= total / 512 * wgs + total % 512 * wgs / 512) ++p.shift;
+  if (!packed) longest = total / nseq;
+  else if (longest <= 0 || longest > total) longest = total;
+  const bool fills = nseq >= (256 + wgs - 1) / wgs;
+  const bool idle = !fills && (longest + kQ - 1) / kQ >= (4096 + 255 - nseq * wgs) / (256 - nseq * wgs);
   if (!packed) {
-    const int64_t len = total / nseq;
-    p.np = fills || len <= (int64_t)1 << p.shift ? 1 : (len + ((int64_t)1 << p.shift) - 1) >> p.shift;
-    p.cut = p.np > 1;
+    p.cut = idle && longest > (int64_t)1 << p.shift;
+    p.np = p.cut ? (longest + ((int64_t)1 << p.shift) - 1) >> p.shift : 1;
     p.whole = p.shift;
     p.pieces = nseq * p.np;
     p.full = nseq * (p.np - 1);
     p.folds = nseq;
     p.parts = p.cut ? nseq * p.np : 0;
   } else {
-    if (longest <= 0 || longest > total) longest = total;
-    p.cut = longest > (int64_t)1 << (fills ? p.shift + 2 : p.shift);
-    p.whole = fills && (int64_t)2 << p.shift <= total / nseq ? p.shift + 2 : p.shift;
-    if (!p.cut) p.shift = p.whole = 62;
+    p.whole = fills ? p.shift + 2 : p.shift;
+    p.cut = (fills || idle) && longest > (int64_t)1 << p.whole;
+    if (!p.cut) p.shift = p.whole = 62;   // every sequence is one piece, however long it is
     p.np = 1;
     p.pieces = (total >> p.shift) + nseq;
     p.full = total >> p.shift;

@@ -695,3 +695,140 @@ def test_binding_refusals():
         with pytest.raises((ValueError, TypeError, mscan.MambaScanError)):
             call()
             say(f"refusal {i} was taken")
+
+
+# ---------------------------------------------------------------- sequences that are cut into pieces
+
+# one or few heads leave CUs idle, so that sequences over a piece (256 tokens and more) are cut; the first of `lens` is the longest
+CUT = [([1300], 1, 64, 64), ([1601, 0, 70, 257, 256, 513], 1, 32, 128), ([2047, 511], 2, 128, 64), ([1100, 1024], 1, 256, 40),
+       ([1537, 1, 255], 3, 48, 200)]
+
+
+@pytest.mark.parametrize("lens,H,K,V", CUT)
+def test_cut_packed(lens, H, K, V):
+    r = Rng(sum(lens) + K)
+    n, first = len(lens), 5
+    cu = offsets(lens, first)
+    total = cu[-1] + 70
+    assert mscan.linear_attention_workspace_size(n, total, H, K, V, packed=True) > 0
+    assert mscan.linear_attention_workspace_size(n, total, H, K, V, packed=True, backward=True) > 0
+    q, k, v, do = (r(total, H, d, dtype=BF16) for d in (K, K, V, V))
+    for t in (q, k, v, do):
+        t[:first] = t[cu[-1]:] = float("nan")
+    ld = decays(H, -6, -10)   # what a piece leaves reaches the pieces behind it
+    slots = torch.randperm(n + 2, generator=r.g)[:n]
+    pos = i64([3 if s % 2 == 0 else 0 for s in range(n)])
+    pool, scale = r(n + 2, H, V, K), K ** -0.5
+    say(f"cut {lens} H {H} K {K} V {V}")
+    o64, s64 = la.forward(q, k, v, ld, cu, pool, slots, pos, scale)
+    oa, sa = la.forward(q, k, v, ld, cu, pool, slots, pos, scale, sums=True)
+    st, out = dev(pool.clone()), torch.full((total, H, V), 7.0, dtype=BF16, device=DEV)
+    args = (apart(q, 8), apart(k, 0), apart(v, 16), dev(ld), dev(i64(cu)))
+    mscan.linear_attention_fwd_varlen(*args, st, dev(slots), dev(pos), out=out)
+    close("o", out, o64, HALF[BF16] * o64.abs() + SPLIT * oa)
+    close("state", st, s64, STATE * sa)
+    assert (out[:first] == 7).all() and (out[cu[-1]:] == 7).all()
+    # a slot outside the pool starts from zeros and keeps nothing
+    out2 = mscan.linear_attention_fwd_varlen(*args, st, dev(torch.full_like(slots, -1)), dev(pos))
+    o64, _ = la.forward(q, k, v, ld, cu, scale=scale)
+    oa, _ = la.forward(q, k, v, ld, cu, scale=scale, sums=True)
+    close("o from zeros", out2, o64, HALF[BF16] * o64.abs() + SPLIT * oa)
+    h0, dh = r(n, H, V, K), r(n, H, V, K)
+    for carried in (True, False):
+        a, b = (h0, dh) if carried else (None, None)
+        want = la.backward(do, q, k, v, ld, cu, a, b, scale)
+        sums = la.backward(do, q, k, v, ld, cu, a, b, scale, sums=True)
+        g = mscan.linear_attention_bwd(apart(do, 24), *args[:4], dev(a), dev(b), cu_seqlens=args[4])
+        for name, w, s in zip(("dq", "dk", "dv"), want, sums):
+            close(name, g[name], w, HALF[BF16] * w.abs() + SPLIT * s)
+        if carried:
+            close("d state", g["d_initial_state"], want[3], STATE * sums[3])
+
+
+@pytest.mark.parametrize("B,L,H,K,V", [(1, 1300, 1, 64, 96), (2, 1088, 1, 128, 128), (3, 1153, 2, 16, 256), (1, 1025, 4, 256, 16)])
+def test_cut_batch(B, L, H, K, V):
+    r = Rng(L + H)
+    q, k, v, do = (r(B, L, H, d, dtype=BF16) for d in (K, K, V, V))
+    ld, h0, dh = decays(H, -5, -10), r(B, H, V, K), r(B, H, V, K)
+    assert mscan.linear_attention_workspace_size(B, B * L, H, K, V) > 0
+    cu, flat = offsets([L] * B), [t.flatten(0, 1) for t in (do, q, k, v)]
+    say(f"cut batch {B} x {L} H {H} K {K} V {V}")
+    o64, s64 = la.forward(*flat[1:], ld, cu, h0, scale=K ** -0.5)
+    oa, sa = la.forward(*flat[1:], ld, cu, h0, scale=K ** -0.5, sums=True)
+    o, s = mscan.linear_attention_fwd(*dev(q, k, v, ld, h0), return_final_state=True)
+    close("o", o.flatten(0, 1), o64, HALF[BF16] * o64.abs() + SPLIT * oa)
+    close("state", s, s64, STATE * sa)
+    pool = dev(h0.clone())   # in place
+    mscan.linear_attention_fwd(*dev(q, k, v, ld), pool, final_state=pool, return_final_state=True)
+    assert same_bits(pool, s)
+    want = la.backward(*flat, ld, cu, h0, dh, K ** -0.5)
+    sums = la.backward(*flat, ld, cu, h0, dh, K ** -0.5, sums=True)
+    g = mscan.linear_attention_bwd(*dev(do, q, k, v, ld, h0, dh))
+    for name, w, a in zip(("dq", "dk", "dv"), want, sums):
+        close(name, g[name].flatten(0, 1), w, HALF[BF16] * w.abs() + SPLIT * a)
+    close("d state", g["d_initial_state"], want[3], STATE * sums[3])
+    again = mscan.linear_attention_bwd(*dev(do, q, k, v, ld, h0, dh))
+    assert all(same_bits(again[name], g[name]) for name in g)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("what", ["q", "k", "v"])
+def test_cut_a_bad_token_reaches_no_earlier_one(what, bad):
+    K, V, L, t0 = 16, 24, 1300, 600
+    r = Rng(8)
+    q, k, v = r(1, L, 2, K, dtype=BF16), r(1, L, 2, K, dtype=BF16), r(1, L, 2, V, dtype=BF16)
+    ld = decays(2, -7, -9)
+    assert mscan.linear_attention_workspace_size(1, L, 2, K, V) > 0
+    clean = mscan.linear_attention_fwd(*dev(q, k, v, ld)).cpu()
+    {"q": q, "k": k, "v": v}[what][0, t0, 0, 3] = bad
+    o, s = mscan.linear_attention_fwd(*dev(q, k, v, ld), return_final_state=True)
+    o = o.cpu()
+    assert torch.equal(o[0, :t0], clean[0, :t0]) and torch.equal(o[0, :, 1], clean[0, :, 1])
+    if what == "q":
+        assert not torch.isfinite(o[0, t0, 0]).any() and torch.equal(o[0, t0 + 1:], clean[0, t0 + 1:]) and torch.isfinite(s).all()
+    elif what == "k":
+        assert not torch.isfinite(o[0, t0:, 0]).any() and not torch.isfinite(s[0, 0, :, 3]).any()
+    else:
+        assert not torch.isfinite(o[0, t0:, 0, 3]).any() and not torch.isfinite(s[0, 0, 3]).any()
+
+
+@pytest.mark.parametrize("log_decay", [0.0, -1e-6, -0.01, -0.3, -40.0, -1e38, float("-inf"), 1e-4])
+def test_cut_decays_of_any_size(log_decay):
+    K, V, L = 16, 32, 1200
+    r = Rng(13)
+    q, k, v, do = (r(1, L, 1, d, dtype=BF16) for d in (K, K, V, V))
+    ld, h0, dh = torch.full((1,), log_decay), r(1, 1, V, K), r(1, 1, V, K)
+    assert mscan.linear_attention_workspace_size(1, L, 1, K, V) > 0
+    cu, flat, tiny = [0, L], [t[0] for t in (do, q, k, v)], 2.0 ** -120
+    o64, s64 = la.forward(*flat[1:], ld, cu, h0, scale=0.5)
+    oa, sa = la.forward(*flat[1:], ld, cu, h0, scale=0.5, sums=True)
+    o, s = mscan.linear_attention_fwd(*dev(q, k, v, ld, h0), return_final_state=True, scale=0.5)
+    close("o", o[0], o64, HALF[BF16] * o64.abs() + SPLIT * oa + tiny)
+    close("state", s, s64, STATE * sa + tiny)
+    want = la.backward(*flat, ld, cu, h0, dh, 0.5)
+    sums = la.backward(*flat, ld, cu, h0, dh, 0.5, sums=True)
+    g = mscan.linear_attention_bwd(*dev(do, q, k, v, ld, h0, dh), scale=0.5)
+    for name, w, a in zip(("dq", "dk", "dv"), want, sums):
+        close(name, g[name][0], w, HALF[BF16] * w.abs() + SPLIT * a + tiny)
+    close("d state", g["d_initial_state"], want[3], STATE * sums[3] + tiny)
+
+
+@pytest.mark.parametrize("cu", [[5, 1900, 3, 2000], [-100, 1 << 40, 1 << 62, 20], [2000, 1200, 600, 0], [0, 2000, 0, 2000]])
+def test_cut_bad_offsets_stay_in_bounds(cu):
+    H, K, V, total, pad = 1, 64, 64, 2000, 600
+    r = Rng(6)
+    q, k, v, do = (r(total + 2 * pad, H, K, dtype=BF16).to(DEV)[pad:pad + total] for _ in range(4))
+    need = mscan.linear_attention_workspace_size(3, total, H, K, V, packed=True, backward=True)
+    assert need > 0
+    ws = torch.full((need + 512 + (1 << 20),), 77, dtype=torch.uint8, device=DEV)
+    ws = ws[(-ws.data_ptr()) % 256:]
+    pool = torch.zeros(5, H, V, K, device=DEV)
+    out = torch.full((total + 2 * pad, H, V), 3.0, dtype=BF16, device=DEV)
+    say(f"offsets {cu}")
+    ld, cud = dev(decays(H)), dev(i64(cu))
+    mscan.linear_attention_fwd_varlen(q, k, v, ld, cud, pool[1:4], dev(i64([0, 1, 2])), dev(i64([1, 1, 1])), out=out[pad:pad + total],
+                                      workspace=ws)
+    mscan.linear_attention_bwd(do, q, k, v, ld, cu_seqlens=cud, workspace=ws)
+    torch.cuda.synchronize()
+    assert (out[:pad] == 3).all() and (out[-pad:] == 3).all() and (pool[0] == 0).all() and (pool[4] == 0).all()
+    assert (ws[need:] == 77).all()
