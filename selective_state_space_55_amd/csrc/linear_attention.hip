@@ -635,18 +635,30 @@ hipError_t launch_for(int pad, int columns, const LaArgs& a, hipStream_t s) {
   return a.exact ? launch_pad<32, kAgg, 3>(pad, a, s) : launch_pad<32, kAgg, 2>(pad, a, s);
 }
 
-// the roles of `of` (a bit each) that one kernel can take, in one launch; returns what is left
+// The roles of `of` (a bit each) that one kernel can take, in one launch; returns what is left.  A gradient whose workgroups
+// have a CU each takes the widest kernel for all: 6 heads of 64 x 96, 6 and 12 sequences of 217 tokens 24 and 24 us, in
+// two launches 31 and 32, but 36 of them 43 and 39; 12 of 512 tokens and 256 x 64 118 and 77.
 template <bool kAgg>
 unsigned launch_some(const LaArgs& all, unsigned of, hipStream_t s, hipError_t* e) {
   LaArgs a = all;
   a.nroles = a.wgs = 0;
-  int pad = 0, columns = 0;
+  int pad = 0, columns = 0, wgs = 0;
   for (int r = 0; r < 3; ++r) {
     if (!(of >> r & 1)) continue;
     const Role& R = all.role[r];
-    if (a.nroles && (pad_of(R.A) != pad || columns_of(R.B) != columns)) continue;
-    pad = pad_of(R.A);
-    columns = columns_of(R.B);
+    wgs += R.slabs;
+    pad = std::max(pad, pad_of(R.A));
+    columns = std::max(columns, columns_of(R.B));
+  }
+  const bool one = a.units * wgs <= 256;
+  for (int r = 0; r < 3; ++r) {
+    if (!(of >> r & 1)) continue;
+    const Role& R = all.role[r];
+    if (!one && a.nroles == 0) {
+      pad = pad_of(R.A);
+      columns = columns_of(R.B);
+    }
+    if (!one && (pad_of(R.A) != pad || columns_of(R.B) != columns)) continue;
     a.first[a.nroles] = a.wgs;
     a.role[a.nroles++] = R;
     a.wgs += R.slabs;
