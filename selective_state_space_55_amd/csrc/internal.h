@@ -282,8 +282,8 @@ hipError_t launch_ssd_varlen(const SsdVarlenArgs& a, const SsdVarlenPlan& p, hip
 // Linear attention with a fixed decay per head over packed or equal sequences, and its gradient
 // (linear_attention.hip), bf16 io.
 struct LinearAttentionPlan {
-  int shift;           // pieces of 2^shift tokens, at least 64
-  int whole;           // packed: a sequence of at most 2^whole tokens is one piece
+  int64_t piece;       // chunks of a piece
+  int64_t whole;       // packed: a sequence of at most so many chunks is one piece
   bool cut;            // a sequence may have more than one piece: two more passes and a workspace
   int64_t np;          // equal sequences: pieces of each
   int64_t pieces;      // piece numbers (of packed sequences some name no piece)

@@ -21,6 +21,7 @@
 #include "packed.h"
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 namespace mscan {
@@ -56,7 +57,7 @@ struct LaArgs {
   int nroles;
   int64_t len, units;
   int np;              // equal sequences: pieces of each
-  int shift, whole;    // pieces of 2^shift tokens; packed sequences of at most 2^whole are not cut
+  Chunks piece, whole; // a piece; packed sequences of at most `whole` are not cut
   int H, KV;
   int exact;           // a state leaves the call, or may: v goes into it in three parts, else in two
   float scale;
@@ -116,12 +117,6 @@ struct Lds {
 
 __device__ __forceinline__ int64_t part_of(int64_t b, int64_t s) { return b + min(b, s); }
 
-// A sequence's piece: its tokens, its part of the workspace, and whether it is alone
-struct Piece {
-  int64_t s, first, end, part;
-  int64_t k, n;   // number, and pieces of the sequence
-};
-
 // Workgroups that the tiles leave room for on a CU (160 KB of LDS), which is waves on a SIMD
 constexpr int per_cu(int A, int CW) { return A == 256 ? 1 : A == 64 && CW == 16 ? 3 : 2; }
 
@@ -179,13 +174,13 @@ __global__ __launch_bounds__(kThreads, per_cu(A, CW)) void linear_attention_kern
       s = by_length(a.seq, number);
       start = seq_offset(a.seq, s); stop = max(start, seq_offset(a.seq, s + 1)); k = 0;
     } else {
-      const Run run = find_run<true>(a.seq, kAgg ? number : number - a.seq.nseq, a.shift);
+      const Run run = find_run<true>(a.seq, kAgg ? number : number - a.seq.nseq, a.piece);
       if (run.s < 0) return;
       s = run.s; start = run.start; stop = run.stop; k = run.k + (kAgg ? 0 : 1);
     }
-    const bool cut = stop - start > (int64_t)1 << a.whole;
+    const bool cut = stop - start > a.whole.tokens(1);
     if (!cut && (kAgg || k > 0)) return;
-    np = cut ? (stop - start + ((int64_t)1 << a.shift) - 1) >> a.shift : 1;
+    np = cut ? a.piece.runs(stop - start - 1) + 1 : 1;
     if (k >= np) return;
   } else {
     const int64_t per = kAgg ? a.np - 1 : a.np;
@@ -194,9 +189,9 @@ __global__ __launch_bounds__(kThreads, per_cu(A, CW)) void linear_attention_kern
   }
   const bool later = R.later != 0;
   if (kAgg && later) ++k;   // a piece that others precede
-  const int64_t t_first = np == 1 ? start : start + (k << a.shift);
-  const int64_t t_end = np == 1 ? stop : min(stop, t_first + ((int64_t)1 << a.shift));
-  const int64_t part = (a.seq.cu ? part_of(start >> a.shift, s) : s * np) + k;
+  const int64_t t_first = np == 1 ? start : start + a.piece.tokens(k);
+  const int64_t t_end = np == 1 ? stop : min(stop, t_first + a.piece.tokens(1));
+  const int64_t part = (a.seq.cu ? part_of(a.piece.runs(start), s) : s * np) + k;
   const int nchunk = (int)((t_end - t_first + kQ - 1) / kQ);   // (an array of 2^31 chunks fits no memory)
   const int rest = (int)((t_end - t_first - 1) % kQ) + 1;     // tokens of the last one
   const int A_ = R.A, cols = min(R.slab, R.B - b0);
@@ -576,8 +571,8 @@ __global__ __launch_bounds__(256) void linear_attention_fold_kernel(LaArgs a) {
     s = blockIdx.y; start = s * a.len; stop = start + a.len;
   }
   if (e >= row_state) return;
-  const int64_t len = (int64_t)1 << a.shift, n = (stop - start + len - 1) >> a.shift;
-  const int64_t v0 = a.seq.cu ? part_of(start >> a.shift, s) : s * n;
+  const int64_t len = a.piece.tokens(1), n = a.piece.runs(stop - start - 1) + 1;
+  const int64_t v0 = a.seq.cu ? part_of(a.piece.runs(start), s) : s * n;
   const float ld = a.log_decay[e / a.KV], l2 = ld * 1.4426950408889634f;
   const int64_t entry = a.seq.slots ? seq_slot(a.seq, s) : s;
   float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -678,43 +673,66 @@ void set_shape(Role& R, int64_t A, int64_t B, bool transposed, int64_t K) {
 
 }  // namespace
 
-// A workgroup that has its CU to itself takes 4.0 us for a chunk of 128 x 128, two on a CU 3.8 us each chunk; a first pass
-// over a piece costs about half of its main pass, and a piece's states as much traffic as four chunks.  So sequences
-// are cut only where they leave CUs idle for long enough: 2048 tokens of 32, 64 and 128 workgroups take 129, 127
-// and 132 us whole and 60, 86 and 135 cut; 8192 tokens of 64 (heads of 64) 279 and 98; gradients of 2048 and 8192 tokens of 192
-// workgroups 124 and 272 us whole, 147 and 195 cut; 509 tokens of 12 workgroups 22 and 28.  Pieces are as long as about 512
-// workgroups share out, a power of two (so that a piece number needs no division), and four chunks at least (2048 tokens of 32
-// workgroups in pieces of 256: 58 us, of 128: 66, of 64: 90).
-// Where packed sequences fill the GPU by themselves, only those over four such pieces are cut (28 of 32768 tokens, 32
-// workgroups each: 422 us with those over one piece cut 530).
+// Sequences are cut only where they leave CUs idle for long enough.  Sequences that do not fill the GPU are cut into the pieces
+// that this model finds cheapest: a CU takes `chunk` us for each 64 tokens of a workgroup, two workgroups on it 0.85 of that
+// for each (of small heads: two together no more than one), the first pass half of the main one's time, the pieces' states
+// are moved at 4.9 TB/s, the fold takes 0.5 us a piece, and launching two more kernels 12 us.  Pieces are as long as one to
+// six workgroups a CU share out, and four chunks at least.  Measured, whole, and in pieces of 4, 8, 16 and 32 chunks:
+//   2048 tokens of 32 / 64 / 128 workgroups, heads of 128   128  51  67 109 / 125  74  73 114 / 129 137 120 128 (the last in 16)
+//   gradients of 2048 tokens of 96 / 192 workgroups         119  82  83 106 / 117 145 125 137
+//   8192 tokens of 16 / 64 workgroups, heads of 64          273  42  44  68 118 / 276 109 102  92 126
+//   509 tokens of 12 workgroups                              22  29
+//   20000 tokens of 32 workgroups, 128 x 256               1193 303 (in 5) 275  272  301, in 20: 242
+// Several packed sequences, whose lengths only the device knows, are not cut unless one of the length that the caller bounds
+// them by leaves 4096 chunks' time idle (6 of 21 chunks in all, 18 workgroups each: 31 us, cut 40).  Where they fill the GPU
+// by themselves, only those over four pieces of a 512th of the work are cut (28 of 32768 tokens, 32 workgroups each: 422 us, with
+// those over one piece cut 530).
 LinearAttentionPlan make_linear_attention_plan(int64_t nseq, int64_t total, int64_t nheads, int64_t kdim, int64_t vdim,
                                                bool packed, int64_t longest, bool backward) {
   LinearAttentionPlan p{};
   const int64_t wgs = nheads * (backward ? 2 * slabs_of(kdim) + slabs_of(vdim) : slabs_of(vdim));
   p.wgs = wgs;
-  p.shift = 8;
-  while ((int64_t)2 << p.shift <= total / 512 * wgs + total % 512 * wgs / 512) ++p.shift;
   if (!packed) longest = total / nseq;
   else if (longest <= 0 || longest > total) longest = total;
+  const int64_t most = INT32_MAX, chunks = std::min((longest + kQ - 1) / kQ, most), all = std::min((total + kQ - 1) / kQ, most);
+  p.piece = p.whole = most;   // every sequence is one piece, however long it is
   const bool fills = nseq >= (256 + wgs - 1) / wgs;
-  const bool idle = !fills && (longest + kQ - 1) / kQ >= (4096 + 255 - nseq * wgs) / (256 - nseq * wgs);
+  if (!fills && (!packed || nseq == 1 || chunks >= (4096 + 255 - nseq * wgs) / (256 - nseq * wgs))) {
+    const bool small = kdim <= 64 && vdim <= 64;
+    const bool two = backward && (pad_of(kdim) != pad_of(vdim) || columns_of(kdim) != columns_of(vdim));   // launches
+    const double chunk = small ? 2.1 : std::max(kdim, vdim) <= 128 ? 3.9 : 7.0;
+    const int64_t slots = small ? 512 : 256, fwd = nheads * slabs_of(vdim), rest = wgs - fwd;
+    auto rounds = [&](double wgs) { return std::ceil(wgs / slots) * (small || wgs <= slots ? 1.0 : 0.85); };
+    double best = (double)chunks * chunk;
+    for (int r = 1; r <= 6; ++r) {
+      const int64_t want = slots * r / wgs - (packed ? nseq - 1 : 0);
+      if (want < 1) continue;
+      const int64_t m = std::max<int64_t>(4, ((packed ? all : chunks * nseq) + want - 1) / want);
+      if (m >= chunks) continue;
+      const double each = (double)((chunks + m - 1) / m), n = packed ? (double)((all + m - 1) / m + nseq - 1) : nseq * each;
+      const double us = chunk * m * ((two ? rounds(n * rest) + rounds(n * fwd) : rounds(n * wgs)) +
+                                     0.5 * rounds((n - nseq) * (backward ? 2 * fwd : fwd))) +
+                        n * nheads * kdim * vdim * (backward ? 24 : 12) / 4.9e6 + each / 2 + 12;
+      if (us < best) { best = us; p.piece = m; }
+    }
+    if (p.piece < most) p.whole = p.piece;
+  } else if (fills && packed) {
+    const double share = std::max(4.0, (double)all * wgs / 512);
+    if (4 * share < chunks) { p.piece = (int64_t)share; p.whole = 4 * p.piece; }
+  }
+  p.cut = p.piece < most;
+  p.np = 1;
   if (!packed) {
-    p.cut = idle && longest > (int64_t)1 << p.shift;
-    p.np = p.cut ? (longest + ((int64_t)1 << p.shift) - 1) >> p.shift : 1;
-    p.whole = p.shift;
+    if (p.cut) p.np = (chunks + p.piece - 1) / p.piece;
     p.pieces = nseq * p.np;
     p.full = nseq * (p.np - 1);
     p.folds = nseq;
     p.parts = p.cut ? nseq * p.np : 0;
   } else {
-    p.whole = fills ? p.shift + 2 : p.shift;
-    p.cut = (fills || idle) && longest > (int64_t)1 << p.whole;
-    if (!p.cut) p.shift = p.whole = 62;   // every sequence is one piece, however long it is
-    p.np = 1;
-    p.pieces = (total >> p.shift) + nseq;
-    p.full = total >> p.shift;
-    p.folds = total >> p.whole;
-    p.parts = p.cut ? (total >> p.shift) + std::min(nseq, total >> p.shift) : 0;
+    p.full = p.cut ? total / kQ / p.piece : 0;
+    p.pieces = p.full + nseq;
+    p.folds = p.cut ? total / kQ / p.whole : 0;
+    p.parts = p.cut ? p.full + std::min(nseq, p.full) : 0;
   }
   const size_t one = ((size_t)p.parts * nheads * kdim * vdim * 4 + 255) / 256 * 256;
   p.off_later = one;
@@ -728,7 +746,7 @@ hipError_t launch_linear_attention(const LinearAttentionArgs& p, const LinearAtt
   a.seq.nseq = p.nseq; a.seq.total = p.total; a.seq.nslots = p.nslots;
   a.log_decay = p.log_decay;
   a.len = p.total / p.nseq;
-  a.np = (int)plan.np; a.shift = plan.shift; a.whole = plan.whole;
+  a.np = (int)plan.np; a.piece.n = (uint32_t)plan.piece; a.whole.n = (uint32_t)plan.whole;
   a.H = (int)p.nheads; a.KV = (int)(p.kdim * p.vdim); a.scale = p.scale;
   a.exact = !p.backward || p.d_initial_state;
   const uint16_t *q = static_cast<const uint16_t*>(p.q), *k = static_cast<const uint16_t*>(p.k),

@@ -37,10 +37,10 @@ __device__ __forceinline__ int64_t lane64(int64_t v, int lane) {
   return (int64_t)(((uint64_t)hi << 32) | lo);
 }
 
-// A run of 2^shift tokens of a sequence (its last one may be shorter).  Runs are numbered so that a wave
-// finds the one of a number without a prefix sum over the lengths:
-//   every run   run k of sequence s is (cu[s] >> shift) + s + k, all below (total >> shift) + nseq
-//   full runs   that another one follows: (cu[s] >> shift) + k, all below total >> shift
+// A run of n tokens of a sequence (its last one may be shorter).  Runs are numbered so that a wave
+// finds the one of a number without a prefix sum over the lengths, a / b rounded down:
+//   every run   run k of sequence s is cu[s] / n + s + k, all below total / n + nseq
+//   full runs   that another one follows: cu[s] / n + k, all below total / n
 // The numbers of one sequence end before the next one's begin; some name no run.
 struct Run {
   int64_t s;            // sequence, -1: no run has this number
@@ -48,15 +48,26 @@ struct Run {
   int64_t k;            // the run's number in it
 };
 
-// The run that a uniform number would be if its sequence had it (run 0 of a sequence without tokens among them);
-// whole waves.  Looks at 64 offsets at a time.
-template <bool kFull>
-__device__ __forceinline__ Run locate_run(const Packed& p, int64_t number, int shift) {
+// Lengths of the runs: 2^shift tokens, or multiples of 64 tokens (of at most 2^37).
+struct Shift {
+  int shift;
+  __device__ __forceinline__ int64_t runs(int64_t tokens) const { return tokens >> shift; }
+  __device__ __forceinline__ int64_t tokens(int64_t runs) const { return runs << shift; }
+};
+struct Chunks {
+  uint32_t n;   // of 64 tokens; at least 1
+  __device__ __forceinline__ int64_t runs(int64_t tokens) const { return (uint32_t)(tokens >> 6) / n; }
+  __device__ __forceinline__ int64_t tokens(int64_t runs) const { return (runs * n) << 6; }
+};
+
+// The run of a uniform number; whole waves.  Looks at 64 offsets at a time.
+template <bool kFull, typename Length>
+__device__ __forceinline__ Run find_run(const Packed& p, int64_t number, Length length) {
   const int lane = threadIdx.x & 63;
   int64_t lo = 0, n = p.nseq;
   while (n > 63) {
     const int64_t step = (n + 62) / 63, i = lo + lane * step;
-    const bool in = lane * step < n && (seq_offset(p, i) >> shift) + (kFull ? 0 : i) <= number;
+    const bool in = lane * step < n && length.runs(seq_offset(p, i)) + (kFull ? 0 : i) <= number;
     const int c = __popcll(__ballot(in));
     if (c == 0) return Run{-1, 0, 0, 0};
     lo += (c - 1) * step;
@@ -64,23 +75,19 @@ __device__ __forceinline__ Run locate_run(const Packed& p, int64_t number, int s
   }
   // offsets lo .. lo + n, the last of them where the last sequence stops
   const int64_t v = seq_offset(p, lo + min((int64_t)lane, n));
-  const int c = __popcll(__ballot(lane < n && (v >> shift) + (kFull ? 0 : lo + lane) <= number));
+  const int c = __popcll(__ballot(lane < n && length.runs(v) + (kFull ? 0 : lo + lane) <= number));
   if (c == 0) return Run{-1, 0, 0, 0};
   Run r;
   r.s = lo + c - 1;
   r.start = lane64(v, c - 1);
   r.stop = lane64(v, c);
-  r.k = number - ((r.start >> shift) + (kFull ? 0 : r.s));
-  if (r.k < 0) r.s = -1;   // only where offsets fall
+  r.k = number - (length.runs(r.start) + (kFull ? 0 : r.s));
+  if (r.k < 0 || r.start + length.tokens(r.k + (kFull ? 1 : 0)) >= r.stop) r.s = -1;   // k < 0 only where offsets fall
   return r;
 }
-
-// The run of a uniform number; whole waves.
 template <bool kFull>
 __device__ __forceinline__ Run find_run(const Packed& p, int64_t number, int shift) {
-  Run r = locate_run<kFull>(p, number, shift);
-  if (r.start + ((r.k + (kFull ? 1 : 0)) << shift) >= r.stop) r.s = -1;
-  return r;
+  return find_run<kFull>(p, number, Shift{shift});
 }
 
 // the slot of sequence s, -1 if it has none
