@@ -1009,18 +1009,22 @@ def _sequences(name: str, t: torch.Tensor) -> torch.Tensor:
 
 def _span(t: torch.Tensor, stride: int) -> int:
     """Bytes from the first to behind the last element of a tensor of tokens."""
-    return 0 if t.numel() == 0 else ((t.shape[0] - 1) * stride + t[0].numel()) * t.element_size()
+    n, rows = t.numel(), t.shape[0]
+    return 0 if n == 0 else ((rows - 1) * stride + n // rows) * t.element_size()
 
 
 def _apart(out: Optional[torch.Tensor], others, same=()) -> None:
     """Refuses an output given by the caller that shares memory with an argument ((tensor, bytes) pairs), but for
     being one of `same` itself."""
-    if out is None or out.numel() == 0:
+    if out is None:
         return
-    at, end = out.data_ptr(), out.numel() * out.element_size()
+    at = out.data_ptr()
+    end = at + out.numel() * out.element_size()
     for t, size in others:
-        if t is not None and not any(t is s and at == s.data_ptr() for s in same) and _overlap(at, end, t.data_ptr(), size):
-            raise ValueError("an output overlaps another argument")
+        if t is not None and size > 0 and end > at:
+            b = t.data_ptr()
+            if b < end and at < b + size and not any(t is s and at == b for s in same):
+                raise ValueError("an output overlaps another argument")
 
 
 def _size_of(t: Optional[torch.Tensor]):
