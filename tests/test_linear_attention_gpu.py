@@ -258,6 +258,27 @@ def test_batch_gradient(B, L, H, K, V, carried):
     assert all(same_bits(again[name], g[name]) for name in g)
 
 
+@pytest.mark.parametrize("which", ["initial", "final"])
+@pytest.mark.parametrize("lens,H", [([70, 0, 200], 2), ([1400, 9], 1)])
+def test_gradient_with_one_state(lens, H, which):
+    """Of the state that a sequence starts from and the gradient of the one it ends with, only one is given."""
+    K, V = 32, 72
+    r = Rng(len(lens) + H)
+    n, cu = len(lens), offsets(lens)
+    q, k, v, do = (r(cu[-1], H, d, dtype=BF16) for d in (K, K, V, V))
+    ld, x = decays(H), r(n, H, V, K)
+    a, b = (x, None) if which == "initial" else (None, x)
+    say(f"gradient with the {which} state, {lens}")
+    want = la.backward(do, q, k, v, ld, cu, a, b, 0.5)
+    sums = la.backward(do, q, k, v, ld, cu, a, b, 0.5, sums=True)
+    g = mscan.linear_attention_bwd(*dev(do, q, k, v, ld, a, b), cu_seqlens=dev(i64(cu)), scale=0.5)
+    assert set(g) == {"dq", "dk", "dv"} | ({"d_initial_state"} if a is not None else set())
+    for name, w, s in zip(("dq", "dk", "dv"), want, sums):
+        close(name, g[name], w, HALF[BF16] * w.abs() + SPLIT * s)
+    if a is not None:
+        close("d state", g["d_initial_state"], want[3], STATE * sums[3])
+
+
 def test_gradient_against_differences():
     """The kernels' own gradient and forward: along a direction, (loss(x + e d) - loss(x - e d)) / 2 e.  The loss is linear in v
     and in the initial state, so e may be 1 there; its rounding is the outputs' 2^-8."""
@@ -701,7 +722,9 @@ def test_binding_refusals():
 
 # one or few heads leave CUs idle, so that sequences over a piece (256 tokens and more) are cut; the first of `lens` is the longest
 CUT = [([1300], 1, 64, 64), ([1601, 0, 70, 257, 256, 513], 1, 32, 128), ([2047, 511], 2, 128, 64), ([1100, 1024], 1, 256, 40),
-       ([1537, 1, 255], 3, 48, 200)]
+       ([1537, 1, 255], 3, 48, 200),
+       # heads and sequences that fill the GPU, one of them far longer than the others
+       ([2500, 70, 1], 90, 16, 16), ([1500] + [3] * 69, 4, 16, 24)]
 
 
 @pytest.mark.parametrize("lens,H,K,V", CUT)
@@ -711,7 +734,8 @@ def test_cut_packed(lens, H, K, V):
     cu = offsets(lens, first)
     total = cu[-1] + 70
     assert mscan.linear_attention_workspace_size(n, total, H, K, V, packed=True) > 0
-    assert mscan.linear_attention_workspace_size(n, total, H, K, V, packed=True, backward=True) > 0
+    # (the gradient's three products of 90 heads fill the GPU with whole sequences)
+    assert H == 90 or mscan.linear_attention_workspace_size(n, total, H, K, V, packed=True, backward=True) > 0
     q, k, v, do = (r(total, H, d, dtype=BF16) for d in (K, K, V, V))
     for t in (q, k, v, do):
         t[:first] = t[cu[-1]:] = float("nan")
