@@ -15,6 +15,32 @@
 //   dq_t = c S_t do_t     q, k, v -> do, v, k, the state transposed
 //   dk_t = R_t v_t        q, k, v -> v, do, q, last token first
 //   dv_t = R_t^T k_t      q, k, v -> k, q, do, last token first
+//
+// Mapping.  A workgroup is four waves that walk a piece of one sequence and head; each owns 32 columns of the state (16
+// where v has at most 64), all its rows, in MFMA accumulators.  q, k and v of a chunk pass through LDS, the next chunk's
+// loads in flight behind them.  A gradient's three products are workgroups of one launch.  The workgroups of eight (sequence,
+// head) at a time lie on one XCD each, so that the slabs and products that share q, k, v and do read them from one L2.
+//   S^T Q^T  S as bf16 hi + lo (2^-16 of it: one part alone would add an error like o's own rounding), straight from the
+//            accumulators: the order of a product's k index is free as long as both operands agree
+//   P        formed once a workgroup, a quarter by each wave beside S^T Q^T, whose operands of Q it shares; masked, decayed
+//            and passed on through LDS in bf16 hi + lo, as S
+//   K^T V    the weighted v in three bf16 parts by truncation (8 bits each: exact), so that a state that leaves keeps fp32's
+//            accuracy; in two (2^-16) where none can, in the gradient without an initial state.  K and V by
+//            transposing LDS reads
+//   S        decays by a factor a chunk whose rounding is carried in 64 bits, so that a head that forgets slowly does not
+//            add it up over a long prompt
+// 32 columns a wave and A = 128 take 76 KB of LDS and 240 registers: two workgroups on a CU, two waves on a SIMD.
+//
+// What bounds it: with heads of 128 instruction issue on matrix and vector units.  A wave's chunk of the gradient (128 x
+// 128) is 84 MFMAs of 32 cycles, 810 vector instructions and 104 LDS accesses; two waves on a SIMD take 5250 cycles for one
+// such chunk each, of which 2690 run MFMAs and 3240 issue vector instructions; a third of these split S and scale it.  8 x
+// 2048 tokens, 32 heads of 128 x 128: 349 - 430 us (cards differ), 271 GFLOP of matrix products, 630 - 775 TFLOP/s of
+// the 1170 - 1230 that a product of 8192^3 in bf16 reaches.  With heads of 64 HBM: 8 x 2048 tokens, 64 heads, 129 us, 4.2 TB/s.
+// 28 sequences of 160 to 4300 tokens, 32 heads of 128: 343 - 410 us, what the longest's chunks take one after another, while
+// all of them would fill the GPU for 220; cut, it would wait for a first pass of 100.  One of 20000, 16 heads of 128 x 256, 253 -
+// 265 us, of these 92 the pieces' own states, 16 the fold and 179 the main pass (traced); one of 509, 12 heads of 64: 22
+// us, eight chunks one after another.  Eight waves of 16 columns on heads of 128, the products interleaved by hand, and keys
+// read a product ahead measured the same or worse.
 #include "internal.h"
 #include "io.h"
 #include "mfma.h"
@@ -121,7 +147,8 @@ __device__ __forceinline__ int64_t part_of(int64_t b, int64_t s) { return b + mi
 constexpr int per_cu(int A, int CW) { return A == 256 ? 1 : A == 64 && CW == 16 ? 3 : 2; }
 
 // The sequence that is `rank`-th by length, the longest first, where up to 64 lengths tell, else sequence `rank` (whole waves).
-// Workgroups start in this order: 28 sequences of 120 to 3600 tokens, 32 workgroups each, as they come 412 us.
+// Workgroups start in this order: 28 sequences of 160 to 4300 tokens, 32 workgroups each, as they come 412 us,
+// longest first 400.
 __device__ __forceinline__ int64_t by_length(const Packed& p, int64_t rank) {
   if (p.nseq > 64) return rank;
   const int lane = threadIdx.x & 63, n = (int)p.nseq;

